@@ -317,6 +317,145 @@ nvfp4_status nvfp4_kv_fp8_encode(const void* x_bf16, int64_t n, const float* ama
 nvfp4_status nvfp4_kv_fp8_decode(const uint8_t* codes, int64_t n, const float* amax, void* out_bf16, void* stream);
 
 /* ---------------------------------------------------------------------------
+ * The token mixers between the projections: a paged key-value cache with the
+ * attention of one new token over it, and the gated linear attention of the
+ * recurrent (Gated-DeltaNet) layers.
+ *
+ * Values that live on the device (slots, positions, page numbers, lengths, state
+ * indices) cannot be checked on the host: the kernels check each one against the
+ * sizes given here and never read or write outside the buffers (what an invalid
+ * one does is said at each call).
+ * ------------------------------------------------------------------------- */
+
+/* Element types of the mixers' tensors. */
+typedef enum {
+  NVFP4_F32 = 0,
+  NVFP4_BF16 = 1,
+  NVFP4_E4M3 = 2 /* E4M3FN codes under a calibrated per-tensor scale (nvfp4_kv_fp8_encode) */
+} nvfp4_dtype;
+
+/* A paged key-value cache (a HOST struct of device pointers).  Row (page, token,
+ * head) of k and of v holds head_dim contiguous elements at element offset
+ * page * page_stride + token * token_stride + head * head_stride; the rows of one
+ * tensor must not overlap, and every row must be 16-byte aligned.  k and v have
+ * the same strides and may lie interleaved in one allocation.
+ * head_dim is 64, 128 or 256, page_size a positive multiple of 16.  dtype is
+ * NVFP4_BF16, or NVFP4_E4M3 with device pointers to the calibrated maxima of |k|
+ * and |v| (finite, >= 0; one float each): a code stands for E4M3(code) * fl(amax / 448). */
+typedef struct {
+  void* k;
+  void* v;
+  const float* k_amax;
+  const float* v_amax;
+  int64_t num_pages;
+  int64_t page_stride;
+  int64_t token_stride;
+  int64_t head_stride;
+  int32_t page_size;
+  int32_t kv_heads;
+  int32_t head_dim;
+  int32_t dtype;
+} nvfp4_kv_cache;
+
+/* Append T tokens' keys and values to the cache, with the rotation by position.
+ *
+ *   q, k, v   rows of q_heads (q) or cache->kv_heads (k, v) heads of head_dim
+ *             elements, heads adjacent, token strides ldq / ldk / ldv elements
+ *             (e.g. the column ranges of a fused projection's fp32 output).
+ *             src_dtype is NVFP4_F32 or NVFP4_BF16.  q may be NULL (q_out too).
+ *   rope      fp32 [max_pos][rot_dim]: the cosines of the rot_dim / 2 angles of a
+ *             position, then their sines.  rot_dim is a multiple of 16, at most
+ *             head_dim; 0 for no rotation (rope and positions are then not read).
+ *             The first rot_dim elements of each head of q and k are rotated in
+ *             pairs (i, i + rot_dim / 2), or (2i, 2i + 1) if interleaved != 0:
+ *               x1' = fl(fl(x1 c) - fl(x2 s)),  x2' = fl(fl(x2 c) + fl(x1 s)).
+ *   positions int64 [T]; slots int64 [T]: the token's cache row, page * page_size
+ *             + offset.  A token whose slot is negative or not below num_pages *
+ *             page_size, or whose position is outside [0, max_pos), is a padded
+ *             row: nothing of it is written.  Slots of one call must differ: of
+ *             tokens that share one, which is kept is unspecified.
+ *   q_out     bf16 [T], token stride ldqo: the rotated queries (RNE).
+ * k (rotated) and v are rounded to bf16 (RNE) and stored as that, or as the codes
+ * that nvfp4_kv_fp8_encode gives for it: results are bit-exact to that definition.
+ * Every token stride is a multiple of 16 bytes; T >= 0. */
+nvfp4_status nvfp4_kv_append(const void* q, const void* k, const void* v, int32_t src_dtype, int64_t T,
+                             int32_t q_heads, int64_t ldq, int64_t ldk, int64_t ldv, const float* rope,
+                             int32_t rot_dim, int64_t max_pos, int32_t interleaved, const int64_t* positions,
+                             const int64_t* slots, const nvfp4_kv_cache* cache, void* q_out, int64_t ldqo,
+                             void* stream);
+
+/* Attention of one new token for each of B sequences over the paged cache:
+ *
+ *   out[b][h] = sum_j p_j V[j],  p = softmax_j(scale * q[b][h] . K[j]),
+ *   lse[b][h] = log sum_j exp(scale * q[b][h] . K[j])
+ * over the cached tokens j in [max(0, len - window), len), len = seq_lens[b]
+ * (clamped to [0, max_len]; window == 0: all of them), which sit in the pages
+ * block_table[b][j / page_size].  Tokens on a page number outside [0, num_pages)
+ * are left out like masked ones; cache rows that are not attended to may hold
+ * anything (NaN included).  A row with no token gives out = 0, lse = -inf.
+ * Query head h reads key-value head h / (q_heads / kv_heads); q_heads is a
+ * multiple of kv_heads.
+ *
+ *   q          bf16 [B][q_heads][head_dim], row stride ldq (multiple of 8).
+ *   block_table int32 [B][ldt], ldt >= ceil(max_len / page_size).
+ *   max_len    upper bound of the lengths, known on the host (a looser bound
+ *              costs little); below 2^31.
+ *   out        bf16, row stride ldo (multiple of 8); lse fp32 [B][q_heads] or NULL.
+ *   workspace  device scratch of nvfp4_attn_decode_workspace_bytes (contents need
+ *              no setup; NULL allowed when that is 0): the partial results of long
+ *              sequences, which several workgroups share and a second kernel joins.
+ * Scores, the softmax and both sums are fp32; probabilities enter the product
+ * with V to 16 significant bits.  The result does not depend on timing. */
+size_t nvfp4_attn_decode_workspace_bytes(int64_t B, int32_t q_heads, int32_t kv_heads, int32_t head_dim,
+                                         int64_t max_len, int64_t window);
+
+nvfp4_status nvfp4_attn_decode(const void* q_bf16, int64_t B, int32_t q_heads, int64_t ldq,
+                               const nvfp4_kv_cache* cache, const int32_t* block_table, int64_t ldt,
+                               const int32_t* seq_lens, int64_t max_len, float scale, int64_t window,
+                               void* out_bf16, int64_t ldo, float* lse, void* workspace, size_t workspace_bytes,
+                               void* stream);
+
+/* Gated linear attention with the delta rule (the Gated-DeltaNet recurrence):
+ *
+ *   S_t = e^{g_t} S_{t-1} + beta_t k_t (v_t - (e^{g_t} S_{t-1})^T k_t)^T,
+ *   o_t = scale * S_t^T q_t                            (S: k_dim x v_dim)
+ * for each value head, with its own g (log decay, <= 0; -inf forgets all) and
+ * beta; beta == NULL: S_t = e^{g_t} S_{t-1} + k_t v_t^T, linear attention with a
+ * decay for each head.  Value head h uses query/key head h / (v_heads / k_heads).
+ *
+ *   q, k   bf16 [tokens][k_heads][k_dim], token strides ldq, ldk; v bf16
+ *          [tokens][v_heads][v_dim], ldv; out bf16 like v, ldo (strides are
+ *          multiples of 8).  k_dim is 64 or 128, v_dim a multiple of 32 up to 1024.
+ *   g, beta fp32 [tokens][v_heads], token strides ldg, ldb; these two need only
+ *          4-byte alignment (column ranges of a fused projection).
+ *   state  fp32 [num_states][v_heads][k_dim][v_dim], updated in place.
+ *   state_index int32 [B]: sequence b's state; NULL: b itself (num_states >= B).
+ *          A sequence whose index is outside [0, num_states) is a padded row:
+ *          none of its outputs is written.  Indices of one call must differ: the
+ *          contents of a state that two sequences share are unspecified.
+ * nvfp4_gdn_step: one token for each of B sequences (tokens = B). */
+nvfp4_status nvfp4_gdn_step(const void* q, int64_t ldq, const void* k, int64_t ldk, const void* v, int64_t ldv,
+                            const float* g, int64_t ldg, const float* beta, int64_t ldb, int64_t B, int32_t k_heads,
+                            int32_t v_heads, int32_t k_dim, int32_t v_dim, float* state, int64_t num_states,
+                            const int32_t* state_index, float scale, void* out, int64_t ldo, void* stream);
+
+/* nvfp4_gdn_prefill: the tokens [cu_seqlens[b], cu_seqlens[b + 1]) of each of B
+ * sequences, T rows in all (device int32 [B + 1], non-decreasing, clamped to
+ * [0, T]; rows of no sequence are left as they were; an empty sequence only
+ * carries its state on).  Sequence b starts from its state if has_state (device
+ * int32 [B]) is given and has_state[b] != 0, else from zero; its last state is
+ * stored.  Workspace: nvfp4_gdn_prefill_workspace_bytes. */
+size_t nvfp4_gdn_prefill_workspace_bytes(int64_t T, int64_t B, int32_t k_heads, int32_t v_heads, int32_t k_dim,
+                                         int32_t v_dim);
+
+nvfp4_status nvfp4_gdn_prefill(const void* q, int64_t ldq, const void* k, int64_t ldk, const void* v, int64_t ldv,
+                               const float* g, int64_t ldg, const float* beta, int64_t ldb, int64_t T, int64_t B,
+                               const int32_t* cu_seqlens, int32_t k_heads, int32_t v_heads, int32_t k_dim,
+                               int32_t v_dim, float* state, int64_t num_states, const int32_t* state_index,
+                               const int32_t* has_state, float scale, void* out, int64_t ldo, void* workspace,
+                               size_t workspace_bytes, void* stream);
+
+/* ---------------------------------------------------------------------------
  * Diagnostic: the device conversion steps the encoders and GEMMs are built
  * on, applied to the binary32 values with bit patterns first_bits + i,
  * i < n, so that tests can compare them with the format definitions over

@@ -39,8 +39,20 @@ class Segment(ctypes.Structure):
     _fields_ = [("n_begin", ctypes.c_int32), ("n_end", ctypes.c_int32)]
 
 
+DTYPE = {torch.float32: 0, torch.bfloat16: 1, torch.uint8: 2}     # nvfp4_dtype (uint8: E4M3 codes)
+
+
+class KVCacheDesc(ctypes.Structure):
+    """nvfp4_kv_cache: the host struct that describes a paged key-value cache."""
+    _fields_ = [("k", ctypes.c_void_p), ("v", ctypes.c_void_p), ("k_amax", ctypes.c_void_p),
+                ("v_amax", ctypes.c_void_p), ("num_pages", ctypes.c_int64), ("page_stride", ctypes.c_int64),
+                ("token_stride", ctypes.c_int64), ("head_stride", ctypes.c_int64), ("page_size", ctypes.c_int32),
+                ("kv_heads", ctypes.c_int32), ("head_dim", ctypes.c_int32), ("dtype", ctypes.c_int32)]
+
+
 _LIB = None
 _i64, _vp, _sz = ctypes.c_int64, ctypes.c_void_p, ctypes.c_size_t
+_i32, _f32 = ctypes.c_int32, ctypes.c_float
 
 
 def _lib():
@@ -99,6 +111,23 @@ def _lib():
         lib.nvfp4_convert_sweep.argtypes = [ctypes.c_int32, ctypes.c_uint32, _i64, _vp, _vp]
         lib.nvfp4_read_probe.restype = ctypes.c_int
         lib.nvfp4_read_probe.argtypes = [_vp, _i64, ctypes.c_int32, _vp, _vp]
+        cache_p = ctypes.POINTER(KVCacheDesc)
+        lib.nvfp4_kv_append.restype = ctypes.c_int
+        lib.nvfp4_kv_append.argtypes = [_vp, _vp, _vp, _i32, _i64, _i32, _i64, _i64, _i64, _vp, _i32, _i64, _i32, _vp,
+                                        _vp, cache_p, _vp, _i64, _vp]
+        lib.nvfp4_attn_decode_workspace_bytes.restype = _sz
+        lib.nvfp4_attn_decode_workspace_bytes.argtypes = [_i64, _i32, _i32, _i32, _i64, _i64]
+        lib.nvfp4_attn_decode.restype = ctypes.c_int
+        lib.nvfp4_attn_decode.argtypes = [_vp, _i64, _i32, _i64, cache_p, _vp, _i64, _vp, _i64, _f32, _i64, _vp, _i64,
+                                          _vp, _vp, _sz, _vp]
+        gdn = [_vp, _i64, _vp, _i64, _vp, _i64, _vp, _i64, _vp, _i64]
+        lib.nvfp4_gdn_step.restype = ctypes.c_int
+        lib.nvfp4_gdn_step.argtypes = gdn + [_i64, _i32, _i32, _i32, _i32, _vp, _i64, _vp, _f32, _vp, _i64, _vp]
+        lib.nvfp4_gdn_prefill_workspace_bytes.restype = _sz
+        lib.nvfp4_gdn_prefill_workspace_bytes.argtypes = [_i64, _i64, _i32, _i32, _i32, _i32]
+        lib.nvfp4_gdn_prefill.restype = ctypes.c_int
+        lib.nvfp4_gdn_prefill.argtypes = gdn + [_i64, _i64, _vp, _i32, _i32, _i32, _i32, _vp, _i64, _vp, _vp, _f32,
+                                                _vp, _i64, _vp, _sz, _vp]
         _LIB = lib
     return _LIB
 
@@ -251,6 +280,46 @@ def nvfp4_convert_sweep(op, first_bits, n, out, stream=None):
 def nvfp4_read_probe(buf, nbytes, workgroups, sink, stream=None):
     _check(_lib().nvfp4_read_probe(_ptr(buf), int(nbytes), int(workgroups), _ptr(sink), _stream(stream)),
            "nvfp4_read_probe")
+
+
+def nvfp4_kv_append(q, k, v, src_dtype, T, q_heads, ldq, ldk, ldv, rope, rot_dim, max_pos, interleaved, positions, slots,
+                    cache, q_out, ldqo, stream=None):
+    """``cache`` is a KVCacheDesc."""
+    _check(_lib().nvfp4_kv_append(_ptr(q), _ptr(k), _ptr(v), src_dtype, T, q_heads, ldq, ldk, ldv, _ptr(rope), rot_dim,
+                                  max_pos, interleaved, _ptr(positions), _ptr(slots), ctypes.byref(cache), _ptr(q_out),
+                                  ldqo, _stream(stream)), "nvfp4_kv_append")
+
+
+def nvfp4_attn_decode_workspace_bytes(B, q_heads, kv_heads, head_dim, max_len, window):
+    return _lib().nvfp4_attn_decode_workspace_bytes(B, q_heads, kv_heads, head_dim, max_len, window)
+
+
+def nvfp4_attn_decode(q, B, q_heads, ldq, cache, block_table, ldt, seq_lens, max_len, scale, window, out, ldo, lse,
+                      workspace, workspace_bytes, stream=None):
+    """``cache`` is a KVCacheDesc."""
+    _check(_lib().nvfp4_attn_decode(_ptr(q), B, q_heads, ldq, ctypes.byref(cache), _ptr(block_table), ldt,
+                                    _ptr(seq_lens), max_len, scale, window, _ptr(out), ldo, _ptr(lse), _ptr(workspace),
+                                    workspace_bytes, _stream(stream)), "nvfp4_attn_decode")
+
+
+def nvfp4_gdn_step(q, ldq, k, ldk, v, ldv, g, ldg, beta, ldb, B, k_heads, v_heads, k_dim, v_dim, state, num_states,
+                   state_index, scale, out, ldo, stream=None):
+    _check(_lib().nvfp4_gdn_step(_ptr(q), ldq, _ptr(k), ldk, _ptr(v), ldv, _ptr(g), ldg, _ptr(beta), ldb, B, k_heads,
+                                 v_heads, k_dim, v_dim, _ptr(state), num_states, _ptr(state_index), scale, _ptr(out),
+                                 ldo, _stream(stream)), "nvfp4_gdn_step")
+
+
+def nvfp4_gdn_prefill_workspace_bytes(T, B, k_heads, v_heads, k_dim, v_dim):
+    return _lib().nvfp4_gdn_prefill_workspace_bytes(T, B, k_heads, v_heads, k_dim, v_dim)
+
+
+def nvfp4_gdn_prefill(q, ldq, k, ldk, v, ldv, g, ldg, beta, ldb, T, B, cu_seqlens, k_heads, v_heads, k_dim, v_dim,
+                      state, num_states, state_index, has_state, scale, out, ldo, workspace, workspace_bytes,
+                      stream=None):
+    _check(_lib().nvfp4_gdn_prefill(_ptr(q), ldq, _ptr(k), ldk, _ptr(v), ldv, _ptr(g), ldg, _ptr(beta), ldb, T, B,
+                                    _ptr(cu_seqlens), k_heads, v_heads, k_dim, v_dim, _ptr(state), num_states,
+                                    _ptr(state_index), _ptr(has_state), scale, _ptr(out), ldo, _ptr(workspace),
+                                    workspace_bytes, _stream(stream)), "nvfp4_gdn_prefill")
 
 
 # ---- convenience layer: allocate with torch, call the C ABI --------------------------
@@ -474,3 +543,195 @@ def quantize_stats(x, amax, *, stream=None):
     counts = torch.empty(2, dtype=torch.int32, device=x.device)
     nvfp4_quantize_stats(x, M, K, max(x.stride(0), K), amax, counts, stream)
     return counts
+
+
+# ---- token mixers: paged cache, decode attention, gated linear attention ----------------
+def _on_device(fn):
+    """For the mixers: runs a function with its first tensor's GPU current, on that
+    GPU's current stream or on ``stream`` (keyword-only, a torch.cuda.Stream of it), and
+    allocates there (see _on_stream)."""
+    @functools.wraps(fn)
+    def wrapper(first, *args, stream=None, **kw):
+        if stream is None and first.get_device() == torch.cuda.current_device():
+            return fn(first, *args, stream=None, **kw)
+        if stream is not None and not isinstance(stream, torch.cuda.Stream):
+            raise TypeError(f"{fn.__name__}: stream must be a torch.cuda.Stream "
+                            "(the nvfp4_* wrappers take raw handles)")
+        assert first.is_cuda, f"{fn.__name__}: a cuda tensor is needed"
+        assert stream is None or stream.device == first.device, f"{fn.__name__}: the stream is another GPU's"
+        with torch.cuda.device(first.device):
+            if stream is None:
+                return fn(first, *args, stream=None, **kw)
+            with torch.cuda.stream(stream):
+                return fn(first, *args, stream=stream.cuda_stream, **kw)
+    return wrapper
+
+
+def _rows3(x, dev, dtype, T, H, D, what):
+    """Checks a [T, H, D] tensor whose heads lie next to each other; its token stride."""
+    assert x.dtype == dtype and x.shape == (T, H, D) and x.get_device() == dev, what
+    if T == 0:
+        return H * D
+    s = x.stride()
+    assert s[2] == 1 and (s[1] == D or H == 1), f"{what}: a token's heads must be contiguous"
+    return s[0] if T > 1 else max(s[0], H * D)
+
+
+def _rows2(x, dev, T, H, what):
+    """Checks an fp32 [T, H] tensor; its token stride."""
+    assert x.dtype == torch.float32 and x.shape == (T, H) and x.get_device() == dev, what
+    s = x.stride()
+    assert s[1] == 1 or H == 1 or T == 0, f"{what}: a token's values must be contiguous"
+    return s[0] if T > 1 else max(s[0], H)
+
+
+def _table(x, dev, dtype, n, what):
+    if x is not None:
+        assert x.dtype == dtype and x.shape == (n,) and x.get_device() == dev and x.is_contiguous(), what
+    return x
+
+
+class PagedKVCache:
+    """A paged key-value cache over two tensors [pages, page_size, kv_heads, head_dim] of the
+    same strides (any layout whose rows are contiguous, e.g. views of [pages, 2, page_size,
+    ...] or permuted [pages, kv_heads, page_size, ...]): bf16, or uint8 E4M3 codes with the
+    calibrated maxima k_amax and v_amax (fp32 [1] on the GPU)."""
+
+    def __init__(self, k, v, k_amax=None, v_amax=None):
+        assert k.dim() == 4 and k.dtype in (torch.bfloat16, torch.uint8) and k.is_cuda, "k: a 4-d bf16 or uint8 cuda tensor"
+        assert v.dtype == k.dtype and v.shape == k.shape and v.stride() == k.stride() and v.device == k.device, \
+            "v: the type, shape, strides and device of k"
+        assert k.stride(3) == 1 or k.numel() == 0, "rows must be contiguous"
+        for a in (k_amax, v_amax):
+            assert (a is None) == (k.dtype == torch.bfloat16), "k_amax and v_amax belong to E4M3 codes, and only to them"
+            assert a is None or (a.dtype == torch.float32 and a.numel() == 1 and a.device == k.device), "amax: fp32 [1]"
+        self.k, self.v, self.k_amax, self.v_amax = k, v, k_amax, v_amax
+        self.device_index = k.get_device()
+        self.num_pages, self.page_size, self.kv_heads, self.head_dim = k.shape
+        s = k.stride()
+        self.desc = KVCacheDesc(k.data_ptr(), v.data_ptr(), _ptr(k_amax), _ptr(v_amax), self.num_pages, s[0], s[1],
+                                s[2], self.page_size, self.kv_heads, self.head_dim, DTYPE[k.dtype])
+
+    @classmethod
+    def empty(cls, num_pages, page_size, kv_heads, head_dim, device, k_amax=None, v_amax=None):
+        """A new cache (contents unset): E4M3 if the calibrated maxima are given, else bf16."""
+        dtype = torch.bfloat16 if k_amax is None else torch.uint8
+        k, v = (torch.empty((num_pages, page_size, kv_heads, head_dim), dtype=dtype, device=device) for _ in range(2))
+        return cls(k, v, k_amax, v_amax)
+
+
+@_on_device
+def kv_append(k, v, cache, slots, q=None, positions=None, rope=None, interleaved=False, q_out=None, *, stream=None):
+    """Rotates k (and q) by position, and appends k and v to a PagedKVCache at rows ``slots``.
+
+    k, v: fp32 or bf16 [T, kv_heads, head_dim]; q: the same type, [T, q_heads, head_dim].
+    slots, positions: int64 [T] (slot < 0: a padded row); rope: fp32 [max_pos, rot_dim], the
+    cosines of a position's angles, then their sines; None: no rotation.  Returns q, rotated, as
+    bf16 (None without q)."""
+    dev, D = cache.device_index, cache.head_dim
+    T = k.shape[0]
+    assert k.dtype in (torch.float32, torch.bfloat16), "k: fp32 or bf16"
+    ldk = _rows3(k, dev, k.dtype, T, cache.kv_heads, D, "k")
+    ldv = _rows3(v, dev, k.dtype, T, cache.kv_heads, D, "v")
+    _table(slots, dev, torch.int64, T, "slots: int64 [T]")
+    _table(positions, dev, torch.int64, T, "positions: int64 [T]")
+    rot, far = 0, 0
+    if rope is not None:
+        assert rope.dtype == torch.float32 and rope.dim() == 2 and rope.is_contiguous() and rope.get_device() == dev, \
+            "rope: contiguous fp32 [max_pos, rot_dim]"
+        assert positions is not None, "rope needs positions"
+        far, rot = rope.shape
+    heads, ldq, ldqo = 0, 0, 0
+    if q is not None:
+        heads = q.shape[1]
+        ldq = _rows3(q, dev, k.dtype, T, heads, D, "q")
+        if q_out is None:
+            q_out = torch.empty((T, heads, D), dtype=torch.bfloat16, device=k.device)
+        ldqo = _rows3(q_out, dev, torch.bfloat16, T, heads, D, "q_out")
+    else:
+        assert q_out is None, "q_out needs q"
+    nvfp4_kv_append(q, k, v, DTYPE[k.dtype], T, heads, ldq, ldk, ldv, rope, rot, far, bool(interleaved), positions, slots,
+                    cache.desc, q_out, ldqo, stream)
+    return q_out
+
+
+@_on_device
+def attn_decode(q, cache, block_table, seq_lens, max_len=None, scale=None, window=0, workspace=None, out=None,
+                lse=None, *, stream=None):
+    """Attention of one new token a sequence over a PagedKVCache -> (out bf16 [B, q_heads, head_dim],
+    lse fp32 [B, q_heads]).
+
+    q: bf16 [B, q_heads, head_dim]; block_table: int32 [B, pages]; seq_lens: int32 [B], the new
+    token's own included.  max_len: a bound of the lengths (default: what the table holds);
+    scale: default head_dim ** -0.5; window: the last tokens attended to (0: all)."""
+    dev, D = cache.device_index, cache.head_dim
+    B, H = q.shape[0], q.shape[1]
+    ldq = _rows3(q, dev, torch.bfloat16, B, H, D, "q")
+    assert block_table.dtype == torch.int32 and block_table.dim() == 2 and block_table.shape[0] == B and \
+        block_table.get_device() == dev and (block_table.stride(1) == 1 or block_table.shape[1] <= 1), \
+        "block_table: int32 [B, pages]"
+    pages = block_table.shape[1]
+    if max_len is None:
+        max_len = pages * cache.page_size
+    assert max_len <= pages * cache.page_size, "max_len: more than the block table holds"
+    _table(seq_lens, dev, torch.int32, B, "seq_lens: int32 [B]")
+    if out is None:
+        out = torch.empty((B, H, D), dtype=torch.bfloat16, device=q.device)
+    if lse is None:
+        lse = torch.empty((B, H), dtype=torch.float32, device=q.device)
+    assert lse.dtype == torch.float32 and lse.shape == (B, H) and lse.is_contiguous() and lse.get_device() == dev, "lse"
+    ldo = _rows3(out, dev, torch.bfloat16, B, H, D, "out")
+    ws = workspace if workspace is not None else Workspace(q.device)
+    buf, nbytes = ws.get(nvfp4_attn_decode_workspace_bytes(B, H, cache.kv_heads, D, max_len, window))
+    nvfp4_attn_decode(q, B, H, ldq, cache.desc, block_table, max(block_table.stride(0), pages), seq_lens, max_len,
+                      D ** -0.5 if scale is None else scale, window, out, ldo, lse, buf, nbytes, stream)
+    return out, lse
+
+
+def _gdn_args(q, k, v, g, beta, state, state_index, B, scale, out):
+    """Checks the tensors of a recurrent layer; the arguments the two calls share, and `out`."""
+    dev, T = q.get_device(), q.shape[0]
+    Hk, Dk, Hv, Dv = q.shape[1], q.shape[2], v.shape[1], v.shape[2]
+    ldq = _rows3(q, dev, torch.bfloat16, T, Hk, Dk, "q")
+    ldk = _rows3(k, dev, torch.bfloat16, T, Hk, Dk, "k")
+    ldv = _rows3(v, dev, torch.bfloat16, T, Hv, Dv, "v")
+    ldg = _rows2(g, dev, T, Hv, "g")
+    ldb = _rows2(beta, dev, T, Hv, "beta") if beta is not None else 0
+    assert state.dtype == torch.float32 and state.dim() == 4 and state.shape[1:] == (Hv, Dk, Dv) and \
+        state.is_contiguous() and state.get_device() == dev, "state: contiguous fp32 [states, v_heads, k_dim, v_dim]"
+    _table(state_index, dev, torch.int32, B, "state_index: int32 [B]")
+    if out is None:
+        out = torch.empty((T, Hv, Dv), dtype=torch.bfloat16, device=q.device)
+    ldo = _rows3(out, dev, torch.bfloat16, T, Hv, Dv, "out")
+    return (q, ldq, k, ldk, v, ldv, g, ldg, beta, ldb), (Hk, Hv, Dk, Dv), (Dk ** -0.5 if scale is None else scale), \
+        out, ldo
+
+
+@_on_device
+def gdn_step(q, k, v, g, beta, state, state_index=None, scale=None, out=None, *, stream=None):
+    """One token for each of B sequences through a gated-delta-rule layer -> out bf16 [B, v_heads, v_dim].
+
+    q, k: bf16 [B, k_heads, k_dim]; v: bf16 [B, v_heads, v_dim]; g (log decay) and beta: fp32
+    [B, v_heads], beta None for linear attention with a decay; state: fp32 [states, v_heads,
+    k_dim, v_dim], updated in place; state_index: int32 [B] (negative: a padded row)."""
+    B = q.shape[0]
+    first, dims, scale, out, ldo = _gdn_args(q, k, v, g, beta, state, state_index, B, scale, out)
+    nvfp4_gdn_step(*first, B, *dims, state, state.shape[0], state_index, scale, out, ldo, stream)
+    return out
+
+
+@_on_device
+def gdn_prefill(q, k, v, g, beta, state, cu_seqlens, has_state=None, state_index=None, scale=None, workspace=None,
+                out=None, *, stream=None):
+    """The prompts of B sequences, rows cu_seqlens[b]..cu_seqlens[b + 1], through a gated-delta-rule
+    layer -> out bf16 [T, v_heads, v_dim]; tensors as in gdn_step.  has_state: int32 [B], whether
+    a sequence starts from its state (None: all start from zero)."""
+    B, T = cu_seqlens.shape[0] - 1, q.shape[0]
+    first, dims, scale, out, ldo = _gdn_args(q, k, v, g, beta, state, state_index, B, scale, out)
+    _table(cu_seqlens, q.get_device(), torch.int32, B + 1, "cu_seqlens: int32 [B + 1]")
+    _table(has_state, q.get_device(), torch.int32, B, "has_state: int32 [B]")
+    ws = workspace if workspace is not None else Workspace(q.device)
+    buf, nbytes = ws.get(nvfp4_gdn_prefill_workspace_bytes(T, B, *dims))
+    nvfp4_gdn_prefill(*first, T, B, cu_seqlens, *dims, state, state.shape[0], state_index, has_state, scale, out, ldo,
+                      buf, nbytes, stream)
+    return out

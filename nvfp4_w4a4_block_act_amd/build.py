@@ -16,8 +16,9 @@ CSRC = os.path.join(PKG, "csrc")
 LIB = os.path.join(PKG, "libnvfp4_w4a4.so")
 ARCH = "gfx950"
 
-HIP_SOURCES = ["quantize.hip", "gemm_skinny.hip", "gemm_mfma.hip", "kv_fp8.hip", "stream_probe.hip"]
-HOST_SOURCES = ["api.cpp", "dispatch.cpp"]
+HIP_SOURCES = ["quantize.hip", "gemm_skinny.hip", "gemm_mfma.hip", "kv_fp8.hip", "kv_append.hip", "attn_decode.hip",
+               "gdn.hip", "stream_probe.hip"]
+HOST_SOURCES = ["api.cpp", "api_mixers.cpp", "dispatch.cpp"]
 
 COMMON = ["-O3", "-std=c++17", "-fPIC", "-Wall", "-Wno-unused-function"]
 DEVICE = [f"--offload-arch={ARCH}", "-ffp-contract=off",
