@@ -339,7 +339,8 @@ typedef enum {
  * page * page_stride + token * token_stride + head * head_stride; the rows of one
  * tensor must not overlap, and every row must be 16-byte aligned.  k and v have
  * the same strides and may lie interleaved in one allocation.
- * head_dim is 64, 128 or 256, page_size a positive multiple of 16.  dtype is
+ * head_dim is 64, 128 or 256, page_size a positive multiple of 16, token_stride
+ * below 2^26.  dtype is
  * NVFP4_BF16, or NVFP4_E4M3 with device pointers to the calibrated maxima of |k|
  * and |v| (finite, >= 0; one float each): a code stands for E4M3(code) * fl(amax / 448). */
 typedef struct {

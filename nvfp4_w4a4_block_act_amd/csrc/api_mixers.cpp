@@ -55,6 +55,7 @@ nvfp4_status check_cache(const nvfp4_kv_cache* c) {
     return NVFP4_ESHAPE;
   for (int64_t s : {c->page_stride, c->token_stride, c->head_stride})
     if (s < 0 || s >= kMaxStride) return NVFP4_ESHAPE;
+  if (c->token_stride >= (1 << 26)) return NVFP4_ESHAPE;  // 16 rows within 32-bit byte offsets
   // (num_pages - 1) * page_stride must stay far inside int64
   if (c->num_pages > 1 && c->page_stride > ((int64_t)1 << 56) / c->num_pages) return NVFP4_ESHAPE;
   if (!rows_disjoint(*c)) return NVFP4_ESHAPE;

@@ -1,97 +1,384 @@
 // Attention of one new token over the paged key-value cache.
 //
-// One pass over the cached tokens with the running maximum m and sum l of the
-// softmax: a score s moves m to m' = max(m, s), and the sums taken so far are
-// scaled by e^(m - m').  A workgroup takes one query head of one sequence; its
-// four waves take every fourth token, a lane head_dim / 64 elements of the rows,
-// and join through LDS at the end.
+// One pass over the cached tokens with a running reference m and sum l of the
+// softmax (scores in units of log 2): tokens enter as 2^(s - m), and when a score
+// exceeds m by more than kSlack, m moves up and the sums so far are scaled.  m
+// need not be the maximum itself: sums and weights are binary32, whose range
+// holds 2^kSlack with ease, and most tiles then need no exchange between lanes.
+//
+// Layout.  A wave takes tiles of 16 tokens (a page holds whole tiles) for up to 16
+// query heads that share a key-value head, and both products run on the matrix
+// cores straight from registers, no LDS:
+//  * scores: S^T = K Q^T (16 x 16 x 32, bf16): lane (r, g) = (lane % 16, lane / 16)
+//    loads 16-byte pieces of token r's key row, four lanes 64 contiguous bytes;
+//    which elements of the row a step multiplies is free as long as q is taken in
+//    the same order;
+//  * S^T leaves token 4 g + j of head r in register j of lane (r, g), which is
+//    where P^T must be for O^T = V^T P^T (16 x 16 x 16): the weights need no move;
+//  * V^T: lane (c, g) loads its head_dim / 16 elements of the value rows of
+//    tokens 4 g .. 4 g + 3 -- 16 lanes read whole rows -- and the transposition is
+//    four rows' worth of byte permutes within the lane; output tile i then holds
+//    element i of every lane's run.
+// A weight enters as the sum of two bf16 values (16 significant bits, two matrix
+// instructions), so that its rounding (2^-17) is far below that of the output.
+// E4M3 codes widen to bf16 exactly; k's scale goes into the scores' factor, v's
+// into the output.  Loads of the next tile are in flight while one is computed.
+//
+// The tokens of a sequence are split over workgroups of four waves (wave w takes
+// tiles w, w + 4, ...), joined through LDS, and over splits, whose partial results
+// a second kernel joins in a fixed order.
+#include <algorithm>
+
 #include "common.hpp"
 #include "mixers.hpp"
 
 namespace nvfp4 {
 
-constexpr float kNone = -3.402823466e38f;  // running maximum before any token: finite, so that differences are numbers
+typedef __bf16 bf16x2_t __attribute__((ext_vector_type(2)));
+typedef __bf16 bf16x8_t __attribute__((ext_vector_type(8)));
+typedef short short4_t __attribute__((ext_vector_type(4)));
+typedef float f32x2_t __attribute__((ext_vector_type(2)));
+
+constexpr float kNone = -3.402823466e38f;  // reference before any token: finite, so that differences are numbers
+constexpr float kSlack = 8.0f;
+constexpr float kLog2e = 1.44269504088896340736f, kLn2 = 0.69314718055994530942f;
+constexpr int kWaves = 4;                  // waves of a workgroup
+constexpr int kSplitTokens = 128;          // fewest tokens of a split: two tiles for each wave
+
+// Splits of a sequence, from sizes the host knows: enough workgroups for every CU
+// to hold several, none with fewer than kSplitTokens tokens.
+struct Splits {
+  int count, tokens;  // tokens of one split: a multiple of 16
+};
+static Splits attn_splits(int64_t B, int q_heads, int kv_heads, int64_t max_len, int64_t window) {
+  const int64_t span = window > 0 && window < max_len ? window + 15 : max_len;
+  const int64_t rows = B * kv_heads * ((q_heads / kv_heads + 15) / 16);
+  const int64_t want = std::max<int64_t>(1, (int64_t)kCUs * 6 / rows);
+  const int64_t most = std::max<int64_t>(1, (span + kSplitTokens - 1) / kSplitTokens);
+  const int64_t n = std::min(want, most);
+  const int64_t tokens = std::max<int64_t>(16, (span + n - 1) / n + 15) / 16 * 16;
+  return {(int)std::max<int64_t>(1, (span + tokens - 1) / tokens), (int)tokens};
+}
 
 template <int DIM, bool FP8>
-__global__ __launch_bounds__(256) void attn_decode_kernel(AttnArgs a) {
-  constexpr int E = DIM / 64;
-  const int h = blockIdx.x, b = blockIdx.y;
-  const int lane = threadIdx.x % 64, wave = threadIdx.x / 64;
-  const nvfp4_kv_cache& c = a.cache;
-  const int kvh = h / (a.q_heads / c.kv_heads);
-  const int len = min(max(a.lens[b], 0), a.max_len);
-  const int begin = a.window ? max(0, len - a.window) : 0;
-  const float kg = FP8 ? *c.k_amax / 448.0f : 1.0f, vg = FP8 ? *c.v_amax / 448.0f : 1.0f;
+struct Tile {
+  static constexpr int kDwords = DIM * (FP8 ? 1 : 2) / 16;  // of a lane, for keys and for values
+  uint32_t k[kDwords];
+  uint32_t v[4][kDwords / 4];
+};
 
-  float q[E], o[E] = {};
+// 16 tokens' keys and values: `base` is the element offset of the tile's first row.
+template <int DIM, bool FP8>
+__device__ __forceinline__ void load_tile(Tile<DIM, FP8>& t, const uint8_t* k, const uint8_t* v, uint32_t k_off,
+                                          uint32_t v_off, uint32_t v_step) {
+  constexpr int ES = FP8 ? 1 : 2;
 #pragma unroll
-  for (int e = 0; e < E; ++e)
-    q[e] = __uint_as_float((uint32_t)a.q[(int64_t)b * a.ldq + h * DIM + lane * E + e] << 16);
-  float m = kNone, l = 0;
-  for (int t = begin + wave; t < len; t += 4) {
-    const int page = a.table[(int64_t)b * a.ldt + t / c.page_size];
-    if (page < 0 || page >= c.num_pages) continue;
-    const int64_t at = page * c.page_stride + (int64_t)(t % c.page_size) * c.token_stride + (int64_t)kvh * c.head_stride +
-                       lane * E;
-    float k[E], v[E], s = 0;
-#pragma unroll
-    for (int e = 0; e < E; ++e) {
-      if (FP8) {
-        k[e] = __builtin_amdgcn_cvt_f32_fp8((int)static_cast<const uint8_t*>(c.k)[at + e], 0);
-        v[e] = __builtin_amdgcn_cvt_f32_fp8((int)static_cast<const uint8_t*>(c.v)[at + e], 0);
-      } else {
-        k[e] = __uint_as_float((uint32_t)static_cast<const uint16_t*>(c.k)[at + e] << 16);
-        v[e] = __uint_as_float((uint32_t)static_cast<const uint16_t*>(c.v)[at + e] << 16);
-      }
-      s += q[e] * k[e];
-    }
-#pragma unroll
-    for (int d = 1; d < 64; d *= 2) s += __shfl_xor(s, d);
-    s *= a.scale * kg;
-    const float top = fmaxf(m, s), keep = expf(m - top), p = expf(s - top);
-    m = top;
-    l = l * keep + p;
-#pragma unroll
-    for (int e = 0; e < E; ++e) o[e] = o[e] * keep + p * v[e];
+  for (int i = 0; i < DIM * ES / 64; ++i) {
+    const uint4 w = *reinterpret_cast<const uint4*>(k + k_off + i * 64);
+    t.k[4 * i] = w.x, t.k[4 * i + 1] = w.y, t.k[4 * i + 2] = w.z, t.k[4 * i + 3] = w.w;
   }
-  __shared__ float ms[4], ls[4], os[4][DIM];
 #pragma unroll
-  for (int e = 0; e < E; ++e) os[wave][lane * E + e] = o[e];
-  if (lane == 0) ms[wave] = m, ls[wave] = l;
-  __syncthreads();
-  if (threadIdx.x < DIM) {
-    float top = kNone, sum = 0, out = 0;
-    for (int w = 0; w < 4; ++w) top = fmaxf(top, ms[w]);
-    for (int w = 0; w < 4; ++w) {
-      const float f = ls[w] > 0 ? expf(ms[w] - top) : 0.0f;
-      sum += ls[w] * f;
-      out += os[w][threadIdx.x] * f;
+  for (int r = 0; r < 4; ++r) {
+    const uint8_t* p = v + v_off + r * v_step;
+    if constexpr (DIM * ES == 64) {
+      t.v[r][0] = *reinterpret_cast<const uint32_t*>(p);
+    } else if constexpr (DIM * ES == 128) {
+      const uint2 w = *reinterpret_cast<const uint2*>(p);
+      t.v[r][0] = w.x, t.v[r][1] = w.y;
+    } else {
+#pragma unroll
+      for (int h = 0; h < DIM * ES / 256; ++h) {
+        const uint4 w = *reinterpret_cast<const uint4*>(p + h * 256);
+        t.v[r][4 * h] = w.x, t.v[r][4 * h + 1] = w.y, t.v[r][4 * h + 2] = w.z, t.v[r][4 * h + 3] = w.w;
+      }
     }
-    const float r = sum > 0 ? out / sum * vg : 0.0f;
-    a.out[(int64_t)b * a.ldo + h * DIM + threadIdx.x] = __builtin_bit_cast(uint16_t, (__bf16)r);
-    if (a.lse && threadIdx.x == 0) a.lse[(int64_t)b * a.q_heads + h] = sum > 0 ? top + logf(sum) : -INFINITY;
   }
 }
 
-size_t attn_decode_workspace(int64_t, int, int, int, int64_t, int64_t) { return 0; }
+__device__ __forceinline__ uint32_t fp8_pair(uint32_t w, bool high) {
+  return __builtin_bit_cast(uint32_t, high ? __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(w, 1.0f, true)
+                                           : __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(w, 1.0f, false));
+}
 
-template <int DIM>
-static void launch_dim(const AttnArgs& a, hipStream_t stream) {
-  const dim3 grid(a.q_heads, (unsigned)a.B), block(256);
-  if (a.cache.dtype == NVFP4_E4M3)
-    attn_decode_kernel<DIM, true><<<grid, block, 0, stream>>>(a);
-  else
-    attn_decode_kernel<DIM, false><<<grid, block, 0, stream>>>(a);
+// The low (high) halves of two dwords as one, the first in the low half.
+__device__ __forceinline__ uint32_t low_halves(uint32_t a, uint32_t b) { return __builtin_amdgcn_perm(b, a, 0x05040100u); }
+__device__ __forceinline__ uint32_t high_halves(uint32_t a, uint32_t b) { return __builtin_amdgcn_perm(b, a, 0x07060302u); }
+
+__device__ __forceinline__ bf16x8_t octet(uint32_t a, uint32_t b, uint32_t c, uint32_t d) {
+  return __builtin_bit_cast(bf16x8_t, make_uint4(a, b, c, d));
+}
+
+struct Running {
+  float m, l;  // of head lane % 16; l: this lane's tokens only
+};
+
+// One tile into the running softmax and the outputs.  first, last: tokens of the
+// tile that count.
+template <int DIM, bool FP8>
+__device__ __forceinline__ void take_tile(Tile<DIM, FP8>& t, const bf16x8_t (&q)[DIM / 32], float factor, int first,
+                                          int last, Running& run, float4_t (&o)[DIM / 16]) {
+  const int g = (threadIdx.x % 64) / 16;
+  float4_t s = {0, 0, 0, 0};
+#pragma unroll
+  for (int i = 0; i < DIM / 32; ++i) {
+    bf16x8_t a;
+    if constexpr (FP8)
+      a = octet(fp8_pair(t.k[2 * i], false), fp8_pair(t.k[2 * i], true), fp8_pair(t.k[2 * i + 1], false),
+                fp8_pair(t.k[2 * i + 1], true));
+    else
+      a = octet(t.k[4 * i], t.k[4 * i + 1], t.k[4 * i + 2], t.k[4 * i + 3]);
+    s = __builtin_amdgcn_mfma_f32_16x16x32_bf16(a, q[i], s, 0, 0, 0);
+  }
+#pragma unroll
+  for (int r = 0; r < 4; ++r) s[r] *= factor;
+  if (first > 0 || last < 16) {  // uniform: the tiles at either end
+#pragma unroll
+    for (int r = 0; r < 4; ++r) {
+      if (g * 4 + r < first || g * 4 + r >= last) {
+        s[r] = -INFINITY;
+#pragma unroll
+        for (int x = 0; x < Tile<DIM, FP8>::kDwords / 4; ++x) t.v[r][x] = 0;  // whatever the row holds, 0 times it is 0
+      }
+    }
+  }
+  float top = fmaxf(fmaxf(s[0], s[1]), fmaxf(s[2], s[3]));
+  if (__any(top > run.m + kSlack)) {
+    top = fmaxf(top, __shfl_xor(top, 16));
+    top = fmaxf(fmaxf(top, __shfl_xor(top, 32)), run.m);
+    const float keep = __builtin_amdgcn_exp2f(run.m - top);
+    run.m = top;
+    run.l *= keep;
+#pragma unroll
+    for (int i = 0; i < DIM / 16; ++i) o[i] *= keep;
+  }
+  float p[4], rest[4];
+#pragma unroll
+  for (int r = 0; r < 4; ++r) {
+    p[r] = __builtin_amdgcn_exp2f(s[r] - run.m);
+    run.l += p[r];
+  }
+  const f32x2_t p01 = {p[0], p[1]}, p23 = {p[2], p[3]};
+  const uint32_t h01 = __builtin_bit_cast(uint32_t, __builtin_convertvector(p01, bf16x2_t));
+  const uint32_t h23 = __builtin_bit_cast(uint32_t, __builtin_convertvector(p23, bf16x2_t));
+  rest[0] = p[0] - __uint_as_float(h01 << 16), rest[1] = p[1] - __uint_as_float(h01 & 0xFFFF0000u);
+  rest[2] = p[2] - __uint_as_float(h23 << 16), rest[3] = p[3] - __uint_as_float(h23 & 0xFFFF0000u);
+  const f32x2_t r01 = {rest[0], rest[1]}, r23 = {rest[2], rest[3]};
+  const short4_t hi = __builtin_bit_cast(short4_t, make_uint2(h01, h23));
+  const short4_t lo = __builtin_bit_cast(
+      short4_t, make_uint2(__builtin_bit_cast(uint32_t, __builtin_convertvector(r01, bf16x2_t)),
+                           __builtin_bit_cast(uint32_t, __builtin_convertvector(r23, bf16x2_t))));
+  auto product = [&](int i, uint32_t v01, uint32_t v23) {
+    const short4_t v = __builtin_bit_cast(short4_t, make_uint2(v01, v23));
+    o[i] = __builtin_amdgcn_mfma_f32_16x16x16bf16_1k(v, lo, o[i], 0, 0, 0);
+    o[i] = __builtin_amdgcn_mfma_f32_16x16x16bf16_1k(v, hi, o[i], 0, 0, 0);
+  };
+#pragma unroll
+  for (int x = 0; x < Tile<DIM, FP8>::kDwords / 4; ++x) {
+    if constexpr (FP8) {
+      uint32_t a[4], b[4];
+#pragma unroll
+      for (int r = 0; r < 4; ++r) a[r] = fp8_pair(t.v[r][x], false), b[r] = fp8_pair(t.v[r][x], true);
+      product(4 * x, low_halves(a[0], a[1]), low_halves(a[2], a[3]));
+      product(4 * x + 1, high_halves(a[0], a[1]), high_halves(a[2], a[3]));
+      product(4 * x + 2, low_halves(b[0], b[1]), low_halves(b[2], b[3]));
+      product(4 * x + 3, high_halves(b[0], b[1]), high_halves(b[2], b[3]));
+    } else {
+      product(2 * x, low_halves(t.v[0][x], t.v[1][x]), low_halves(t.v[2][x], t.v[3][x]));
+      product(2 * x + 1, high_halves(t.v[0][x], t.v[1][x]), high_halves(t.v[2][x], t.v[3][x]));
+    }
+  }
+}
+
+// Element of the head that output tile i holds in row c: value rows are read in
+// runs of 16 bytes at most, 16 lanes beside each other.
+template <int DIM, bool FP8>
+__device__ __forceinline__ int out_element(int c, int i) {
+  if constexpr (!FP8 && DIM == 256) return (i / 8) * 128 + c * 8 + i % 8;
+  return c * (DIM / 16) + i;
+}
+
+// Partial results of a split: per (sequence, query head, split) the sums, then m and l.
+__device__ __forceinline__ int64_t part_row(const AttnArgs& a, int b, int head, int splits, int s) {
+  return ((int64_t)b * a.q_heads + head) * splits + s;
+}
+
+template <int DIM, bool FP8>
+__global__ __launch_bounds__(kWaves * 64) void attn_decode_kernel(AttnArgs a, int splits, int split_tokens) {
+  constexpr int ES = FP8 ? 1 : 2, PAD = DIM + 4;
+  const int group = a.q_heads / a.cache.kv_heads, per = (group + 15) / 16;
+  const int kvh = blockIdx.x / per, head0 = kvh * group + (blockIdx.x % per) * 16;
+  const int heads = min(16, (kvh + 1) * group - head0);
+  const int split = blockIdx.y, b = blockIdx.z;
+  const int lane = threadIdx.x % 64, wave = threadIdx.x / 64, r = lane % 16, g = lane / 16;
+  const nvfp4_kv_cache& c = a.cache;
+
+  const int len = min(max(a.lens[b], 0), a.max_len);
+  const int begin = a.window > 0 ? max(0, len - a.window) : 0;
+  const int first_tile = begin / 16;
+  // this split's tokens, from the tile that `begin` lies in
+  const int from = first_tile * 16 + split * split_tokens;
+  const int to = min(len, from + split_tokens);
+  const bool only = first_tile * 16 + split_tokens >= len;  // the sequence has one split: no join
+  if (split > 0 && from >= len) return;
+
+  bf16x8_t q[DIM / 32];
+  {
+    const uint16_t* qp = a.q + (int64_t)b * a.ldq + (int64_t)(head0 + min(r, heads - 1)) * DIM;
+#pragma unroll
+    for (int i = 0; i < DIM / 32; ++i)
+      q[i] = *reinterpret_cast<const bf16x8_t*>(qp + (FP8 ? (i / 2) * 64 + g * 16 + (i % 2) * 8 : i * 32 + g * 8));
+  }
+  const float factor = a.scale * (FP8 ? *c.k_amax / 448.0f : 1.0f) * kLog2e;
+  const uint8_t* kc = static_cast<const uint8_t*>(c.k) + (int64_t)kvh * c.head_stride * ES;
+  const uint8_t* vc = static_cast<const uint8_t*>(c.v) + (int64_t)kvh * c.head_stride * ES;
+  const uint32_t row = (uint32_t)c.token_stride * ES;
+  const uint32_t k_off = r * row + g * 16;
+  const uint32_t v_off = g * 4 * row + (uint32_t)min(DIM * ES / 16, 16) * r;
+  const int tiles_per_page = c.page_size / 16;
+
+  Running run = {kNone, 0};
+  float4_t o[DIM / 16];
+#pragma unroll
+  for (int i = 0; i < DIM / 16; ++i) o[i] = {0, 0, 0, 0};
+
+  // tiles of this wave: from / 16 + wave + kWaves * n
+  const int tile0 = from / 16 + wave, tile_end = (to + 15) / 16;
+  const int mine = tile0 < tile_end ? (tile_end - tile0 + kWaves - 1) / kWaves : 0;
+  for (int n0 = 0; n0 < mine; n0 += 64) {
+    // page and place in it of 64 tiles ahead, one in each lane
+    const int ahead = min(n0 + lane, mine - 1) * kWaves + tile0;
+    const int page_index = ahead / tiles_per_page;
+    const int page = a.table[(int64_t)b * a.ldt + page_index];
+    const int inside = ahead - page_index * tiles_per_page;
+    const int count = min(64, mine - n0);
+    Tile<DIM, FP8> buf[2];
+    auto fetch = [&](Tile<DIM, FP8>& t, int n) {
+      const int p = __builtin_amdgcn_readlane(page, n), in = __builtin_amdgcn_readlane(inside, n);
+      if (p < 0 || p >= c.num_pages) return;
+      const int64_t at = ((int64_t)p * c.page_stride + (int64_t)in * 16 * c.token_stride) * ES;
+      load_tile<DIM, FP8>(t, kc + at, vc + at, k_off, v_off, row);
+    };
+    auto take = [&](Tile<DIM, FP8>& t, int n) {
+      const int p = __builtin_amdgcn_readlane(page, n);
+      if (p < 0 || p >= c.num_pages) return;
+      const int start = (tile0 + (n0 + n) * kWaves) * 16;
+      take_tile<DIM, FP8>(t, q, factor, begin - start, len - start, run, o);
+    };
+    fetch(buf[0], 0);
+    for (int n = 0; n < count; n += 2) {
+      if (n + 1 < count) fetch(buf[1], n + 1);
+      take(buf[0], n);
+      if (n + 1 < count) {
+        if (n + 2 < count) fetch(buf[0], n + 2);
+        take(buf[1], n + 1);
+      }
+    }
+  }
+  run.l += __shfl_xor(run.l, 16);
+  run.l += __shfl_xor(run.l, 32);
+
+  // the waves' results, joined in LDS
+  __shared__ float ms[kWaves][16], ls[kWaves][16];
+  extern __shared__ float4_t dynamic_lds[];
+  float* os = reinterpret_cast<float*>(dynamic_lds);  // [wave][heads][PAD]
+  if (r < heads) {
+    if (g == 0) ms[wave][r] = run.m, ls[wave][r] = run.l;
+#pragma unroll
+    for (int j = 0; j < 4; ++j)
+#pragma unroll
+      for (int i = 0; i < DIM / 16; i += 4) {
+        const float4_t w = {o[i][j], o[i + 1][j], o[i + 2][j], o[i + 3][j]};
+        *reinterpret_cast<float4_t*>(os + (wave * heads + r) * PAD + out_element<DIM, FP8>(g * 4 + j, i)) = w;
+      }
+  }
+  __syncthreads();
+  const float vg = FP8 ? *c.v_amax / 448.0f : 1.0f;
+  float* parts = static_cast<float*>(a.workspace);
+  float2* heads_ml = reinterpret_cast<float2*>(parts + part_row(a, (int)gridDim.z, 0, splits, 0) * DIM);
+  for (int e = threadIdx.x * 4; e < heads * DIM; e += kWaves * 64 * 4) {
+    const int h = e / DIM, d = e % DIM;
+    float top = kNone, sum = 0;
+#pragma unroll
+    for (int w = 0; w < kWaves; ++w) top = fmaxf(top, ms[w][h]);
+    float4_t x = {0, 0, 0, 0};
+#pragma unroll
+    for (int w = 0; w < kWaves; ++w) {
+      const float f = __builtin_amdgcn_exp2f(ms[w][h] - top);
+      sum += ls[w][h] * f;
+      x += *reinterpret_cast<const float4_t*>(os + (w * heads + h) * PAD + d) * f;
+    }
+    if (only) {
+      const float by = sum == 0 ? 0.0f : vg / sum;
+      const f32x2_t lo = {x[0] * by, x[1] * by}, hi = {x[2] * by, x[3] * by};
+      *reinterpret_cast<uint2*>(a.out + (int64_t)b * a.ldo + (int64_t)(head0 + h) * DIM + d) =
+          make_uint2(__builtin_bit_cast(uint32_t, __builtin_convertvector(lo, bf16x2_t)),
+                     __builtin_bit_cast(uint32_t, __builtin_convertvector(hi, bf16x2_t)));
+      if (a.lse && d == 0)
+        a.lse[(int64_t)b * a.q_heads + head0 + h] = sum == 0 ? -INFINITY : top * kLn2 + logf(sum);
+    } else {
+      const int64_t at = part_row(a, b, head0 + h, splits, split);
+      *reinterpret_cast<float4_t*>(parts + at * DIM + d) = x;
+      if (d == 0) heads_ml[at] = make_float2(top, sum);
+    }
+  }
+}
+
+// Joins the splits of one query head: each counts 2^(its m - the largest m).
+template <int DIM, bool FP8>
+__global__ __launch_bounds__(DIM) void attn_join_kernel(AttnArgs a, int splits, int split_tokens) {
+  const int h = blockIdx.x, b = blockIdx.y, d = threadIdx.x;
+  const int len = min(max(a.lens[b], 0), a.max_len);
+  const int start = a.window > 0 ? max(0, len - a.window) / 16 * 16 : 0;
+  const int used = (len - start + split_tokens - 1) / split_tokens;
+  if (used <= 1) return;
+  const float* parts = static_cast<const float*>(a.workspace);
+  const float2* ml = reinterpret_cast<const float2*>(parts + part_row(a, (int)gridDim.y, 0, splits, 0) * DIM) +
+                     part_row(a, b, h, splits, 0);
+  const float* row = parts + part_row(a, b, h, splits, 0) * DIM + d;
+  float top = kNone;
+  for (int s = 0; s < used; ++s) top = fmaxf(top, ml[s].x);
+  float sum = 0, x = 0;
+  for (int s = 0; s < used; ++s) {
+    const float2 w = ml[s];
+    const float f = __builtin_amdgcn_exp2f(w.x - top);
+    sum += w.y * f;
+    x += row[(int64_t)s * DIM] * f;
+  }
+  const float vg = FP8 ? *a.cache.v_amax / 448.0f : 1.0f;
+  a.out[(int64_t)b * a.ldo + (int64_t)h * DIM + d] = __builtin_bit_cast(uint16_t, (__bf16)(sum == 0 ? 0.0f : x * (vg / sum)));
+  if (a.lse && d == 0) a.lse[(int64_t)b * a.q_heads + h] = sum == 0 ? -INFINITY : top * kLn2 + logf(sum);
+}
+
+size_t attn_decode_workspace(int64_t B, int q_heads, int kv_heads, int head_dim, int64_t max_len, int64_t window) {
+  const Splits s = attn_splits(B, q_heads, kv_heads, max_len, window);
+  return s.count > 1 ? (size_t)B * q_heads * s.count * (head_dim + 2) * sizeof(float) : 0;
+}
+
+template <int DIM, bool FP8>
+static hipError_t launch_dim(const AttnArgs& a, hipStream_t stream) {
+  const int group = a.q_heads / a.cache.kv_heads;
+  const Splits s = attn_splits(a.B, a.q_heads, a.cache.kv_heads, a.max_len, a.window);
+  const dim3 grid(a.cache.kv_heads * ((group + 15) / 16), s.count, (unsigned)a.B);
+  const size_t lds = (size_t)kWaves * std::min(group, 16) * (DIM + 4) * sizeof(float);
+  hipError_t e = hipSuccess;
+  if (lds > 48 * 1024)  // above the default bound of dynamic LDS: sixteen heads of 256
+    e = hipFuncSetAttribute(reinterpret_cast<const void*>(&attn_decode_kernel<DIM, FP8>),
+                            hipFuncAttributeMaxDynamicSharedMemorySize, (int)lds);
+  if (e != hipSuccess) return e;
+  attn_decode_kernel<DIM, FP8><<<grid, kWaves * 64, lds, stream>>>(a, s.count, s.tokens);
+  e = hipGetLastError();
+  if (e != hipSuccess || s.count == 1) return e;
+  attn_join_kernel<DIM, FP8><<<dim3(a.q_heads, (unsigned)a.B), DIM, 0, stream>>>(a, s.count, s.tokens);
+  return hipGetLastError();
 }
 
 hipError_t launch_attn_decode(const AttnArgs& a, hipStream_t stream) {
-  if (a.cache.head_dim == 64)
-    launch_dim<64>(a, stream);
-  else if (a.cache.head_dim == 128)
-    launch_dim<128>(a, stream);
-  else
-    launch_dim<256>(a, stream);
-  return hipGetLastError();
+  const bool fp8 = a.cache.dtype == NVFP4_E4M3;
+  switch (a.cache.head_dim) {
+    case 64: return fp8 ? launch_dim<64, true>(a, stream) : launch_dim<64, false>(a, stream);
+    case 128: return fp8 ? launch_dim<128, true>(a, stream) : launch_dim<128, false>(a, stream);
+    default: return fp8 ? launch_dim<256, true>(a, stream) : launch_dim<256, false>(a, stream);
+  }
 }
 
 }  // namespace nvfp4

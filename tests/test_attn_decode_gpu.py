@@ -89,7 +89,7 @@ class Case:
 
 @pytest.mark.parametrize("fp8", [False, True])
 @pytest.mark.parametrize("heads,kv,dim,page", [(40, 8, 128, 64), (24, 4, 256, 16), (16, 16, 64, 48), (48, 2, 128, 16),
-                                               (33, 1, 64, 32), (1, 1, 256, 128)])
+                                               (33, 1, 64, 32), (1, 1, 256, 128), (17, 1, 256, 16)])
 def test_layouts_and_lengths(heads, kv, dim, page, fp8):
     lens = [1, 0, 15, 16, 17, 31, 33, 64, 100, 257, 3]
     say(f"[attn] heads={heads}/{kv}x{dim} page={page} fp8={fp8}")
