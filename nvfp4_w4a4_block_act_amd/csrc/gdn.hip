@@ -113,11 +113,4 @@ hipError_t launch_gdn_step(const GdnArgs& a, hipStream_t stream) {
   return hipGetLastError();
 }
 
-size_t gdn_prefill_workspace(int64_t, int64_t, int, int, int, int) { return 0; }
-
-hipError_t launch_gdn_prefill(const GdnArgs& a, hipStream_t stream) {
-  a.k_dim == 64 ? launch_recurrent<64, true>(a, stream) : launch_recurrent<128, true>(a, stream);
-  return hipGetLastError();
-}
-
 }  // namespace nvfp4

@@ -1,0 +1,486 @@
+// Gated linear attention with the delta rule over prompts, in chunks of 64 tokens.
+//
+// Within a chunk, with G_t the sum of the log decays up to token t, S the state
+// before the chunk and rows as matrices,
+//   A_ij = beta_i (k_i . k_j) e^(G_i - G_j)  (i > j),   T = (1 + A)^-1 diag(beta),
+//   N = T (V - e^G K S)                       (the values that are written; N = V without beta),
+//   O = scale (e^G Q S + P N),  P_ij = (q_i . k_j) e^(G_i - G_j)  (i >= j),
+//   S' = e^(G_64) S + K^T (e^(G_64 - G) N).
+// Two kernels: the first computes T and P of every chunk at once, the second
+// carries the state from chunk to chunk, one wave for 16 (or 32) of its columns,
+// which touch no other column.
+//
+// Precision.  The state is binary32 and its path keeps binary32's accuracy on the
+// bf16 matrix cores (fp32 matrix products run at 1/16 of their rate): q, k and v are
+// bf16 already, and a binary32 operand x enters as three bf16 planes, x = hi + mid +
+// lo to 24 significant bits, so K S is three products, and T times a binary32
+// matrix the six of the nine plane products that are above 2^-24.  What only
+// reaches the bf16 output keeps two planes (16 bits).  Sums accumulate in binary32.
+// G is summed in binary64, so that differences of far decays keep their digits.
+#include <algorithm>
+
+#include "common.hpp"
+#include "mixers.hpp"
+
+namespace nvfp4 {
+
+typedef __bf16 bf16x2_t __attribute__((ext_vector_type(2)));
+typedef __bf16 bf16x8_t __attribute__((ext_vector_type(8)));
+typedef float f32x2_t __attribute__((ext_vector_type(2)));
+
+constexpr int kChunk = 64;
+
+// Workspace of one (chunk, value head): operand blocks of 1 KB, lane-contiguous --
+// block (i, s) of a matrix holds for lane (t, g) row 16 i + t, columns 32 s + 4 g + j
+// and 32 s + 16 + 4 g + j (j < 4) -- for the six blocks that a lower triangle
+// touches, T in three planes and P in two; then e^G and e^(G_64 - G) of the rows.
+constexpr int kBlocks = 6, kBlockBytes = 1024;
+constexpr int kTPlanes = 3, kPPlanes = 2;
+__host__ __device__ constexpr int block_of(int i, int s) { return s == 0 ? i : 2 + i; }  // s == 1: i is 2 or 3
+struct Slot {
+  static constexpr int kP = 0, kDecay = kP + kBlocks * kPPlanes * kBlockBytes, kLeft = kDecay + kChunk * 4,
+                       kT = kDecay + 1024, kBytesLinear = kT, kBytesDelta = kT + kBlocks * kTPlanes * kBlockBytes;
+};
+
+// Chunk slots: sequence b's chunks start at cu[b] / 64 + b, so no two share one.
+__host__ __device__ inline int64_t chunk_slots(int64_t T, int64_t B) { return T / kChunk + B; }
+
+__device__ __forceinline__ uint32_t pack_bf16(float a, float b) {
+  const f32x2_t v = {a, b};
+  return __builtin_bit_cast(uint32_t, __builtin_convertvector(v, bf16x2_t));
+}
+
+// Two binary32 values as N bf16 planes: what a plane leaves goes to the next.
+template <int N>
+__device__ __forceinline__ void split_pair(float a, float b, uint32_t (&out)[N]) {
+#pragma unroll
+  for (int p = 0; p < N; ++p) {
+    out[p] = pack_bf16(a, b);
+    a -= __uint_as_float(out[p] << 16);
+    b -= __uint_as_float(out[p] & 0xFFFF0000u);
+  }
+}
+
+__device__ __forceinline__ float4_t mfma_bf16(uint4 a, uint4 b, float4_t c) {
+  return __builtin_amdgcn_mfma_f32_16x16x32_bf16(__builtin_bit_cast(bf16x8_t, a), __builtin_bit_cast(bf16x8_t, b), c, 0,
+                                                 0, 0);
+}
+
+__device__ __forceinline__ uint32_t low_halves(uint32_t a, uint32_t b) { return __builtin_amdgcn_perm(b, a, 0x05040100u); }
+__device__ __forceinline__ uint32_t high_halves(uint32_t a, uint32_t b) { return __builtin_amdgcn_perm(b, a, 0x07060302u); }
+
+struct Rows {
+  int64_t first;  // row of the sequence's first token
+  int count;
+};
+__device__ __forceinline__ Rows rows_of(const GdnArgs& a, int b) {
+  const int64_t first = min(max((int64_t)a.cu[b], (int64_t)0), a.T);
+  return {first, (int)(min(max((int64_t)a.cu[b + 1], first), a.T) - first)};
+}
+
+// ---- T and P of every chunk ------------------------------------------------------
+// A workgroup takes one chunk of one query/key head and its value heads in turn.
+// Wave w holds rows 16 w .. 16 w + 15 of K K^T and Q K^T.  The inverse: the four
+// 16 x 16 diagonal blocks by substitution, all at once in one wave (lane (n, g):
+// column n of block g), then the blocks below them, T_ij = -T_ii sum_k A_ik T_kj,
+// one diagonal after the other, as fp32 matrix products.
+constexpr int kLd = 68;  // row stride of the 64 x 64 matrices in LDS
+
+template <int DK, bool DELTA>
+__global__ __launch_bounds__(256) void gdn_chunk_kernel(GdnArgs a) {
+  __shared__ float mat[kChunk * kLd], inv[DELTA ? kChunk * kLd : 1];
+  __shared__ double sums[kChunk];
+  __shared__ float betas[kChunk];
+  const int hk = blockIdx.y, lane = threadIdx.x % 64, w = threadIdx.x / 64, n = lane % 16, g = lane / 16;
+  // the sequence whose slots this chunk's index falls into
+  const int64_t slot = blockIdx.x;
+  int b = -1;
+  for (int64_t b0 = 0; b0 < a.B; b0 += 64) {
+    const int64_t i = b0 + lane;
+    const bool before = i < a.B && min(max((int64_t)a.cu[i], (int64_t)0), a.T) / kChunk + i <= slot;
+    b += __popcll(__ballot(before));
+  }
+  if (b < 0) return;
+  const Rows rows = rows_of(a, b);
+  const int chunk = (int)(slot - (rows.first / kChunk + b));
+  const int count = min(kChunk, rows.count - chunk * kChunk);
+  if (chunk < 0 || count <= 0) return;
+  const int64_t row0 = rows.first + (int64_t)chunk * kChunk;
+
+  // rows 16 w + .. of K K^T and Q K^T against column blocks 0 .. w
+  float4_t kk[4], qk[4];
+  {
+    uint4 ka[DK / 32], qa[DK / 32];
+    const int64_t r = row0 + min(16 * w + n, count - 1);
+#pragma unroll
+    for (int s = 0; s < DK / 32; ++s) {
+      ka[s] = *reinterpret_cast<const uint4*>(a.k + r * a.ldk + hk * DK + s * 32 + g * 8);
+      qa[s] = *reinterpret_cast<const uint4*>(a.q + r * a.ldq + hk * DK + s * 32 + g * 8);
+    }
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+      kk[j] = qk[j] = {0, 0, 0, 0};
+      if (j > w) continue;
+      const int64_t c = row0 + min(16 * j + n, count - 1);
+#pragma unroll
+      for (int s = 0; s < DK / 32; ++s) {
+        const uint4 kb = *reinterpret_cast<const uint4*>(a.k + c * a.ldk + hk * DK + s * 32 + g * 8);
+        if (DELTA) kk[j] = mfma_bf16(ka[s], kb, kk[j]);
+        qk[j] = mfma_bf16(qa[s], kb, qk[j]);
+      }
+    }
+  }
+  const int many = a.v_heads / a.k_heads;
+  for (int hv = hk * many; hv < (hk + 1) * many; ++hv) {
+    uint8_t* to = static_cast<uint8_t*>(a.workspace) +
+                  (slot * a.v_heads + hv) * (int64_t)(DELTA ? Slot::kBytesDelta : Slot::kBytesLinear);
+    if (w == 0) {
+      const int64_t r = row0 + min(lane, count - 1);
+      // below -1000 a factor is 0 in binary32 either way, and the sums stay finite
+      const float step = lane < count ? a.g[r * a.ldg + hv] : 0.0f;
+      double sum = step < -1000.0f ? -1000.0 : (double)step;
+#pragma unroll
+      for (int d = 1; d < 64; d *= 2) {
+        const double x = __shfl_up(sum, d);
+        if (lane >= d) sum += x;
+      }
+      sums[lane] = sum;
+      if (DELTA) betas[lane] = lane < count ? a.beta[r * a.ldb + hv] : 0.0f;
+      const double all = __shfl(sum, 63);
+      reinterpret_cast<float*>(to + Slot::kDecay)[lane] = expf((float)sum);
+      reinterpret_cast<float*>(to + Slot::kLeft)[lane] = lane < count ? expf((float)(all - sum)) : 0.0f;
+    }
+    __syncthreads();
+    // A into mat, rows of this wave; P stays in registers
+    float4_t p[4];
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+      p[j] = {0, 0, 0, 0};
+      if (j > w) continue;
+#pragma unroll
+      for (int r = 0; r < 4; ++r) {
+        const int row = 16 * w + 4 * g + r, col = 16 * j + n;
+        const float fade = row >= col && row < count ? expf((float)(sums[row] - sums[col])) : 0.0f;
+        p[j][r] = row >= col && row < count ? a.scale * qk[j][r] * fade : 0.0f;
+        if (DELTA) mat[row * kLd + col] = row > col ? betas[row] * kk[j][r] * fade : 0.0f;
+      }
+    }
+    if (DELTA) {
+      __syncthreads();
+      if (w == 0) {  // block g, column n of the diagonal blocks' inverses
+        const float* blk = mat + (16 * g) * kLd + 16 * g;
+        float x[16];
+#pragma unroll
+        for (int i = 0; i < 16; ++i) {
+          float s = i == n ? 1.0f : 0.0f;
+#pragma unroll
+          for (int j = 0; j < i; ++j) s = __builtin_fmaf(-blk[i * kLd + j], x[j], s);
+          x[i] = s;
+        }
+#pragma unroll
+        for (int i = 0; i < 16; ++i) inv[(16 * g + i) * kLd + 16 * g + n] = x[i];
+      }
+      __syncthreads();
+#pragma unroll
+      for (int d = 1; d < 4; ++d) {  // blocks (i, i - d)
+        const int i = w, j = w - d;
+        if (j >= 0) {
+          float4_t m = {0, 0, 0, 0}, t = {0, 0, 0, 0};
+          for (int k = j; k < i; ++k)
+#pragma unroll
+            for (int s = 0; s < 4; ++s)
+              m = __builtin_amdgcn_mfma_f32_16x16x4f32(mat[(16 * i + n) * kLd + 16 * k + 4 * s + g],
+                                                       inv[(16 * k + 4 * s + g) * kLd + 16 * j + n], m, 0, 0, 0);
+          // rows 4 g + r of m are where step r of the next product wants them
+#pragma unroll
+          for (int r = 0; r < 4; ++r)
+            t = __builtin_amdgcn_mfma_f32_16x16x4f32(inv[(16 * i + n) * kLd + 16 * i + 4 * g + r], m[r], t, 0, 0, 0);
+#pragma unroll
+          for (int r = 0; r < 4; ++r) inv[(16 * i + 4 * g + r) * kLd + 16 * j + n] = -t[r];
+        }
+        __syncthreads();
+      }
+    }
+    // P to LDS (over A), then both matrices as operand blocks
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+      if (j > w && j / 2 > w / 2) continue;  // a block's second half may lie above the diagonal: zeros
+#pragma unroll
+      for (int r = 0; r < 4; ++r) {
+        mat[(16 * w + 4 * g + r) * kLd + 16 * j + n] = p[j][r];
+        if (DELTA && j > w) inv[(16 * w + 4 * g + r) * kLd + 16 * j + n] = 0.0f;
+      }
+    }
+    __syncthreads();
+#pragma unroll
+    for (int s = 0; s < 2; ++s) {
+      if (s == 1 && w < 2) continue;
+      const int blk = block_of(w, s);
+      const int at = (16 * w + n) * kLd + 32 * s + 4 * g;
+      uint32_t pl[4][kPPlanes], tl[4][kTPlanes];
+#pragma unroll
+      for (int h = 0; h < 2; ++h) {
+        const float4 x = *reinterpret_cast<const float4*>(mat + at + 16 * h);
+        split_pair(x.x, x.y, pl[2 * h]);
+        split_pair(x.z, x.w, pl[2 * h + 1]);
+        if (DELTA) {
+          const float4 y = *reinterpret_cast<const float4*>(inv + at + 16 * h);
+          const float4 bt = *reinterpret_cast<const float4*>(betas + 32 * s + 4 * g + 16 * h);
+          split_pair(y.x * bt.x, y.y * bt.y, tl[2 * h]);
+          split_pair(y.z * bt.z, y.w * bt.w, tl[2 * h + 1]);
+        }
+      }
+#pragma unroll
+      for (int q = 0; q < kPPlanes; ++q)
+        *reinterpret_cast<uint4*>(to + Slot::kP + (q * kBlocks + blk) * kBlockBytes + lane * 16) =
+            make_uint4(pl[0][q], pl[1][q], pl[2][q], pl[3][q]);
+      if (DELTA)
+#pragma unroll
+        for (int q = 0; q < kTPlanes; ++q)
+          *reinterpret_cast<uint4*>(to + Slot::kT + (q * kBlocks + blk) * kBlockBytes + lane * 16) =
+              make_uint4(tl[0][q], tl[1][q], tl[2][q], tl[3][q]);
+    }
+    __syncthreads();
+  }
+}
+
+// ---- the state from chunk to chunk -----------------------------------------------
+// A wave holds 16 NT columns of the state: tile (c, i) of E = DK / 16 tiles holds in
+// lane (n, g), register r the element of row (4 g + r) E + i, column n.  Everything
+// it multiplies stays in its registers: a product's output (row 4 g + r in register
+// r) is the next product's right operand as it is, with the left operand's columns
+// taken in that order.  A lane's state rows are g DK / 4 + 0 .. DK / 4 - 1 in the
+// order (register, tile), so K S takes 16-byte runs of a key row; K^T is read as
+// whole key rows, a lane E elements of each of 4 tokens, transposed within the lane.
+template <int DK, int NT, bool DELTA>
+__global__ __launch_bounds__(64, 1) void gdn_state_kernel(GdnArgs a) {
+  constexpr int E = DK / 16, KS = DK / 32;
+  const int slabs = a.v_dim / (16 * NT);
+  // slabs of a head run on one XCD (workgroups go round the eight in turn) and share its L2
+  const int64_t turn = blockIdx.x / 8;
+  const int64_t pair = (turn / slabs) * 8 + blockIdx.x % 8;
+  const int slab = (int)(turn % slabs);
+  if (pair >= a.B * a.v_heads) return;
+  const int b = (int)(pair / a.v_heads), h = (int)(pair % a.v_heads), hk = h / (a.v_heads / a.k_heads);
+  const int64_t slot = a.index ? a.index[b] : b;
+  if (slot < 0 || slot >= a.num_states) return;
+  const int lane = threadIdx.x, n = lane % 16, g = lane / 16;
+  const Rows rows = rows_of(a, b);
+
+  float* st = a.state + ((slot * a.v_heads + h) * DK + 4 * g * E) * (int64_t)a.v_dim + slab * 16 * NT + n;
+  float4_t S[NT][E];
+  const bool load = a.has_state && a.has_state[b] != 0;
+#pragma unroll
+  for (int c = 0; c < NT; ++c)
+#pragma unroll
+    for (int i = 0; i < E; ++i)
+#pragma unroll
+      for (int r = 0; r < 4; ++r) S[c][i][r] = load ? st[(int64_t)(r * E + i) * a.v_dim + 16 * c] : 0.0f;
+
+  const int chunks = (rows.count + kChunk - 1) / kChunk;
+  const uint8_t* ws = static_cast<const uint8_t*>(a.workspace) +
+                      ((rows.first / kChunk + b) * a.v_heads + h) *
+                          (int64_t)(DELTA ? Slot::kBytesDelta : Slot::kBytesLinear);
+  const int64_t ws_step = (int64_t)a.v_heads * (DELTA ? Slot::kBytesDelta : Slot::kBytesLinear);
+  const int col = h * a.v_dim + slab * 16 * NT + n;
+
+  for (int ch = 0; ch < chunks; ++ch, ws += ws_step) {
+    const int64_t row0 = rows.first + (int64_t)ch * kChunk;
+    const int last = min(kChunk, rows.count - ch * kChunk) - 1;
+    // the state's planes as right operands of K S and Q S
+    uint4 sp[3][NT][KS];
+#pragma unroll
+    for (int c = 0; c < NT; ++c)
+#pragma unroll
+      for (int s = 0; s < KS; ++s) {
+        uint32_t w[4][3];
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+          const int f = s * 8 + 2 * e;
+          split_pair(S[c][f % E][f / E], S[c][(f + 1) % E][(f + 1) / E], w[e]);
+        }
+#pragma unroll
+        for (int p = 0; p < 3; ++p) sp[p][c][s] = make_uint4(w[0][p], w[1][p], w[2][p], w[3][p]);
+      }
+    float4_t decay[4], left[4];
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      decay[i] = *reinterpret_cast<const float4_t*>(ws + Slot::kDecay + (16 * i + 4 * g) * 4);
+      left[i] = *reinterpret_cast<const float4_t*>(ws + Slot::kLeft + (16 * i + 4 * g) * 4);
+    }
+    const float whole = *reinterpret_cast<const float*>(ws + Slot::kDecay + 63 * 4);
+
+    float4_t o[NT][4], N[NT][4];
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      const int64_t r = row0 + min(16 * i + n, last);
+      const uint16_t* kp = a.k + r * a.ldk + hk * DK + g * (DK / 4);
+      const uint16_t* qp = a.q + r * a.ldq + hk * DK + g * (DK / 4);
+      float4_t ks[NT], qs[NT];
+#pragma unroll
+      for (int c = 0; c < NT; ++c) ks[c] = qs[c] = {0, 0, 0, 0};
+#pragma unroll
+      for (int s = 0; s < KS; ++s) {
+        const uint4 qa = *reinterpret_cast<const uint4*>(qp + s * 8);
+        uint4 ka;
+        if (DELTA) ka = *reinterpret_cast<const uint4*>(kp + s * 8);
+#pragma unroll
+        for (int c = 0; c < NT; ++c) {
+          if (DELTA) {
+#pragma unroll
+            for (int p = 2; p >= 0; --p) ks[c] = mfma_bf16(ka, sp[p][c][s], ks[c]);
+          }
+#pragma unroll
+          for (int p = 1; p >= 0; --p) qs[c] = mfma_bf16(qa, sp[p][c][s], qs[c]);
+        }
+      }
+#pragma unroll
+      for (int c = 0; c < NT; ++c)
+#pragma unroll
+        for (int r4 = 0; r4 < 4; ++r4) {
+          const int64_t vr = row0 + min(16 * i + 4 * g + r4, last);
+          const float v = __uint_as_float((uint32_t)a.v[vr * a.ldv + col + 16 * c] << 16);
+          o[c][i][r4] = a.scale * decay[i][r4] * qs[c][r4];
+          N[c][i][r4] = DELTA ? v - decay[i][r4] * ks[c][r4] : v;
+        }
+    }
+    if (DELTA) {  // N = T (V - e^G K S)
+#pragma unroll
+      for (int c = 0; c < NT; ++c) {
+        uint4 rp[3][2];
+#pragma unroll
+        for (int s = 0; s < 2; ++s) {
+          uint32_t w[4][3];
+#pragma unroll
+          for (int e = 0; e < 4; ++e) split_pair(N[c][2 * s + e / 2][(e % 2) * 2], N[c][2 * s + e / 2][(e % 2) * 2 + 1], w[e]);
+#pragma unroll
+          for (int p = 0; p < 3; ++p) rp[p][s] = make_uint4(w[0][p], w[1][p], w[2][p], w[3][p]);
+        }
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          float4_t x = {0, 0, 0, 0};
+#pragma unroll
+          for (int s = 0; s <= i / 2; ++s) {
+            uint4 t[3];
+#pragma unroll
+            for (int p = 0; p < 3; ++p)
+              t[p] = *reinterpret_cast<const uint4*>(ws + Slot::kT + (p * kBlocks + block_of(i, s)) * kBlockBytes + lane * 16);
+            x = mfma_bf16(t[2], rp[0][s], x);
+            x = mfma_bf16(t[1], rp[1][s], x);
+            x = mfma_bf16(t[0], rp[2][s], x);
+            x = mfma_bf16(t[1], rp[0][s], x);
+            x = mfma_bf16(t[0], rp[1][s], x);
+            x = mfma_bf16(t[0], rp[0][s], x);
+          }
+          N[c][i] = x;
+        }
+      }
+    }
+    // O += P N and the state's update
+    uint4 np[2][NT][2], up[3][NT][2];
+#pragma unroll
+    for (int c = 0; c < NT; ++c)
+#pragma unroll
+      for (int s = 0; s < 2; ++s) {
+        uint32_t w[4][2], u[4][3];
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+          const int i = 2 * s + e / 2, r = (e % 2) * 2;
+          split_pair(N[c][i][r], N[c][i][r + 1], w[e]);
+          split_pair(N[c][i][r] * left[i][r], N[c][i][r + 1] * left[i][r + 1], u[e]);
+        }
+#pragma unroll
+        for (int p = 0; p < 2; ++p) np[p][c][s] = make_uint4(w[0][p], w[1][p], w[2][p], w[3][p]);
+#pragma unroll
+        for (int p = 0; p < 3; ++p) up[p][c][s] = make_uint4(u[0][p], u[1][p], u[2][p], u[3][p]);
+      }
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+#pragma unroll
+      for (int s = 0; s <= i / 2; ++s) {
+        uint4 p[2];
+#pragma unroll
+        for (int q = 0; q < 2; ++q)
+          p[q] = *reinterpret_cast<const uint4*>(ws + Slot::kP + (q * kBlocks + block_of(i, s)) * kBlockBytes + lane * 16);
+#pragma unroll
+        for (int c = 0; c < NT; ++c) {
+          o[c][i] = mfma_bf16(p[1], np[0][c][s], o[c][i]);
+          if (DELTA) o[c][i] = mfma_bf16(p[0], np[1][c][s], o[c][i]);  // without it N is bf16 itself
+          o[c][i] = mfma_bf16(p[0], np[0][c][s], o[c][i]);
+        }
+      }
+#pragma unroll
+      for (int c = 0; c < NT; ++c)
+#pragma unroll
+        for (int r = 0; r < 4; ++r)
+          if (16 * i + 4 * g + r <= last)
+            a.out[(row0 + 16 * i + 4 * g + r) * a.ldo + col + 16 * c] = __builtin_bit_cast(uint16_t, (__bf16)o[c][i][r]);
+    }
+#pragma unroll
+    for (int c = 0; c < NT; ++c)
+#pragma unroll
+      for (int i = 0; i < E; ++i) S[c][i] *= whole;
+#pragma unroll
+    for (int s = 0; s < 2; ++s) {
+      uint32_t kt[8][E / 2];  // E elements of the rows of tokens 32 s + 4 g + j and 32 s + 16 + 4 g + j
+#pragma unroll
+      for (int j = 0; j < 8; ++j) {
+        const int64_t r = row0 + min(32 * s + (j / 4) * 16 + 4 * g + j % 4, last);
+        const uint16_t* p = a.k + r * a.ldk + hk * DK + n * E;
+        if constexpr (E == 8) {
+          const uint4 x = *reinterpret_cast<const uint4*>(p);
+          kt[j][0] = x.x, kt[j][1] = x.y, kt[j][2] = x.z, kt[j][3] = x.w;
+        } else {
+          const uint2 x = *reinterpret_cast<const uint2*>(p);
+          kt[j][0] = x.x, kt[j][1] = x.y;
+        }
+      }
+#pragma unroll
+      for (int i = 0; i < E; ++i) {
+        uint32_t w[4];
+#pragma unroll
+        for (int e = 0; e < 4; ++e)
+          w[e] = i % 2 ? high_halves(kt[2 * e][i / 2], kt[2 * e + 1][i / 2]) : low_halves(kt[2 * e][i / 2], kt[2 * e + 1][i / 2]);
+        const uint4 ka = make_uint4(w[0], w[1], w[2], w[3]);
+#pragma unroll
+        for (int c = 0; c < NT; ++c)
+#pragma unroll
+          for (int p = 2; p >= 0; --p) S[c][i] = mfma_bf16(ka, up[p][c][s], S[c][i]);
+      }
+    }
+  }
+#pragma unroll
+  for (int c = 0; c < NT; ++c)
+#pragma unroll
+    for (int i = 0; i < E; ++i)
+#pragma unroll
+      for (int r = 0; r < 4; ++r) st[(int64_t)(r * E + i) * a.v_dim + 16 * c] = S[c][i][r];
+}
+
+size_t gdn_prefill_workspace(int64_t T, int64_t B, int, int v_heads, int, int) {
+  return T == 0 ? 0 : (size_t)chunk_slots(T, B) * v_heads * Slot::kBytesDelta;
+}
+
+template <int DK, bool DELTA>
+static hipError_t launch_prefill(const GdnArgs& a, hipStream_t stream) {
+  if (a.T > 0) {
+    gdn_chunk_kernel<DK, DELTA><<<dim3((unsigned)chunk_slots(a.T, a.B), a.k_heads), 256, 0, stream>>>(a);
+    const hipError_t e = hipGetLastError();
+    if (e != hipSuccess) return e;
+  }
+  const int64_t pairs = (a.B * a.v_heads + 7) / 8 * 8;
+  const bool two = pairs * (a.v_dim / 16) > 4 * kCUs;
+  const unsigned grid = (unsigned)(pairs * (a.v_dim / (two ? 32 : 16)));
+  if (two)
+    gdn_state_kernel<DK, 2, DELTA><<<grid, 64, 0, stream>>>(a);
+  else
+    gdn_state_kernel<DK, 1, DELTA><<<grid, 64, 0, stream>>>(a);
+  return hipGetLastError();
+}
+
+hipError_t launch_gdn_prefill(const GdnArgs& a, hipStream_t stream) {
+  if (a.k_dim == 64) return a.beta ? launch_prefill<64, true>(a, stream) : launch_prefill<64, false>(a, stream);
+  return a.beta ? launch_prefill<128, true>(a, stream) : launch_prefill<128, false>(a, stream);
+}
+
+}  // namespace nvfp4
