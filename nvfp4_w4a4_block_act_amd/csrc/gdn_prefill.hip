@@ -7,7 +7,7 @@
 //   O = scale (e^G Q S + P N),  P_ij = (q_i . k_j) e^(G_i - G_j)  (i >= j),
 //   S' = e^(G_64) S + K^T (e^(G_64 - G) N).
 // Two kernels: the first computes T and P of every chunk at once, the second
-// carries the state from chunk to chunk, one wave for 16 (or 32) of its columns,
+// carries the state from chunk to chunk, a workgroup for 16 (or 32) of its columns,
 // which touch no other column.
 //
 // Precision.  The state is binary32 and its path keeps binary32's accuracy on the
@@ -18,6 +18,7 @@
 // reaches the bf16 output keeps two planes (16 bits).  Sums accumulate in binary32.
 // G is summed in binary64, so that differences of far decays keep their digits.
 #include <algorithm>
+#include <type_traits>
 
 #include "common.hpp"
 #include "mixers.hpp"
@@ -245,16 +246,36 @@ __global__ __launch_bounds__(256) void gdn_chunk_kernel(GdnArgs a) {
 }
 
 // ---- the state from chunk to chunk -----------------------------------------------
-// A wave holds 16 NT columns of the state: tile (c, i) of E = DK / 16 tiles holds in
-// lane (n, g), register r the element of row (4 g + r) E + i, column n.  Everything
-// it multiplies stays in its registers: a product's output (row 4 g + r in register
-// r) is the next product's right operand as it is, with the left operand's columns
-// taken in that order.  A lane's state rows are g DK / 4 + 0 .. DK / 4 - 1 in the
-// order (register, tile), so K S takes 16-byte runs of a key row; K^T is read as
-// whole key rows, a lane E elements of each of 4 tokens, transposed within the lane.
+// A workgroup of four waves carries 16 NT columns.  Wave w takes the token rows
+// 16 w .. 16 w + 15 of every product over tokens (K S, Q S, T R, P N) and a quarter of
+// the state's rows, so each left operand is read by one wave only, from global
+// memory into the registers that its last use freed a chunk before.  Right operands
+// -- the planes of S, of R = V - e^G K S and of N -- pass between the waves through LDS
+// in operand order (16 bytes for each lane, no bank conflicts): a product leaves
+// row 4 g + r in register r, which is how the next product's right operand wants
+// its rows, with the left operand's columns taken in that order.  The key rows go
+// through LDS too, for K^T.
+//
+// LDS, in units of NT KB: S of this chunk and of the next in two areas of 12; N
+// (planes for the state's update, then for the output) over S once every wave has read it; R in
+// 6.  Without beta N is V, known before the chunk, and lies in R's place.
+constexpr int kKeyRow = 272;  // bytes of a key row of 128 in LDS: rows 4 apart fall on other banks
+
 template <int DK, int NT, bool DELTA>
-__global__ __launch_bounds__(64, 1) void gdn_state_kernel(GdnArgs a) {
-  constexpr int E = DK / 16, KS = DK / 32;
+struct StateLds {
+  static constexpr int kSteps = DK / 32, kSPlanes = DELTA ? 3 : 2;
+  static constexpr int kS = kSPlanes * kSteps * NT * 1024;      // planes of S
+  static constexpr int kN = (3 + (DELTA ? 2 : 1)) * 2 * NT * 1024;  // planes of e^(G_64 - G) N and of N
+  static constexpr int kX = kS > kN || !DELTA ? kS : kN;
+  static constexpr int kY = DELTA ? 3 * 2 * NT * 1024 : kN;
+  static constexpr int kKeys = 2 * kX + kY, kBytes = kKeys + kChunk * kKeyRow;
+};
+
+template <int DK, int NT, bool DELTA>
+__global__ __launch_bounds__(256, 1) void gdn_state_kernel(GdnArgs a) {
+  using L = StateLds<DK, NT, DELTA>;
+  constexpr int KS = L::kSteps, TW = DK / 64, SP = L::kSPlanes, NP = DELTA ? 2 : 1;
+  __shared__ __align__(16) uint8_t lds[L::kBytes];
   const int slabs = a.v_dim / (16 * NT);
   // slabs of a head run on one XCD (workgroups go round the eight in turn) and share its L2
   const int64_t turn = blockIdx.x / 8;
@@ -264,197 +285,270 @@ __global__ __launch_bounds__(64, 1) void gdn_state_kernel(GdnArgs a) {
   const int b = (int)(pair / a.v_heads), h = (int)(pair % a.v_heads), hk = h / (a.v_heads / a.k_heads);
   const int64_t slot = a.index ? a.index[b] : b;
   if (slot < 0 || slot >= a.num_states) return;
-  const int lane = threadIdx.x, n = lane % 16, g = lane / 16;
+  const int lane = threadIdx.x % 64, n = lane % 16, g = lane / 16;
+  const int w = __builtin_amdgcn_readfirstlane(threadIdx.x / 64);
   const Rows rows = rows_of(a, b);
+  const int chunks = (rows.count + kChunk - 1) / kChunk;
 
-  float* st = a.state + ((slot * a.v_heads + h) * DK + 4 * g * E) * (int64_t)a.v_dim + slab * 16 * NT + n;
-  float4_t S[NT][E];
+  // state rows of this wave: tile i, register r holds row w DK / 4 + (4 g + r) TW + i, column n
+  float* st = a.state + ((slot * a.v_heads + h) * DK + w * (DK / 4) + 4 * g * TW) * (int64_t)a.v_dim + slab * 16 * NT + n;
+  float4_t S[NT][TW];
   const bool load = a.has_state && a.has_state[b] != 0;
 #pragma unroll
   for (int c = 0; c < NT; ++c)
 #pragma unroll
-    for (int i = 0; i < E; ++i)
+    for (int i = 0; i < TW; ++i)
 #pragma unroll
-      for (int r = 0; r < 4; ++r) S[c][i][r] = load ? st[(int64_t)(r * E + i) * a.v_dim + 16 * c] : 0.0f;
+      for (int r = 0; r < 4; ++r) S[c][i][r] = load ? st[(int64_t)(r * TW + i) * a.v_dim + 16 * c] : 0.0f;
 
-  const int chunks = (rows.count + kChunk - 1) / kChunk;
   const uint8_t* ws = static_cast<const uint8_t*>(a.workspace) +
                       ((rows.first / kChunk + b) * a.v_heads + h) *
                           (int64_t)(DELTA ? Slot::kBytesDelta : Slot::kBytesLinear);
   const int64_t ws_step = (int64_t)a.v_heads * (DELTA ? Slot::kBytesDelta : Slot::kBytesLinear);
   const int col = h * a.v_dim + slab * 16 * NT + n;
+  const int steps = w / 2 + 1;  // 32-token steps that rows 16 w .. reach in a lower triangle
 
-  for (int ch = 0; ch < chunks; ++ch, ws += ws_step) {
+  // left operands in flight
+  uint4 ka[KS], qa[KS], ta[2][3], pa[2][2];
+  uint16_t va[NT][4];
+  float4_t decay, left;
+  float whole;
+  auto key_run = [&](const uint16_t* row, int s) {  // the order of the state's planes
+    if constexpr (TW == 2) return *reinterpret_cast<const uint4*>(row + 32 * s + 8 * g);
+    const uint2 x = *reinterpret_cast<const uint2*>(row + 32 * s + 4 * g);
+    const uint2 y = *reinterpret_cast<const uint2*>(row + 32 * s + 16 + 4 * g);
+    return make_uint4(x.x, x.y, y.x, y.y);
+  };
+  auto fetch_rows = [&](int ch) {  // K, Q, V and the decays of a chunk
     const int64_t row0 = rows.first + (int64_t)ch * kChunk;
     const int last = min(kChunk, rows.count - ch * kChunk) - 1;
-    // the state's planes as right operands of K S and Q S
-    uint4 sp[3][NT][KS];
+    const int64_t r = row0 + min(16 * w + n, last);
+#pragma unroll
+    for (int s = 0; s < KS; ++s) {
+      ka[s] = key_run(a.k + r * a.ldk + hk * DK, s);
+      qa[s] = key_run(a.q + r * a.ldq + hk * DK, s);
+    }
+    const uint8_t* p = ws + ch * ws_step;
+    decay = *reinterpret_cast<const float4_t*>(p + Slot::kDecay + (16 * w + 4 * g) * 4);
+    left = *reinterpret_cast<const float4_t*>(p + Slot::kLeft + (16 * w + 4 * g) * 4);
+    whole = *reinterpret_cast<const float*>(p + Slot::kDecay + 63 * 4);
 #pragma unroll
     for (int c = 0; c < NT; ++c)
 #pragma unroll
-      for (int s = 0; s < KS; ++s) {
-        uint32_t w[4][3];
+      for (int j = 0; j < 4; ++j) va[c][j] = a.v[(row0 + min(16 * w + 4 * g + j, last)) * a.ldv + col + 16 * c];
+  };
+  auto fetch_t = [&](int ch) {
 #pragma unroll
-        for (int e = 0; e < 4; ++e) {
-          const int f = s * 8 + 2 * e;
-          split_pair(S[c][f % E][f / E], S[c][(f + 1) % E][(f + 1) / E], w[e]);
-        }
+    for (int s = 0; s < 2; ++s)
 #pragma unroll
-        for (int p = 0; p < 3; ++p) sp[p][c][s] = make_uint4(w[0][p], w[1][p], w[2][p], w[3][p]);
+      for (int p = 0; p < 3; ++p)
+        if (s < steps)
+          ta[s][p] = *reinterpret_cast<const uint4*>(ws + ch * ws_step + Slot::kT +
+                                                     (p * kBlocks + block_of(w, s)) * kBlockBytes + lane * 16);
+  };
+  auto fetch_p = [&](int ch) {
+#pragma unroll
+    for (int s = 0; s < 2; ++s)
+#pragma unroll
+      for (int p = 0; p < 2; ++p)
+        if (s < steps)
+          pa[s][p] = *reinterpret_cast<const uint4*>(ws + ch * ws_step + Slot::kP +
+                                                     (p * kBlocks + block_of(w, s)) * kBlockBytes + lane * 16);
+  };
+  // this wave's rows of S as right-operand planes
+  auto put_state = [&](uint8_t* x) {
+#pragma unroll
+    for (int c = 0; c < NT; ++c) {
+      uint32_t z[2 * TW][SP];
+#pragma unroll
+      for (int e = 0; e < 2 * TW; ++e) {
+        const int f = 2 * e;
+        split_pair(S[c][f % TW][f / TW], S[c][(f + 1) % TW][(f + 1) / TW], z[e]);
       }
-    float4_t decay[4], left[4];
 #pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      decay[i] = *reinterpret_cast<const float4_t*>(ws + Slot::kDecay + (16 * i + 4 * g) * 4);
-      left[i] = *reinterpret_cast<const float4_t*>(ws + Slot::kLeft + (16 * i + 4 * g) * 4);
+      for (int p = 0; p < SP; ++p) {
+        if constexpr (TW == 2)
+          *reinterpret_cast<uint4*>(x + ((p * KS + w) * NT + c) * 1024 + lane * 16) =
+              make_uint4(z[0][p], z[1][p], z[2][p], z[3][p]);
+        else
+          *reinterpret_cast<uint2*>(x + ((p * KS + w / 2) * NT + c) * 1024 + lane * 16 + (w % 2) * 8) =
+              make_uint2(z[0][p], z[1][p]);
+      }
     }
-    const float whole = *reinterpret_cast<const float*>(ws + Slot::kDecay + 63 * 4);
+  };
+  // four rows of this wave as P planes at x
+  auto put_rows = [&](uint8_t* x, int c, float4_t v, auto planes) {
+    constexpr int P = decltype(planes)::value;
+    uint32_t z[2][P];
+    split_pair(v[0], v[1], z[0]);
+    split_pair(v[2], v[3], z[1]);
+#pragma unroll
+    for (int p = 0; p < P; ++p)
+      *reinterpret_cast<uint2*>(x + ((p * 2 + w / 2) * NT + c) * 1024 + lane * 16 + (w % 2) * 8) =
+          make_uint2(z[0][p], z[1][p]);
+  };
+  auto get = [&](const uint8_t* x, int p, int per, int s, int c) {
+    return *reinterpret_cast<const uint4*>(x + ((p * per + s) * NT + c) * 1024 + lane * 16);
+  };
 
-    float4_t o[NT][4], N[NT][4];
+  uint8_t* x0 = lds;
+  uint8_t* x1 = lds + L::kX;
+  uint8_t* y = lds + 2 * L::kX;
+  uint8_t* keys = lds + L::kKeys;
+  if (chunks > 0) {
+    fetch_rows(0);
+    if (DELTA) fetch_t(0);
+    fetch_p(0);
+    put_state(x0);
+    __syncthreads();
+  }
+  for (int ch = 0; ch < chunks; ++ch) {
+    const int64_t row0 = rows.first + (int64_t)ch * kChunk;
+    const int last = min(kChunk, rows.count - ch * kChunk) - 1;
+    const int next = min(ch + 1, chunks - 1);
+    // key rows for K^T
 #pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      const int64_t r = row0 + min(16 * i + n, last);
-      const uint16_t* kp = a.k + r * a.ldk + hk * DK + g * (DK / 4);
-      const uint16_t* qp = a.q + r * a.ldq + hk * DK + g * (DK / 4);
-      float4_t ks[NT], qs[NT];
+    for (int s = 0; s < KS; ++s) {
+      uint8_t* to = keys + (16 * w + n) * kKeyRow;
+      if constexpr (TW == 2) {
+        *reinterpret_cast<uint4*>(to + 64 * s + 16 * g) = ka[s];
+      } else {
+        *reinterpret_cast<uint2*>(to + 64 * s + 8 * g) = make_uint2(ka[s].x, ka[s].y);
+        *reinterpret_cast<uint2*>(to + 64 * s + 32 + 8 * g) = make_uint2(ka[s].z, ka[s].w);
+      }
+    }
+    float4_t o[NT], N[NT];
+    uint4 sp[SP][NT][KS];
 #pragma unroll
-      for (int c = 0; c < NT; ++c) ks[c] = qs[c] = {0, 0, 0, 0};
+    for (int c = 0; c < NT; ++c)
+#pragma unroll
+      for (int s = 0; s < KS; ++s)
+#pragma unroll
+        for (int p = 0; p < SP; ++p) sp[p][c][s] = get(x0, p, KS, s, c);
+#pragma unroll
+    for (int c = 0; c < NT; ++c) {
+#pragma unroll
+      for (int r = 0; r < 4; ++r) N[c][r] = __uint_as_float((uint32_t)va[c][r] << 16);
+      if (DELTA) {
+        float4_t acc[3];
+#pragma unroll
+        for (int p = 0; p < 3; ++p) {
+          acc[p] = {0, 0, 0, 0};
+#pragma unroll
+          for (int s = 0; s < KS; ++s) acc[p] = mfma_bf16(ka[s], sp[p % SP][c][s], acc[p]);
+        }
+        N[c] -= decay * ((acc[2] + acc[1]) + acc[0]);
+        put_rows(y, c, N[c], std::integral_constant<int, 3>());
+      } else {
+        put_rows(y, c, N[c] * left, std::integral_constant<int, 3>());
+        put_rows(y + 6 * NT * 1024, c, N[c], std::integral_constant<int, 1>());
+      }
+    }
+    __syncthreads();
+#pragma unroll
+    for (int c = 0; c < NT; ++c) {
+      float4_t lo = {0, 0, 0, 0};
+      o[c] = {0, 0, 0, 0};
 #pragma unroll
       for (int s = 0; s < KS; ++s) {
-        const uint4 qa = *reinterpret_cast<const uint4*>(qp + s * 8);
-        uint4 ka;
-        if (DELTA) ka = *reinterpret_cast<const uint4*>(kp + s * 8);
-#pragma unroll
-        for (int c = 0; c < NT; ++c) {
-          if (DELTA) {
-#pragma unroll
-            for (int p = 2; p >= 0; --p) ks[c] = mfma_bf16(ka, sp[p][c][s], ks[c]);
-          }
-#pragma unroll
-          for (int p = 1; p >= 0; --p) qs[c] = mfma_bf16(qa, sp[p][c][s], qs[c]);
-        }
+        lo = mfma_bf16(qa[s], sp[1][c][s], lo);
+        o[c] = mfma_bf16(qa[s], sp[0][c][s], o[c]);
       }
-#pragma unroll
-      for (int c = 0; c < NT; ++c)
-#pragma unroll
-        for (int r4 = 0; r4 < 4; ++r4) {
-          const int64_t vr = row0 + min(16 * i + 4 * g + r4, last);
-          const float v = __uint_as_float((uint32_t)a.v[vr * a.ldv + col + 16 * c] << 16);
-          o[c][i][r4] = a.scale * decay[i][r4] * qs[c][r4];
-          N[c][i][r4] = DELTA ? v - decay[i][r4] * ks[c][r4] : v;
-        }
+      o[c] = (o[c] + lo) * (decay * a.scale);
     }
-    if (DELTA) {  // N = T (V - e^G K S)
-#pragma unroll
-      for (int c = 0; c < NT; ++c) {
-        uint4 rp[3][2];
-#pragma unroll
-        for (int s = 0; s < 2; ++s) {
-          uint32_t w[4][3];
-#pragma unroll
-          for (int e = 0; e < 4; ++e) split_pair(N[c][2 * s + e / 2][(e % 2) * 2], N[c][2 * s + e / 2][(e % 2) * 2 + 1], w[e]);
-#pragma unroll
-          for (int p = 0; p < 3; ++p) rp[p][s] = make_uint4(w[0][p], w[1][p], w[2][p], w[3][p]);
-        }
-#pragma unroll
-        for (int i = 0; i < 4; ++i) {
-          float4_t x = {0, 0, 0, 0};
-#pragma unroll
-          for (int s = 0; s <= i / 2; ++s) {
-            uint4 t[3];
-#pragma unroll
-            for (int p = 0; p < 3; ++p)
-              t[p] = *reinterpret_cast<const uint4*>(ws + Slot::kT + (p * kBlocks + block_of(i, s)) * kBlockBytes + lane * 16);
-            x = mfma_bf16(t[2], rp[0][s], x);
-            x = mfma_bf16(t[1], rp[1][s], x);
-            x = mfma_bf16(t[0], rp[2][s], x);
-            x = mfma_bf16(t[1], rp[0][s], x);
-            x = mfma_bf16(t[0], rp[1][s], x);
-            x = mfma_bf16(t[0], rp[0][s], x);
-          }
-          N[c][i] = x;
-        }
-      }
-    }
-    // O += P N and the state's update
-    uint4 np[2][NT][2], up[3][NT][2];
-#pragma unroll
-    for (int c = 0; c < NT; ++c)
-#pragma unroll
-      for (int s = 0; s < 2; ++s) {
-        uint32_t w[4][2], u[4][3];
-#pragma unroll
-        for (int e = 0; e < 4; ++e) {
-          const int i = 2 * s + e / 2, r = (e % 2) * 2;
-          split_pair(N[c][i][r], N[c][i][r + 1], w[e]);
-          split_pair(N[c][i][r] * left[i][r], N[c][i][r + 1] * left[i][r + 1], u[e]);
-        }
-#pragma unroll
-        for (int p = 0; p < 2; ++p) np[p][c][s] = make_uint4(w[0][p], w[1][p], w[2][p], w[3][p]);
-#pragma unroll
-        for (int p = 0; p < 3; ++p) up[p][c][s] = make_uint4(u[0][p], u[1][p], u[2][p], u[3][p]);
-      }
-#pragma unroll
-    for (int i = 0; i < 4; ++i) {
-#pragma unroll
-      for (int s = 0; s <= i / 2; ++s) {
-        uint4 p[2];
-#pragma unroll
-        for (int q = 0; q < 2; ++q)
-          p[q] = *reinterpret_cast<const uint4*>(ws + Slot::kP + (q * kBlocks + block_of(i, s)) * kBlockBytes + lane * 16);
-#pragma unroll
-        for (int c = 0; c < NT; ++c) {
-          o[c][i] = mfma_bf16(p[1], np[0][c][s], o[c][i]);
-          if (DELTA) o[c][i] = mfma_bf16(p[0], np[1][c][s], o[c][i]);  // without it N is bf16 itself
-          o[c][i] = mfma_bf16(p[0], np[0][c][s], o[c][i]);
-        }
-      }
-#pragma unroll
-      for (int c = 0; c < NT; ++c)
-#pragma unroll
-        for (int r = 0; r < 4; ++r)
-          if (16 * i + 4 * g + r <= last)
-            a.out[(row0 + 16 * i + 4 * g + r) * a.ldo + col + 16 * c] = __builtin_bit_cast(uint16_t, (__bf16)o[c][i][r]);
-    }
-#pragma unroll
-    for (int c = 0; c < NT; ++c)
-#pragma unroll
-      for (int i = 0; i < E; ++i) S[c][i] *= whole;
+    const float4_t left_now = left;
+    const float whole_now = whole;
+    fetch_rows(next);
+    // this wave's rows of K^T: TW elements of 8 tokens' rows, transposed within the lane
+    uint4 kt[2][TW];
 #pragma unroll
     for (int s = 0; s < 2; ++s) {
-      uint32_t kt[8][E / 2];  // E elements of the rows of tokens 32 s + 4 g + j and 32 s + 16 + 4 g + j
+      uint32_t z[8];
 #pragma unroll
       for (int j = 0; j < 8; ++j) {
-        const int64_t r = row0 + min(32 * s + (j / 4) * 16 + 4 * g + j % 4, last);
-        const uint16_t* p = a.k + r * a.ldk + hk * DK + n * E;
-        if constexpr (E == 8) {
-          const uint4 x = *reinterpret_cast<const uint4*>(p);
-          kt[j][0] = x.x, kt[j][1] = x.y, kt[j][2] = x.z, kt[j][3] = x.w;
-        } else {
-          const uint2 x = *reinterpret_cast<const uint2*>(p);
-          kt[j][0] = x.x, kt[j][1] = x.y;
-        }
+        const uint8_t* from = keys + (32 * s + (j / 4) * 16 + 4 * g + j % 4) * kKeyRow + (w * (DK / 4) + n * TW) * 2;
+        if constexpr (TW == 2)
+          z[j] = *reinterpret_cast<const uint32_t*>(from);
+        else
+          z[j] = *reinterpret_cast<const uint16_t*>(from);
       }
 #pragma unroll
-      for (int i = 0; i < E; ++i) {
-        uint32_t w[4];
+      for (int i = 0; i < TW; ++i) {
+        uint32_t e[4];
 #pragma unroll
-        for (int e = 0; e < 4; ++e)
-          w[e] = i % 2 ? high_halves(kt[2 * e][i / 2], kt[2 * e + 1][i / 2]) : low_halves(kt[2 * e][i / 2], kt[2 * e + 1][i / 2]);
-        const uint4 ka = make_uint4(w[0], w[1], w[2], w[3]);
-#pragma unroll
-        for (int c = 0; c < NT; ++c)
-#pragma unroll
-          for (int p = 2; p >= 0; --p) S[c][i] = mfma_bf16(ka, up[p][c][s], S[c][i]);
+        for (int j = 0; j < 4; ++j)
+          e[j] = i ? high_halves(z[2 * j], z[2 * j + 1]) : low_halves(z[2 * j], z[2 * j + 1]);
+        kt[s][i] = make_uint4(e[0], e[1], e[2], e[3]);
       }
     }
+    const uint8_t* np = y;
+    if (DELTA) {  // N = T R
+#pragma unroll
+      for (int c = 0; c < NT; ++c) {
+        float4_t acc[2] = {{0, 0, 0, 0}, {0, 0, 0, 0}};
+#pragma unroll
+        for (int s = 0; s < 2; ++s) {
+          if (s >= steps) continue;
+          const uint4 r0 = get(y, 0, 2, s, c), r1 = get(y, 1, 2, s, c), r2 = get(y, 2, 2, s, c);
+          acc[s] = mfma_bf16(ta[s][2], r0, acc[s]);
+          acc[s] = mfma_bf16(ta[s][1], r1, acc[s]);
+          acc[s] = mfma_bf16(ta[s][0], r2, acc[s]);
+          acc[s] = mfma_bf16(ta[s][1], r0, acc[s]);
+          acc[s] = mfma_bf16(ta[s][0], r1, acc[s]);
+          acc[s] = mfma_bf16(ta[s][0], r0, acc[s]);
+        }
+        N[c] = acc[0] + acc[1];
+        put_rows(x0, c, N[c] * left_now, std::integral_constant<int, 3>());
+        put_rows(x0 + 6 * NT * 1024, c, N[c], std::integral_constant<int, 2>());
+      }
+      fetch_t(next);
+      np = x0;
+      __syncthreads();
+    }
+    // S' = e^G S + K^T (e^(G_64 - G) N)
+#pragma unroll
+    for (int c = 0; c < NT; ++c) {
+#pragma unroll
+      for (int i = 0; i < TW; ++i) S[c][i] *= whole_now;
+#pragma unroll
+      for (int s = 0; s < 2; ++s) {
+        const uint4 u0 = get(np, 0, 2, s, c), u1 = get(np, 1, 2, s, c), u2 = get(np, 2, 2, s, c);
+#pragma unroll
+        for (int i = 0; i < TW; ++i) {
+          S[c][i] = mfma_bf16(kt[s][i], u2, S[c][i]);
+          S[c][i] = mfma_bf16(kt[s][i], u1, S[c][i]);
+          S[c][i] = mfma_bf16(kt[s][i], u0, S[c][i]);
+        }
+      }
+    }
+    put_state(x1);
+    // O += P N
+#pragma unroll
+    for (int c = 0; c < NT; ++c) {
+#pragma unroll
+      for (int s = 0; s < 2; ++s) {
+        if (s >= steps) continue;
+        const uint4 n0 = get(np + 6 * NT * 1024, 0, 2, s, c);
+        if (NP == 2) o[c] = mfma_bf16(pa[s][0], get(np + 6 * NT * 1024, NP - 1, 2, s, c), o[c]);
+        o[c] = mfma_bf16(pa[s][1], n0, o[c]);
+        o[c] = mfma_bf16(pa[s][0], n0, o[c]);
+      }
+#pragma unroll
+      for (int r = 0; r < 4; ++r)
+        if (16 * w + 4 * g + r <= last)
+          a.out[(row0 + 16 * w + 4 * g + r) * a.ldo + col + 16 * c] = __builtin_bit_cast(uint16_t, (__bf16)o[c][r]);
+    }
+    fetch_p(next);
+    uint8_t* t = x0;
+    x0 = x1, x1 = t;
+    __syncthreads();
   }
 #pragma unroll
   for (int c = 0; c < NT; ++c)
 #pragma unroll
-    for (int i = 0; i < E; ++i)
+    for (int i = 0; i < TW; ++i)
 #pragma unroll
-      for (int r = 0; r < 4; ++r) st[(int64_t)(r * E + i) * a.v_dim + 16 * c] = S[c][i][r];
+      for (int r = 0; r < 4; ++r) st[(int64_t)(r * TW + i) * a.v_dim + 16 * c] = S[c][i][r];
 }
 
 size_t gdn_prefill_workspace(int64_t T, int64_t B, int, int v_heads, int, int) {
@@ -472,9 +566,9 @@ static hipError_t launch_prefill(const GdnArgs& a, hipStream_t stream) {
   const bool two = pairs * (a.v_dim / 16) > 4 * kCUs;
   const unsigned grid = (unsigned)(pairs * (a.v_dim / (two ? 32 : 16)));
   if (two)
-    gdn_state_kernel<DK, 2, DELTA><<<grid, 64, 0, stream>>>(a);
+    gdn_state_kernel<DK, 2, DELTA><<<grid, 256, 0, stream>>>(a);
   else
-    gdn_state_kernel<DK, 1, DELTA><<<grid, 64, 0, stream>>>(a);
+    gdn_state_kernel<DK, 1, DELTA><<<grid, 256, 0, stream>>>(a);
   return hipGetLastError();
 }
 
