@@ -18,7 +18,6 @@
 // reaches the bf16 output keeps two planes (16 bits).  Sums accumulate in binary32.
 // G is summed in binary64, so that differences of far decays keep their digits.
 #include <algorithm>
-#include <type_traits>
 
 #include "common.hpp"
 #include "mixers.hpp"
@@ -246,54 +245,99 @@ __global__ __launch_bounds__(256) void gdn_chunk_kernel(GdnArgs a) {
 }
 
 // ---- the state from chunk to chunk -----------------------------------------------
-// A workgroup of four waves carries 16 NT columns.  Wave w takes the token rows
-// 16 w .. 16 w + 15 of every product over tokens (K S, Q S, T R, P N) and a quarter of
-// the state's rows, so each left operand is read by one wave only, from global
-// memory into the registers that its last use freed a chunk before.  Right operands
-// -- the planes of S, of R = V - e^G K S and of N -- pass between the waves through LDS
-// in operand order (16 bytes for each lane, no bank conflicts): a product leaves
-// row 4 g + r in register r, which is how the next product's right operand wants
-// its rows, with the left operand's columns taken in that order.  The key rows go
-// through LDS too, for K^T.
+// A workgroup of eight waves carries 16 NT columns: four for the chain from state to
+// state, four for the outputs, which fill the chain's waits on the same SIMDs.  Of
+// each four, wave w takes the token rows 16 w .. 16 w + 15 of the products over tokens (K S,
+// T R; Q S, P N) and a quarter of the state's rows, so each left operand is read by
+// one wave only, from global memory into the registers that its last use freed a
+// chunk before.  Right operands -- the planes of S, of R = V - e^G K S and of N -- pass
+// between the waves through LDS in operand order (16 bytes for each lane, no bank
+// conflicts): a product leaves row 4 g + r in register r, which is how the next
+// product's right operand wants its rows, with the left operand's columns taken in
+// that order.  The key rows go through LDS too, for K^T.
 //
 // LDS, in units of NT KB: S of this chunk and of the next in two areas of 12; N
-// (planes for the state's update, then for the output) over S once every wave has read it; R in
-// 6.  Without beta N is V, known before the chunk, and lies in R's place.
+// (planes for the state's update, then for the output) over S once every wave has
+// read it; R in 6.  Without beta N is V, known before the chunk, and lies in R's place.
 constexpr int kKeyRow = 272;  // bytes of a key row of 128 in LDS: rows 4 apart fall on other banks
 
 template <int DK, int NT, bool DELTA>
 struct StateLds {
   static constexpr int kSteps = DK / 32, kSPlanes = DELTA ? 3 : 2;
-  static constexpr int kS = kSPlanes * kSteps * NT * 1024;      // planes of S
-  static constexpr int kN = (3 + (DELTA ? 2 : 1)) * 2 * NT * 1024;  // planes of e^(G_64 - G) N and of N
+  static constexpr int kS = kSPlanes * kSteps * NT * 1024;          // planes of S
+  static constexpr int kN = (3 + (DELTA ? 2 : 1)) * 2 * NT * 1024;  // planes of e^(G_64 - G) N, then of N
   static constexpr int kX = kS > kN || !DELTA ? kS : kN;
   static constexpr int kY = DELTA ? 3 * 2 * NT * 1024 : kN;
+  static constexpr int kOut = 6 * NT * 1024;  // of N for the output in kN
   static constexpr int kKeys = 2 * kX + kY, kBytes = kKeys + kChunk * kKeyRow;
 };
 
+// What both halves of the workgroup share.
 template <int DK, int NT, bool DELTA>
-__global__ __launch_bounds__(256, 1) void gdn_state_kernel(GdnArgs a) {
+struct StateWave {
   using L = StateLds<DK, NT, DELTA>;
-  constexpr int KS = L::kSteps, TW = DK / 64, SP = L::kSPlanes, NP = DELTA ? 2 : 1;
-  __shared__ __align__(16) uint8_t lds[L::kBytes];
-  const int slabs = a.v_dim / (16 * NT);
-  // slabs of a head run on one XCD (workgroups go round the eight in turn) and share its L2
-  const int64_t turn = blockIdx.x / 8;
-  const int64_t pair = (turn / slabs) * 8 + blockIdx.x % 8;
-  const int slab = (int)(turn % slabs);
-  if (pair >= a.B * a.v_heads) return;
-  const int b = (int)(pair / a.v_heads), h = (int)(pair % a.v_heads), hk = h / (a.v_heads / a.k_heads);
-  const int64_t slot = a.index ? a.index[b] : b;
-  if (slot < 0 || slot >= a.num_states) return;
-  const int lane = threadIdx.x % 64, n = lane % 16, g = lane / 16;
-  const int w = __builtin_amdgcn_readfirstlane(threadIdx.x / 64);
-  const Rows rows = rows_of(a, b);
-  const int chunks = (rows.count + kChunk - 1) / kChunk;
+  static constexpr int TW = DK / 64, KS = DK / 32;
+  const GdnArgs& a;
+  uint8_t* lds;
+  int64_t first;     // row of the sequence's first token
+  int count, chunks; // its tokens and chunks
+  int hk, col;       // key head; lane's column of a row of v and out
+  const uint8_t* ws; // the first chunk's slot
+  int64_t ws_step;
+  int w, lane, n, g;
 
-  // state rows of this wave: tile i, register r holds row w DK / 4 + (4 g + r) TW + i, column n
-  float* st = a.state + ((slot * a.v_heads + h) * DK + w * (DK / 4) + 4 * g * TW) * (int64_t)a.v_dim + slab * 16 * NT + n;
+  __device__ __forceinline__ int last_of(int ch) const { return min(kChunk, count - ch * kChunk) - 1; }
+  __device__ __forceinline__ uint4 get(const uint8_t* x, int p, int per, int s, int c) const {
+    return *reinterpret_cast<const uint4*>(x + ((p * per + s) * NT + c) * 1024 + lane * 16);
+  }
+  // 8 elements of step s of a q or k row, in the order of the state's planes
+  __device__ __forceinline__ uint4 run(const uint16_t* row, int s) const {
+    if constexpr (TW == 2) return *reinterpret_cast<const uint4*>(row + 32 * s + 8 * g);
+    const uint2 x = *reinterpret_cast<const uint2*>(row + 32 * s + 4 * g);
+    const uint2 y = *reinterpret_cast<const uint2*>(row + 32 * s + 16 + 4 * g);
+    return make_uint4(x.x, x.y, y.x, y.y);
+  }
+  // block (w, s) of a matrix's plane in chunk ch's slot
+  __device__ __forceinline__ uint4 block(int ch, int at, int p, int s) const {
+    return *reinterpret_cast<const uint4*>(ws + ch * ws_step + at + (p * kBlocks + block_of(w, s)) * kBlockBytes + lane * 16);
+  }
+  // four rows of this wave as P planes at x
+  template <int P>
+  __device__ __forceinline__ void put_rows(uint8_t* x, int c, float4_t v) const {
+    uint32_t z[2][P];
+    split_pair(v[0], v[1], z[0]);
+    split_pair(v[2], v[3], z[1]);
+#pragma unroll
+    for (int p = 0; p < P; ++p)
+      *reinterpret_cast<uint2*>(x + ((p * 2 + w / 2) * NT + c) * 1024 + lane * 16 + (w % 2) * 8) =
+          make_uint2(z[0][p], z[1][p]);
+  }
+};
+
+// Rows of a tensor that a lane reads in chunk after chunk: N pointers, moved on by a
+// chunk's rows; the sequence's last chunk, when partial, clamps to its last row.
+template <int N, typename T>
+struct RowPointers {
+  T* p[N];
+  __device__ __forceinline__ void at(T* base, int64_t row0, int64_t ld, int first, int last) {
+#pragma unroll
+    for (int j = 0; j < N; ++j) p[j] = base + (row0 + min(first + j, last)) * ld;
+  }
+  __device__ __forceinline__ void on(int64_t step) {
+#pragma unroll
+    for (int j = 0; j < N; ++j) p[j] += step;
+  }
+};
+
+template <int DK, int NT, bool DELTA>
+__device__ __forceinline__ void carry_state(const StateWave<DK, NT, DELTA>& m, float* st, bool load) {
+  using L = StateLds<DK, NT, DELTA>;
+  constexpr int KS = DK / 32, TW = DK / 64, SP = L::kSPlanes;
+  const GdnArgs& a = m.a;
+  const int w = m.w, n = m.n, g = m.g, lane = m.lane, chunks = m.chunks;
+  const int steps = w / 2 + 1;  // 32-token steps that rows 16 w .. reach in a lower triangle
+  // tile i, register r: state row w DK / 4 + (4 g + r) TW + i
   float4_t S[NT][TW];
-  const bool load = a.has_state && a.has_state[b] != 0;
 #pragma unroll
   for (int c = 0; c < NT; ++c)
 #pragma unroll
@@ -301,61 +345,10 @@ __global__ __launch_bounds__(256, 1) void gdn_state_kernel(GdnArgs a) {
 #pragma unroll
       for (int r = 0; r < 4; ++r) S[c][i][r] = load ? st[(int64_t)(r * TW + i) * a.v_dim + 16 * c] : 0.0f;
 
-  const uint8_t* ws = static_cast<const uint8_t*>(a.workspace) +
-                      ((rows.first / kChunk + b) * a.v_heads + h) *
-                          (int64_t)(DELTA ? Slot::kBytesDelta : Slot::kBytesLinear);
-  const int64_t ws_step = (int64_t)a.v_heads * (DELTA ? Slot::kBytesDelta : Slot::kBytesLinear);
-  const int col = h * a.v_dim + slab * 16 * NT + n;
-  const int steps = w / 2 + 1;  // 32-token steps that rows 16 w .. reach in a lower triangle
-
-  // left operands in flight
-  uint4 ka[KS], qa[KS], ta[2][3], pa[2][2];
-  uint16_t va[NT][4];
-  float4_t decay, left;
-  float whole;
-  auto key_run = [&](const uint16_t* row, int s) {  // the order of the state's planes
-    if constexpr (TW == 2) return *reinterpret_cast<const uint4*>(row + 32 * s + 8 * g);
-    const uint2 x = *reinterpret_cast<const uint2*>(row + 32 * s + 4 * g);
-    const uint2 y = *reinterpret_cast<const uint2*>(row + 32 * s + 16 + 4 * g);
-    return make_uint4(x.x, x.y, y.x, y.y);
-  };
-  auto fetch_rows = [&](int ch) {  // K, Q, V and the decays of a chunk
-    const int64_t row0 = rows.first + (int64_t)ch * kChunk;
-    const int last = min(kChunk, rows.count - ch * kChunk) - 1;
-    const int64_t r = row0 + min(16 * w + n, last);
-#pragma unroll
-    for (int s = 0; s < KS; ++s) {
-      ka[s] = key_run(a.k + r * a.ldk + hk * DK, s);
-      qa[s] = key_run(a.q + r * a.ldq + hk * DK, s);
-    }
-    const uint8_t* p = ws + ch * ws_step;
-    decay = *reinterpret_cast<const float4_t*>(p + Slot::kDecay + (16 * w + 4 * g) * 4);
-    left = *reinterpret_cast<const float4_t*>(p + Slot::kLeft + (16 * w + 4 * g) * 4);
-    whole = *reinterpret_cast<const float*>(p + Slot::kDecay + 63 * 4);
-#pragma unroll
-    for (int c = 0; c < NT; ++c)
-#pragma unroll
-      for (int j = 0; j < 4; ++j) va[c][j] = a.v[(row0 + min(16 * w + 4 * g + j, last)) * a.ldv + col + 16 * c];
-  };
-  auto fetch_t = [&](int ch) {
-#pragma unroll
-    for (int s = 0; s < 2; ++s)
-#pragma unroll
-      for (int p = 0; p < 3; ++p)
-        if (s < steps)
-          ta[s][p] = *reinterpret_cast<const uint4*>(ws + ch * ws_step + Slot::kT +
-                                                     (p * kBlocks + block_of(w, s)) * kBlockBytes + lane * 16);
-  };
-  auto fetch_p = [&](int ch) {
-#pragma unroll
-    for (int s = 0; s < 2; ++s)
-#pragma unroll
-      for (int p = 0; p < 2; ++p)
-        if (s < steps)
-          pa[s][p] = *reinterpret_cast<const uint4*>(ws + ch * ws_step + Slot::kP +
-                                                     (p * kBlocks + block_of(w, s)) * kBlockBytes + lane * 16);
-  };
-  // this wave's rows of S as right-operand planes
+  uint8_t* x0 = m.lds;
+  uint8_t* x1 = m.lds + L::kX;
+  uint8_t* y = m.lds + 2 * L::kX;
+  uint8_t* keys = m.lds + L::kKeys;
   auto put_state = [&](uint8_t* x) {
 #pragma unroll
     for (int c = 0; c < NT; ++c) {
@@ -376,35 +369,45 @@ __global__ __launch_bounds__(256, 1) void gdn_state_kernel(GdnArgs a) {
       }
     }
   };
-  // four rows of this wave as P planes at x
-  auto put_rows = [&](uint8_t* x, int c, float4_t v, auto planes) {
-    constexpr int P = decltype(planes)::value;
-    uint32_t z[2][P];
-    split_pair(v[0], v[1], z[0]);
-    split_pair(v[2], v[3], z[1]);
+  // left operands in flight
+  RowPointers<1, const uint16_t> kp;
+  RowPointers<4, const uint16_t> vp;
+  uint4 ka[KS], ta[2][3];
+  uint16_t va[NT][4];
+  float4_t decay, left;
+  float whole;
+  auto point = [&](int ch) {
+    const int64_t row0 = m.first + (int64_t)ch * kChunk;
+    kp.at(a.k + m.hk * DK, row0, a.ldk, 16 * w + n, m.last_of(ch));
+    vp.at(a.v + m.col, row0, a.ldv, 16 * w + 4 * g, m.last_of(ch));
+  };
+  auto fetch_rows = [&](int ch) {
 #pragma unroll
-    for (int p = 0; p < P; ++p)
-      *reinterpret_cast<uint2*>(x + ((p * 2 + w / 2) * NT + c) * 1024 + lane * 16 + (w % 2) * 8) =
-          make_uint2(z[0][p], z[1][p]);
+    for (int s = 0; s < KS; ++s) ka[s] = m.run(kp.p[0], s);
+    const uint8_t* p = m.ws + ch * m.ws_step;
+    decay = *reinterpret_cast<const float4_t*>(p + Slot::kDecay + (16 * w + 4 * g) * 4);
+    left = *reinterpret_cast<const float4_t*>(p + Slot::kLeft + (16 * w + 4 * g) * 4);
+    whole = *reinterpret_cast<const float*>(p + Slot::kDecay + 63 * 4);
+#pragma unroll
+    for (int c = 0; c < NT; ++c)
+#pragma unroll
+      for (int j = 0; j < 4; ++j) va[c][j] = vp.p[j][16 * c];
   };
-  auto get = [&](const uint8_t* x, int p, int per, int s, int c) {
-    return *reinterpret_cast<const uint4*>(x + ((p * per + s) * NT + c) * 1024 + lane * 16);
+  auto fetch_t = [&](int ch) {
+#pragma unroll
+    for (int s = 0; s < 2; ++s)
+#pragma unroll
+      for (int p = 0; p < 3; ++p)
+        if (s < steps) ta[s][p] = m.block(ch, Slot::kT, p, s);
   };
-
-  uint8_t* x0 = lds;
-  uint8_t* x1 = lds + L::kX;
-  uint8_t* y = lds + 2 * L::kX;
-  uint8_t* keys = lds + L::kKeys;
   if (chunks > 0) {
+    point(0);
     fetch_rows(0);
     if (DELTA) fetch_t(0);
-    fetch_p(0);
     put_state(x0);
     __syncthreads();
   }
   for (int ch = 0; ch < chunks; ++ch) {
-    const int64_t row0 = rows.first + (int64_t)ch * kChunk;
-    const int last = min(kChunk, rows.count - ch * kChunk) - 1;
     const int next = min(ch + 1, chunks - 1);
     // key rows for K^T
 #pragma unroll
@@ -417,47 +420,32 @@ __global__ __launch_bounds__(256, 1) void gdn_state_kernel(GdnArgs a) {
         *reinterpret_cast<uint2*>(to + 64 * s + 32 + 8 * g) = make_uint2(ka[s].z, ka[s].w);
       }
     }
-    float4_t o[NT], N[NT];
-    uint4 sp[SP][NT][KS];
-#pragma unroll
-    for (int c = 0; c < NT; ++c)
-#pragma unroll
-      for (int s = 0; s < KS; ++s)
-#pragma unroll
-        for (int p = 0; p < SP; ++p) sp[p][c][s] = get(x0, p, KS, s, c);
+    float4_t N[NT];
 #pragma unroll
     for (int c = 0; c < NT; ++c) {
 #pragma unroll
       for (int r = 0; r < 4; ++r) N[c][r] = __uint_as_float((uint32_t)va[c][r] << 16);
       if (DELTA) {
-        float4_t acc[3];
+        float4_t acc[3] = {{0, 0, 0, 0}, {0, 0, 0, 0}, {0, 0, 0, 0}};
 #pragma unroll
-        for (int p = 0; p < 3; ++p) {
-          acc[p] = {0, 0, 0, 0};
+        for (int s = 0; s < KS; ++s)
 #pragma unroll
-          for (int s = 0; s < KS; ++s) acc[p] = mfma_bf16(ka[s], sp[p % SP][c][s], acc[p]);
-        }
+          for (int p = 0; p < 3; ++p) acc[p] = mfma_bf16(ka[s], m.get(x0, p % SP, KS, s, c), acc[p]);
         N[c] -= decay * ((acc[2] + acc[1]) + acc[0]);
-        put_rows(y, c, N[c], std::integral_constant<int, 3>());
+        m.template put_rows<3>(y, c, N[c]);
       } else {
-        put_rows(y, c, N[c] * left, std::integral_constant<int, 3>());
-        put_rows(y + 6 * NT * 1024, c, N[c], std::integral_constant<int, 1>());
+        m.template put_rows<3>(y, c, N[c] * left);
+        m.template put_rows<1>(y + L::kOut, c, N[c]);
       }
     }
     __syncthreads();
-#pragma unroll
-    for (int c = 0; c < NT; ++c) {
-      float4_t lo = {0, 0, 0, 0};
-      o[c] = {0, 0, 0, 0};
-#pragma unroll
-      for (int s = 0; s < KS; ++s) {
-        lo = mfma_bf16(qa[s], sp[1][c][s], lo);
-        o[c] = mfma_bf16(qa[s], sp[0][c][s], o[c]);
-      }
-      o[c] = (o[c] + lo) * (decay * a.scale);
-    }
     const float4_t left_now = left;
     const float whole_now = whole;
+    if (m.last_of(next) == kChunk - 1) {
+      if (next > ch) kp.on(a.ldk * kChunk), vp.on(a.ldv * kChunk);
+    } else {
+      point(next);
+    }
     fetch_rows(next);
     // this wave's rows of K^T: TW elements of 8 tokens' rows, transposed within the lane
     uint4 kt[2][TW];
@@ -485,21 +473,21 @@ __global__ __launch_bounds__(256, 1) void gdn_state_kernel(GdnArgs a) {
     if (DELTA) {  // N = T R
 #pragma unroll
       for (int c = 0; c < NT; ++c) {
-        float4_t acc[2] = {{0, 0, 0, 0}, {0, 0, 0, 0}};
+        float4_t acc[3] = {{0, 0, 0, 0}, {0, 0, 0, 0}, {0, 0, 0, 0}};
 #pragma unroll
         for (int s = 0; s < 2; ++s) {
           if (s >= steps) continue;
-          const uint4 r0 = get(y, 0, 2, s, c), r1 = get(y, 1, 2, s, c), r2 = get(y, 2, 2, s, c);
-          acc[s] = mfma_bf16(ta[s][2], r0, acc[s]);
-          acc[s] = mfma_bf16(ta[s][1], r1, acc[s]);
-          acc[s] = mfma_bf16(ta[s][0], r2, acc[s]);
-          acc[s] = mfma_bf16(ta[s][1], r0, acc[s]);
-          acc[s] = mfma_bf16(ta[s][0], r1, acc[s]);
-          acc[s] = mfma_bf16(ta[s][0], r0, acc[s]);
+          const uint4 r0 = m.get(y, 0, 2, s, c), r1 = m.get(y, 1, 2, s, c), r2 = m.get(y, 2, 2, s, c);
+          acc[0] = mfma_bf16(ta[s][0], r0, acc[0]);
+          acc[1] = mfma_bf16(ta[s][1], r0, acc[1]);
+          acc[2] = mfma_bf16(ta[s][2], r0, acc[2]);
+          acc[1] = mfma_bf16(ta[s][0], r1, acc[1]);
+          acc[2] = mfma_bf16(ta[s][1], r1, acc[2]);
+          acc[2] = mfma_bf16(ta[s][0], r2, acc[2]);
         }
-        N[c] = acc[0] + acc[1];
-        put_rows(x0, c, N[c] * left_now, std::integral_constant<int, 3>());
-        put_rows(x0 + 6 * NT * 1024, c, N[c], std::integral_constant<int, 2>());
+        N[c] = (acc[2] + acc[1]) + acc[0];
+        m.template put_rows<3>(x0, c, N[c] * left_now);
+        m.template put_rows<2>(x0 + L::kOut, c, N[c]);
       }
       fetch_t(next);
       np = x0;
@@ -511,34 +499,15 @@ __global__ __launch_bounds__(256, 1) void gdn_state_kernel(GdnArgs a) {
 #pragma unroll
       for (int i = 0; i < TW; ++i) S[c][i] *= whole_now;
 #pragma unroll
-      for (int s = 0; s < 2; ++s) {
-        const uint4 u0 = get(np, 0, 2, s, c), u1 = get(np, 1, 2, s, c), u2 = get(np, 2, 2, s, c);
+      for (int s = 0; s < 2; ++s)
 #pragma unroll
-        for (int i = 0; i < TW; ++i) {
-          S[c][i] = mfma_bf16(kt[s][i], u2, S[c][i]);
-          S[c][i] = mfma_bf16(kt[s][i], u1, S[c][i]);
-          S[c][i] = mfma_bf16(kt[s][i], u0, S[c][i]);
+        for (int p = 2; p >= 0; --p) {
+          const uint4 u = m.get(np, p, 2, s, c);
+#pragma unroll
+          for (int i = 0; i < TW; ++i) S[c][i] = mfma_bf16(kt[s][i], u, S[c][i]);
         }
-      }
     }
     put_state(x1);
-    // O += P N
-#pragma unroll
-    for (int c = 0; c < NT; ++c) {
-#pragma unroll
-      for (int s = 0; s < 2; ++s) {
-        if (s >= steps) continue;
-        const uint4 n0 = get(np + 6 * NT * 1024, 0, 2, s, c);
-        if (NP == 2) o[c] = mfma_bf16(pa[s][0], get(np + 6 * NT * 1024, NP - 1, 2, s, c), o[c]);
-        o[c] = mfma_bf16(pa[s][1], n0, o[c]);
-        o[c] = mfma_bf16(pa[s][0], n0, o[c]);
-      }
-#pragma unroll
-      for (int r = 0; r < 4; ++r)
-        if (16 * w + 4 * g + r <= last)
-          a.out[(row0 + 16 * w + 4 * g + r) * a.ldo + col + 16 * c] = __builtin_bit_cast(uint16_t, (__bf16)o[c][r]);
-    }
-    fetch_p(next);
     uint8_t* t = x0;
     x0 = x1, x1 = t;
     __syncthreads();
@@ -549,6 +518,135 @@ __global__ __launch_bounds__(256, 1) void gdn_state_kernel(GdnArgs a) {
     for (int i = 0; i < TW; ++i)
 #pragma unroll
       for (int r = 0; r < 4; ++r) st[(int64_t)(r * TW + i) * a.v_dim + 16 * c] = S[c][i][r];
+}
+
+template <int DK, int NT, bool DELTA>
+__device__ __forceinline__ void write_outputs(const StateWave<DK, NT, DELTA>& m) {
+  using L = StateLds<DK, NT, DELTA>;
+  constexpr int KS = DK / 32;
+  const GdnArgs& a = m.a;
+  const int w = m.w, n = m.n, g = m.g, chunks = m.chunks;
+  const int steps = w / 2 + 1;
+  const uint8_t* x0 = m.lds;
+  const uint8_t* x1 = m.lds + L::kX;
+  const uint8_t* y = m.lds + 2 * L::kX;
+  RowPointers<1, const uint16_t> qp;
+  RowPointers<4, uint16_t> op;
+  uint4 qa[KS], pa[2][2];
+  float4_t decay;
+  auto point = [&](int ch) {
+    qp.at(a.q + m.hk * DK, m.first + (int64_t)ch * kChunk, a.ldq, 16 * w + n, m.last_of(ch));
+  };
+  auto fetch_q = [&](int ch) {
+#pragma unroll
+    for (int s = 0; s < KS; ++s) qa[s] = m.run(qp.p[0], s);
+    decay = *reinterpret_cast<const float4_t*>(m.ws + ch * m.ws_step + Slot::kDecay + (16 * w + 4 * g) * 4);
+  };
+  auto fetch_p = [&](int ch) {
+#pragma unroll
+    for (int s = 0; s < 2; ++s)
+#pragma unroll
+      for (int p = 0; p < 2; ++p)
+        if (s < steps) pa[s][p] = m.block(ch, Slot::kP, p, s);
+  };
+  if (chunks > 0) {
+    point(0);
+    op.at(a.out + m.col, m.first, a.ldo, 16 * w + 4 * g, kChunk);
+    fetch_q(0);
+    fetch_p(0);
+    __syncthreads();
+  }
+  for (int ch = 0; ch < chunks; ++ch) {
+    const int next = min(ch + 1, chunks - 1), last = m.last_of(ch);
+    uint4 sp[2][NT][KS];
+#pragma unroll
+    for (int c = 0; c < NT; ++c)
+#pragma unroll
+      for (int s = 0; s < KS; ++s)
+#pragma unroll
+        for (int p = 0; p < 2; ++p) sp[p][c][s] = m.get(x0, p, KS, s, c);
+    __syncthreads();
+    float4_t o[NT];
+#pragma unroll
+    for (int c = 0; c < NT; ++c) {
+      float4_t lo = {0, 0, 0, 0};
+      o[c] = {0, 0, 0, 0};
+#pragma unroll
+      for (int s = 0; s < KS; ++s) {
+        o[c] = mfma_bf16(qa[s], sp[0][c][s], o[c]);
+        lo = mfma_bf16(qa[s], sp[1][c][s], lo);
+      }
+      o[c] = (o[c] + lo) * (decay * a.scale);
+    }
+    if (m.last_of(next) == kChunk - 1) {
+      if (next > ch) qp.on(a.ldq * kChunk);
+    } else {
+      point(next);
+    }
+    fetch_q(next);
+    if (DELTA) __syncthreads();
+    const uint8_t* np = (DELTA ? x0 : y) + L::kOut;
+#pragma unroll
+    for (int c = 0; c < NT; ++c) {
+      float4_t lo = {0, 0, 0, 0};
+#pragma unroll
+      for (int s = 0; s < 2; ++s) {
+        if (s >= steps) continue;
+        const uint4 n0 = m.get(np, 0, 2, s, c);
+        o[c] = mfma_bf16(pa[s][0], n0, o[c]);
+        lo = mfma_bf16(pa[s][1], n0, lo);
+        if (DELTA) lo = mfma_bf16(pa[s][0], m.get(np, 1, 2, s, c), lo);
+      }
+      o[c] += lo;
+    }
+    fetch_p(next);
+    if (last == kChunk - 1) {
+#pragma unroll
+      for (int c = 0; c < NT; ++c)
+#pragma unroll
+        for (int r = 0; r < 4; ++r) op.p[r][16 * c] = __builtin_bit_cast(uint16_t, (__bf16)o[c][r]);
+    } else {
+#pragma unroll
+      for (int c = 0; c < NT; ++c)
+#pragma unroll
+        for (int r = 0; r < 4; ++r)
+          if (16 * w + 4 * g + r <= last) op.p[r][16 * c] = __builtin_bit_cast(uint16_t, (__bf16)o[c][r]);
+    }
+    op.on(a.ldo * kChunk);
+    const uint8_t* t = x0;
+    x0 = x1, x1 = t;
+    __syncthreads();
+  }
+}
+
+template <int DK, int NT, bool DELTA>
+__global__ __launch_bounds__(512, 2) void gdn_state_kernel(GdnArgs a) {
+  using L = StateLds<DK, NT, DELTA>;
+  __shared__ __align__(16) uint8_t lds[L::kBytes];
+  const int slabs = a.v_dim / (16 * NT);
+  // slabs of a head run on one XCD (workgroups go round the eight in turn) and share its L2
+  const int64_t turn = blockIdx.x / 8;
+  const int64_t pair = (turn / slabs) * 8 + blockIdx.x % 8;
+  const int slab = (int)(turn % slabs);
+  if (pair >= a.B * a.v_heads) return;
+  const int b = (int)(pair / a.v_heads), h = (int)(pair % a.v_heads);
+  const int64_t slot = a.index ? a.index[b] : b;
+  if (slot < 0 || slot >= a.num_states) return;
+  const int lane = threadIdx.x % 64, n = lane % 16, g = lane / 16;
+  const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x / 64), w = wave % 4;
+  const Rows rows = rows_of(a, b);
+  const int64_t step = (int64_t)a.v_heads * (DELTA ? Slot::kBytesDelta : Slot::kBytesLinear);
+  const uint8_t* ws = static_cast<const uint8_t*>(a.workspace) + (rows.first / kChunk + b) * step +
+                      h * (int64_t)(DELTA ? Slot::kBytesDelta : Slot::kBytesLinear);
+  const StateWave<DK, NT, DELTA> m{a, lds, rows.first, rows.count, (rows.count + kChunk - 1) / kChunk,
+                                   h / (a.v_heads / a.k_heads), h * a.v_dim + slab * 16 * NT + n, ws, step, w, lane, n, g};
+  // both halves pass the same barriers: one before the chunks and three (two without beta) in each
+  if (wave < 4)
+    carry_state<DK, NT, DELTA>(m, a.state + ((slot * a.v_heads + h) * DK + w * (DK / 4) + 4 * g * (DK / 64)) * (int64_t)a.v_dim +
+                                      slab * 16 * NT + n,
+                               a.has_state && a.has_state[b] != 0);
+  else
+    write_outputs<DK, NT, DELTA>(m);
 }
 
 size_t gdn_prefill_workspace(int64_t T, int64_t B, int, int v_heads, int, int) {
@@ -566,9 +664,9 @@ static hipError_t launch_prefill(const GdnArgs& a, hipStream_t stream) {
   const bool two = pairs * (a.v_dim / 16) > 4 * kCUs;
   const unsigned grid = (unsigned)(pairs * (a.v_dim / (two ? 32 : 16)));
   if (two)
-    gdn_state_kernel<DK, 2, DELTA><<<grid, 256, 0, stream>>>(a);
+    gdn_state_kernel<DK, 2, DELTA><<<grid, 512, 0, stream>>>(a);
   else
-    gdn_state_kernel<DK, 1, DELTA><<<grid, 256, 0, stream>>>(a);
+    gdn_state_kernel<DK, 1, DELTA><<<grid, 512, 0, stream>>>(a);
   return hipGetLastError();
 }
 
