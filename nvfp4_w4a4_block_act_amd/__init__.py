@@ -285,8 +285,8 @@ def nvfp4_read_probe(buf, nbytes, workgroups, sink, stream=None):
 def nvfp4_kv_append(q, k, v, src_dtype, T, q_heads, ldq, ldk, ldv, rope, rot_dim, max_pos, interleaved, positions, slots,
                     cache, q_out, ldqo, stream=None):
     """``cache`` is a KVCacheDesc."""
-    _check(_lib().nvfp4_kv_append(_ptr(q), _ptr(k), _ptr(v), src_dtype, T, q_heads, ldq, ldk, ldv, _ptr(rope), rot_dim,
-                                  max_pos, interleaved, _ptr(positions), _ptr(slots), ctypes.byref(cache), _ptr(q_out),
+    _check(_lib().nvfp4_kv_append(_ptr(q), k.data_ptr(), v.data_ptr(), src_dtype, T, q_heads, ldq, ldk, ldv, _ptr(rope), rot_dim,
+                                  max_pos, interleaved, _ptr(positions), slots.data_ptr(), ctypes.byref(cache), _ptr(q_out),
                                   ldqo, _stream(stream)), "nvfp4_kv_append")
 
 
@@ -297,15 +297,15 @@ def nvfp4_attn_decode_workspace_bytes(B, q_heads, kv_heads, head_dim, max_len, w
 def nvfp4_attn_decode(q, B, q_heads, ldq, cache, block_table, ldt, seq_lens, max_len, scale, window, out, ldo, lse,
                       workspace, workspace_bytes, stream=None):
     """``cache`` is a KVCacheDesc."""
-    _check(_lib().nvfp4_attn_decode(_ptr(q), B, q_heads, ldq, ctypes.byref(cache), _ptr(block_table), ldt,
-                                    _ptr(seq_lens), max_len, scale, window, _ptr(out), ldo, _ptr(lse), _ptr(workspace),
+    _check(_lib().nvfp4_attn_decode(q.data_ptr(), B, q_heads, ldq, ctypes.byref(cache), block_table.data_ptr(), ldt,
+                                    seq_lens.data_ptr(), max_len, scale, window, out.data_ptr(), ldo, _ptr(lse), _ptr(workspace),
                                     workspace_bytes, _stream(stream)), "nvfp4_attn_decode")
 
 
 def nvfp4_gdn_step(q, ldq, k, ldk, v, ldv, g, ldg, beta, ldb, B, k_heads, v_heads, k_dim, v_dim, state, num_states,
                    state_index, scale, out, ldo, stream=None):
-    _check(_lib().nvfp4_gdn_step(_ptr(q), ldq, _ptr(k), ldk, _ptr(v), ldv, _ptr(g), ldg, _ptr(beta), ldb, B, k_heads,
-                                 v_heads, k_dim, v_dim, _ptr(state), num_states, _ptr(state_index), scale, _ptr(out),
+    _check(_lib().nvfp4_gdn_step(q.data_ptr(), ldq, k.data_ptr(), ldk, v.data_ptr(), ldv, g.data_ptr(), ldg, _ptr(beta), ldb, B, k_heads,
+                                 v_heads, k_dim, v_dim, state.data_ptr(), num_states, _ptr(state_index), scale, out.data_ptr(),
                                  ldo, _stream(stream)), "nvfp4_gdn_step")
 
 
@@ -316,9 +316,9 @@ def nvfp4_gdn_prefill_workspace_bytes(T, B, k_heads, v_heads, k_dim, v_dim):
 def nvfp4_gdn_prefill(q, ldq, k, ldk, v, ldv, g, ldg, beta, ldb, T, B, cu_seqlens, k_heads, v_heads, k_dim, v_dim,
                       state, num_states, state_index, has_state, scale, out, ldo, workspace, workspace_bytes,
                       stream=None):
-    _check(_lib().nvfp4_gdn_prefill(_ptr(q), ldq, _ptr(k), ldk, _ptr(v), ldv, _ptr(g), ldg, _ptr(beta), ldb, T, B,
-                                    _ptr(cu_seqlens), k_heads, v_heads, k_dim, v_dim, _ptr(state), num_states,
-                                    _ptr(state_index), _ptr(has_state), scale, _ptr(out), ldo, _ptr(workspace),
+    _check(_lib().nvfp4_gdn_prefill(q.data_ptr(), ldq, k.data_ptr(), ldk, v.data_ptr(), ldv, g.data_ptr(), ldg, _ptr(beta), ldb, T, B,
+                                    cu_seqlens.data_ptr(), k_heads, v_heads, k_dim, v_dim, state.data_ptr(), num_states,
+                                    _ptr(state_index), _ptr(has_state), scale, out.data_ptr(), ldo, _ptr(workspace),
                                     workspace_bytes, _stream(stream)), "nvfp4_gdn_prefill")
 
 
@@ -546,14 +546,21 @@ def quantize_stats(x, amax, *, stream=None):
 
 
 # ---- token mixers: paged cache, decode attention, gated linear attention ----------------
+# A GPU's current hipStream_t as an integer, without the Stream object that
+# torch.cuda.current_stream builds (2.8 us of a call whose kernels take 4).
+_current_stream = getattr(torch._C, "_cuda_getCurrentRawStream",
+                          lambda dev: torch.cuda.current_stream(dev).cuda_stream)
+
+
 def _on_device(fn):
     """For the mixers: runs a function with its first tensor's GPU current, on that
     GPU's current stream or on ``stream`` (keyword-only, a torch.cuda.Stream of it), and
     allocates there (see _on_stream)."""
     @functools.wraps(fn)
     def wrapper(first, *args, stream=None, **kw):
-        if stream is None and first.get_device() == torch.cuda.current_device():
-            return fn(first, *args, stream=None, **kw)
+        dev = first.get_device()
+        if stream is None and dev == torch.cuda.current_device():
+            return fn(first, *args, stream=_current_stream(dev), **kw)
         if stream is not None and not isinstance(stream, torch.cuda.Stream):
             raise TypeError(f"{fn.__name__}: stream must be a torch.cuda.Stream "
                             "(the nvfp4_* wrappers take raw handles)")
@@ -561,7 +568,7 @@ def _on_device(fn):
         assert stream is None or stream.device == first.device, f"{fn.__name__}: the stream is another GPU's"
         with torch.cuda.device(first.device):
             if stream is None:
-                return fn(first, *args, stream=None, **kw)
+                return fn(first, *args, stream=_current_stream(dev), **kw)
             with torch.cuda.stream(stream):
                 return fn(first, *args, stream=stream.cuda_stream, **kw)
     return wrapper
@@ -569,25 +576,26 @@ def _on_device(fn):
 
 def _rows3(x, dev, dtype, T, H, D, what):
     """Checks a [T, H, D] tensor whose heads lie next to each other; its token stride."""
-    assert x.dtype == dtype and x.shape == (T, H, D) and x.get_device() == dev, what
-    if T == 0:
-        return H * D
-    s = x.stride()
-    assert s[2] == 1 and (s[1] == D or H == 1), f"{what}: a token's heads must be contiguous"
-    return s[0] if T > 1 else max(s[0], H * D)
+    assert x.dtype is dtype and x.shape == (T, H, D) and x.get_device() == dev, what
+    s0, s1, s2 = x.stride()
+    if T > 1:
+        assert s2 == 1 and (s1 == D or H == 1), f"{what}: a token's heads must be contiguous"
+        return s0
+    assert T == 0 or (s2 == 1 and (s1 == D or H == 1)), f"{what}: a token's heads must be contiguous"
+    return H * D                                     # one row: any stride will do
 
 
 def _rows2(x, dev, T, H, what):
     """Checks an fp32 [T, H] tensor; its token stride."""
-    assert x.dtype == torch.float32 and x.shape == (T, H) and x.get_device() == dev, what
-    s = x.stride()
-    assert s[1] == 1 or H == 1 or T == 0, f"{what}: a token's values must be contiguous"
-    return s[0] if T > 1 else max(s[0], H)
+    assert x.dtype is torch.float32 and x.shape == (T, H) and x.get_device() == dev, what
+    s0, s1 = x.stride()
+    assert s1 == 1 or H == 1 or T == 0, f"{what}: a token's values must be contiguous"
+    return s0 if T > 1 else H
 
 
 def _table(x, dev, dtype, n, what):
     if x is not None:
-        assert x.dtype == dtype and x.shape == (n,) and x.get_device() == dev and x.is_contiguous(), what
+        assert x.dtype is dtype and x.shape == (n,) and x.get_device() == dev and (n <= 1 or x.stride(0) == 1), what
     return x
 
 

@@ -42,19 +42,18 @@ typedef float f32x2_t __attribute__((ext_vector_type(2)));
 constexpr float kNone = -3.402823466e38f;  // reference before any token: finite, so that differences are numbers
 constexpr float kSlack = 8.0f;
 constexpr float kLog2e = 1.44269504088896340736f, kLn2 = 0.69314718055994530942f;
-constexpr int kWaves = 4;                  // waves of a workgroup
-constexpr int kSplitTokens = 128;          // fewest tokens of a split: two tiles for each wave
+constexpr int kSplitTokens = 512;          // fewest tokens of a split
 
-// Splits of a sequence, from sizes the host knows: enough workgroups for every CU
-// to hold several, none with fewer than kSplitTokens tokens.
+// Splits of a sequence, from sizes the host knows: about sixteen workgroups for each
+// CU (uneven lengths even out over them), none with fewer than kSplitTokens tokens.
 struct Splits {
   int count, tokens;  // tokens of one split: a multiple of 16
 };
 static Splits attn_splits(int64_t B, int q_heads, int kv_heads, int64_t max_len, int64_t window) {
   const int64_t span = window > 0 && window < max_len ? window + 15 : max_len;
   const int64_t rows = B * kv_heads * ((q_heads / kv_heads + 15) / 16);
-  const int64_t want = std::max<int64_t>(1, (int64_t)kCUs * 6 / rows);
-  const int64_t most = std::max<int64_t>(1, (span + kSplitTokens - 1) / kSplitTokens);
+  const int64_t want = std::max<int64_t>(1, (int64_t)kCUs * 16 / rows);
+  const int64_t most = std::max<int64_t>(1, span / kSplitTokens);
   const int64_t n = std::min(want, most);
   const int64_t tokens = std::max<int64_t>(16, (span + n - 1) / n + 15) / 16 * 16;
   return {(int)std::max<int64_t>(1, (span + tokens - 1) / tokens), (int)tokens};
@@ -106,6 +105,12 @@ __device__ __forceinline__ uint32_t high_halves(uint32_t a, uint32_t b) { return
 
 __device__ __forceinline__ bf16x8_t octet(uint32_t a, uint32_t b, uint32_t c, uint32_t d) {
   return __builtin_bit_cast(bf16x8_t, make_uint4(a, b, c, d));
+}
+
+__device__ __forceinline__ void store_out(uint16_t* to, float4_t x) {
+  const f32x2_t lo = {x[0], x[1]}, hi = {x[2], x[3]};
+  *reinterpret_cast<uint2*>(to) = make_uint2(__builtin_bit_cast(uint32_t, __builtin_convertvector(lo, bf16x2_t)),
+                                             __builtin_bit_cast(uint32_t, __builtin_convertvector(hi, bf16x2_t)));
 }
 
 struct Running {
@@ -202,7 +207,7 @@ __device__ __forceinline__ int64_t part_row(const AttnArgs& a, int b, int head, 
   return ((int64_t)b * a.q_heads + head) * splits + s;
 }
 
-template <int DIM, bool FP8>
+template <int DIM, bool FP8, int kWaves>
 __global__ __launch_bounds__(kWaves * 64) void attn_decode_kernel(AttnArgs a, int splits, int split_tokens) {
   constexpr int ES = FP8 ? 1 : 2, PAD = DIM + 4;
   const int group = a.q_heads / a.cache.kv_heads, per = (group + 15) / 16;
@@ -309,10 +314,7 @@ __global__ __launch_bounds__(kWaves * 64) void attn_decode_kernel(AttnArgs a, in
     }
     if (only) {
       const float by = sum == 0 ? 0.0f : vg / sum;
-      const f32x2_t lo = {x[0] * by, x[1] * by}, hi = {x[2] * by, x[3] * by};
-      *reinterpret_cast<uint2*>(a.out + (int64_t)b * a.ldo + (int64_t)(head0 + h) * DIM + d) =
-          make_uint2(__builtin_bit_cast(uint32_t, __builtin_convertvector(lo, bf16x2_t)),
-                     __builtin_bit_cast(uint32_t, __builtin_convertvector(hi, bf16x2_t)));
+      store_out(a.out + (int64_t)b * a.ldo + (int64_t)(head0 + h) * DIM + d, x * by);
       if (a.lse && d == 0)
         a.lse[(int64_t)b * a.q_heads + head0 + h] = sum == 0 ? -INFINITY : top * kLn2 + logf(sum);
     } else {
@@ -323,10 +325,12 @@ __global__ __launch_bounds__(kWaves * 64) void attn_decode_kernel(AttnArgs a, in
   }
 }
 
-// Joins the splits of one query head: each counts 2^(its m - the largest m).
+// Joins the splits of one query head: each counts 2^(its m - the largest m).  Sixteen
+// groups of DIM / 4 threads take the splits in turn, then one group their sums.
 template <int DIM, bool FP8>
-__global__ __launch_bounds__(DIM) void attn_join_kernel(AttnArgs a, int splits, int split_tokens) {
-  const int h = blockIdx.x, b = blockIdx.y, d = threadIdx.x;
+__global__ __launch_bounds__(DIM * 4) void attn_join_kernel(AttnArgs a, int splits, int split_tokens) {
+  constexpr int kLanes = DIM / 4, kGroups = 16;
+  const int h = blockIdx.x, b = blockIdx.y, d = threadIdx.x % kLanes, grp = threadIdx.x / kLanes;
   const int len = min(max(a.lens[b], 0), a.max_len);
   const int start = a.window > 0 ? max(0, len - a.window) / 16 * 16 : 0;
   const int used = (len - start + split_tokens - 1) / split_tokens;
@@ -334,18 +338,35 @@ __global__ __launch_bounds__(DIM) void attn_join_kernel(AttnArgs a, int splits, 
   const float* parts = static_cast<const float*>(a.workspace);
   const float2* ml = reinterpret_cast<const float2*>(parts + part_row(a, (int)gridDim.y, 0, splits, 0) * DIM) +
                      part_row(a, b, h, splits, 0);
-  const float* row = parts + part_row(a, b, h, splits, 0) * DIM + d;
-  float top = kNone;
-  for (int s = 0; s < used; ++s) top = fmaxf(top, ml[s].x);
-  float sum = 0, x = 0;
-  for (int s = 0; s < used; ++s) {
+  const float* row = parts + part_row(a, b, h, splits, 0) * DIM + d * 4;
+  float m = kNone, sum = 0;
+  float4_t x = {0, 0, 0, 0};
+  for (int s = grp; s < used; s += kGroups) {
     const float2 w = ml[s];
-    const float f = __builtin_amdgcn_exp2f(w.x - top);
-    sum += w.y * f;
-    x += row[(int64_t)s * DIM] * f;
+    const float4_t v = *reinterpret_cast<const float4_t*>(row + (int64_t)s * DIM);
+    const float top = fmaxf(m, w.x), keep = __builtin_amdgcn_exp2f(m - top), f = __builtin_amdgcn_exp2f(w.x - top);
+    m = top;
+    sum = sum * keep + w.y * f;
+    x = x * keep + v * f;
   }
-  const float vg = FP8 ? *a.cache.v_amax / 448.0f : 1.0f;
-  a.out[(int64_t)b * a.ldo + (int64_t)h * DIM + d] = __builtin_bit_cast(uint16_t, (__bf16)(sum == 0 ? 0.0f : x * (vg / sum)));
+  __shared__ float ms[kGroups], ls[kGroups];
+  __shared__ float4_t xs[kGroups][kLanes];
+  xs[grp][d] = x;
+  if (d == 0) ms[grp] = m, ls[grp] = sum;
+  __syncthreads();
+  if (grp > 0) return;
+  float top = kNone;
+#pragma unroll
+  for (int i = 0; i < kGroups; ++i) top = fmaxf(top, ms[i]);
+  sum = 0, x = {0, 0, 0, 0};
+#pragma unroll
+  for (int i = 0; i < kGroups; ++i) {
+    const float f = __builtin_amdgcn_exp2f(ms[i] - top);
+    sum += ls[i] * f;
+    x += xs[i][d] * f;
+  }
+  const float by = sum == 0 ? 0.0f : (FP8 ? *a.cache.v_amax / 448.0f : 1.0f) / sum;
+  store_out(a.out + (int64_t)b * a.ldo + (int64_t)h * DIM + d * 4, x * by);
   if (a.lse && d == 0) a.lse[(int64_t)b * a.q_heads + h] = sum == 0 ? -INFINITY : top * kLn2 + logf(sum);
 }
 
@@ -354,21 +375,28 @@ size_t attn_decode_workspace(int64_t B, int q_heads, int kv_heads, int head_dim,
   return s.count > 1 ? (size_t)B * q_heads * s.count * (head_dim + 2) * sizeof(float) : 0;
 }
 
-template <int DIM, bool FP8>
-static hipError_t launch_dim(const AttnArgs& a, hipStream_t stream) {
+template <int DIM, bool FP8, int kWaves>
+static hipError_t launch_waves(const AttnArgs& a, const Splits& s, hipStream_t stream) {
   const int group = a.q_heads / a.cache.kv_heads;
-  const Splits s = attn_splits(a.B, a.q_heads, a.cache.kv_heads, a.max_len, a.window);
   const dim3 grid(a.cache.kv_heads * ((group + 15) / 16), s.count, (unsigned)a.B);
   const size_t lds = (size_t)kWaves * std::min(group, 16) * (DIM + 4) * sizeof(float);
   hipError_t e = hipSuccess;
-  if (lds > 48 * 1024)  // above the default bound of dynamic LDS: sixteen heads of 256
-    e = hipFuncSetAttribute(reinterpret_cast<const void*>(&attn_decode_kernel<DIM, FP8>),
+  if (lds > 48 * 1024)  // above the default bound of dynamic LDS: many heads of 256
+    e = hipFuncSetAttribute(reinterpret_cast<const void*>(&attn_decode_kernel<DIM, FP8, kWaves>),
                             hipFuncAttributeMaxDynamicSharedMemorySize, (int)lds);
   if (e != hipSuccess) return e;
-  attn_decode_kernel<DIM, FP8><<<grid, kWaves * 64, lds, stream>>>(a, s.count, s.tokens);
-  e = hipGetLastError();
+  attn_decode_kernel<DIM, FP8, kWaves><<<grid, kWaves * 64, lds, stream>>>(a, s.count, s.tokens);
+  return hipGetLastError();
+}
+
+template <int DIM, bool FP8>
+static hipError_t launch_dim(const AttnArgs& a, hipStream_t stream) {
+  const Splits s = attn_splits(a.B, a.q_heads, a.cache.kv_heads, a.max_len, a.window);
+  // few short sequences: eight waves to a workgroup, so that each has fewer tiles to go through
+  const bool few = s.count == 1 && a.B * a.q_heads <= 2 * kCUs;
+  hipError_t e = few ? launch_waves<DIM, FP8, 8>(a, s, stream) : launch_waves<DIM, FP8, 4>(a, s, stream);
   if (e != hipSuccess || s.count == 1) return e;
-  attn_join_kernel<DIM, FP8><<<dim3(a.q_heads, (unsigned)a.B), DIM, 0, stream>>>(a, s.count, s.tokens);
+  attn_join_kernel<DIM, FP8><<<dim3(a.q_heads, (unsigned)a.B), DIM * 4, 0, stream>>>(a, s.count, s.tokens);
   return hipGetLastError();
 }
 
