@@ -27,6 +27,7 @@ namespace nvfp4 {
 typedef __bf16 bf16x2_t __attribute__((ext_vector_type(2)));
 typedef __bf16 bf16x8_t __attribute__((ext_vector_type(8)));
 typedef float f32x2_t __attribute__((ext_vector_type(2)));
+typedef short short4_t __attribute__((ext_vector_type(4)));
 
 constexpr int kChunk = 64;
 
@@ -64,6 +65,11 @@ __device__ __forceinline__ void split_pair(float a, float b, uint32_t (&out)[N])
 __device__ __forceinline__ float4_t mfma_bf16(uint4 a, uint4 b, float4_t c) {
   return __builtin_amdgcn_mfma_f32_16x16x32_bf16(__builtin_bit_cast(bf16x8_t, a), __builtin_bit_cast(bf16x8_t, b), c, 0,
                                                  0, 0);
+}
+
+__device__ __forceinline__ float4_t mfma_bf16_16(uint2 a, uint2 b, float4_t c) {
+  return __builtin_amdgcn_mfma_f32_16x16x16bf16_1k(__builtin_bit_cast(short4_t, a), __builtin_bit_cast(short4_t, b), c, 0,
+                                                   0, 0);
 }
 
 __device__ __forceinline__ uint32_t low_halves(uint32_t a, uint32_t b) { return __builtin_amdgcn_perm(b, a, 0x05040100u); }
@@ -246,30 +252,39 @@ __global__ __launch_bounds__(256) void gdn_chunk_kernel(GdnArgs a) {
 
 // ---- the state from chunk to chunk -----------------------------------------------
 // A workgroup of eight waves carries 16 NT columns: four for the chain from state to
-// state, four for the outputs, which fill the chain's waits on the same SIMDs.  Of
-// each four, wave w takes the token rows 16 w .. 16 w + 15 of the products over tokens (K S,
-// T R; Q S, P N) and a quarter of the state's rows, so each left operand is read by
-// one wave only, from global memory into the registers that its last use freed a
-// chunk before.  Right operands -- the planes of S, of R = V - e^G K S and of N -- pass
-// between the waves through LDS in operand order (16 bytes for each lane, no bank
-// conflicts): a product leaves row 4 g + r in register r, which is how the next
-// product's right operand wants its rows, with the left operand's columns taken in
-// that order.  The key rows go through LDS too, for K^T.
+// state, four for the outputs, which fill the chain's waits on the same SIMDs.
 //
-// LDS, in units of NT KB: S of this chunk and of the next in two areas of 12; N
-// (planes for the state's update, then for the output) over S once every wave has
-// read it; R in 6.  Without beta N is V, known before the chunk, and lies in R's place.
-constexpr int kKeyRow = 272;  // bytes of a key row of 128 in LDS: rows 4 apart fall on other banks
-
+// Chain wave w owns a quarter of the state's rows, in registers throughout: a
+// product leaves row 4 g + r in register r, which is how the next product's right
+// operand wants its rows, so the state's planes are right operands as they are,
+// with the left operand's columns taken in that order.  Its products with the
+// wave's quarter of the key columns are shares of K S for all 64 tokens, which the
+// four waves add up through LDS, each for 16 tokens; R = V - e^G K S and N = T R pass
+// between the waves as planes in operand order (16 bytes for each lane, no bank
+// conflicts), and the update needs the wave's quarter of K^T only, transposed
+// through the wave's own corner of LDS.  Output wave w takes tokens 16 w .. 16 w + 15
+// of Q S and P N.  Left operands come from global memory into the registers that
+// their last use freed a chunk before.  Without beta N is V, known before the chunk.
+//
+// Each area of LDS is written between one pair of barriers and read between the next.
 template <int DK, int NT, bool DELTA>
 struct StateLds {
-  static constexpr int kSteps = DK / 32, kSPlanes = DELTA ? 3 : 2;
-  static constexpr int kS = kSPlanes * kSteps * NT * 1024;          // planes of S
-  static constexpr int kN = (3 + (DELTA ? 2 : 1)) * 2 * NT * 1024;  // planes of e^(G_64 - G) N, then of N
-  static constexpr int kX = kS > kN || !DELTA ? kS : kN;
-  static constexpr int kY = DELTA ? 3 * 2 * NT * 1024 : kN;
-  static constexpr int kOut = 6 * NT * 1024;  // of N for the output in kN
-  static constexpr int kKeys = 2 * kX + kY, kBytes = kKeys + kChunk * kKeyRow;
+  static constexpr int kRun = DK / 4 * 2;                           // bytes of a wave's quarter of a key row
+  static constexpr int kKeyRow = kRun + 16;                         // rows fall on different banks
+  static constexpr int kS = 0;                                      // two planes of S, for the outputs
+  static constexpr int kN = kS + 2 * (DK / 32) * NT * 1024;         // planes of e^(G_64 - G) N, then of N
+  static constexpr int kOut = 6 * NT * 1024;                        // of the latter in kN
+  static constexpr int kR = kN + kOut + (DELTA ? 2 : 1) * 2 * NT * 1024;
+  static constexpr int kShares = kR + (DELTA ? 6 * NT * 1024 : 0);  // of K S: [token tile][column tile][wave]
+  static constexpr int kKeys = kShares + (DELTA ? 16 * NT * 1024 : 0);
+  // corners of the waves: values and decays of a chain wave's 16 tokens, an output wave's results
+  static constexpr int kRow = 32 * NT + 16;
+  static constexpr int kValues = kKeys + 4 * kChunk * kKeyRow;
+  static constexpr int kDecays = kValues + 4 * 16 * kRow;           // e^G, then e^(G_64 - G); of odd chunks behind
+  static constexpr int kResults = kDecays + 8 * 128;
+  static constexpr int kQueryRow = DK * 2 + 16;
+  static constexpr int kQueries = kResults + 4 * 16 * kRow;
+  static constexpr int kBytes = kQueries + 4 * 16 * kQueryRow;
 };
 
 // What both halves of the workgroup share.
@@ -281,7 +296,7 @@ struct StateWave {
   uint8_t* lds;
   int64_t first;     // row of the sequence's first token
   int count, chunks; // its tokens and chunks
-  int hk, col;       // key head; lane's column of a row of v and out
+  int hk, col;       // key head; first column of the rows of v and out
   const uint8_t* ws; // the first chunk's slot
   int64_t ws_step;
   int w, lane, n, g;
@@ -290,7 +305,7 @@ struct StateWave {
   __device__ __forceinline__ uint4 get(const uint8_t* x, int p, int per, int s, int c) const {
     return *reinterpret_cast<const uint4*>(x + ((p * per + s) * NT + c) * 1024 + lane * 16);
   }
-  // 8 elements of step s of a q or k row, in the order of the state's planes
+  // 8 elements of step s of a q row in LDS, in the order of the state's planes
   __device__ __forceinline__ uint4 run(const uint16_t* row, int s) const {
     if constexpr (TW == 2) return *reinterpret_cast<const uint4*>(row + 32 * s + 8 * g);
     const uint2 x = *reinterpret_cast<const uint2*>(row + 32 * s + 4 * g);
@@ -332,7 +347,7 @@ struct RowPointers {
 template <int DK, int NT, bool DELTA>
 __device__ __forceinline__ void carry_state(const StateWave<DK, NT, DELTA>& m, float* st, bool load) {
   using L = StateLds<DK, NT, DELTA>;
-  constexpr int KS = DK / 32, TW = DK / 64, SP = L::kSPlanes;
+  constexpr int TW = DK / 64;  // state tiles, and dwords of a lane's piece of a key row by two
   const GdnArgs& a = m.a;
   const int w = m.w, n = m.n, g = m.g, lane = m.lane, chunks = m.chunks;
   const int steps = w / 2 + 1;  // 32-token steps that rows 16 w .. reach in a lower triangle
@@ -345,53 +360,69 @@ __device__ __forceinline__ void carry_state(const StateWave<DK, NT, DELTA>& m, f
 #pragma unroll
       for (int r = 0; r < 4; ++r) S[c][i][r] = load ? st[(int64_t)(r * TW + i) * a.v_dim + 16 * c] : 0.0f;
 
-  uint8_t* x0 = m.lds;
-  uint8_t* x1 = m.lds + L::kX;
-  uint8_t* y = m.lds + 2 * L::kX;
-  uint8_t* keys = m.lds + L::kKeys;
-  auto put_state = [&](uint8_t* x) {
-#pragma unroll
-    for (int c = 0; c < NT; ++c) {
-      uint32_t z[2 * TW][SP];
-#pragma unroll
-      for (int e = 0; e < 2 * TW; ++e) {
-        const int f = 2 * e;
-        split_pair(S[c][f % TW][f / TW], S[c][(f + 1) % TW][(f + 1) / TW], z[e]);
-      }
-#pragma unroll
-      for (int p = 0; p < SP; ++p) {
-        if constexpr (TW == 2)
-          *reinterpret_cast<uint4*>(x + ((p * KS + w) * NT + c) * 1024 + lane * 16) =
-              make_uint4(z[0][p], z[1][p], z[2][p], z[3][p]);
-        else
-          *reinterpret_cast<uint2*>(x + ((p * KS + w / 2) * NT + c) * 1024 + lane * 16 + (w % 2) * 8) =
-              make_uint2(z[0][p], z[1][p]);
-      }
-    }
-  };
-  // left operands in flight
-  RowPointers<1, const uint16_t> kp;
-  RowPointers<4, const uint16_t> vp;
-  uint4 ka[KS], ta[2][3];
-  uint16_t va[NT][4];
-  float4_t decay, left;
-  float whole;
+  // What comes from memory for the next chunk: rows in pieces of 16 bytes, lanes side
+  // by side along a row, and the decays one to a lane.  (A load in operand order, 16
+  // rows side by side, takes one turn of the vector cache for each lane, four
+  // times as many; a load of 2 bytes a lane as many as one of 16.)  The wave sorts them
+  // in its corners of LDS a chunk ahead.
+  constexpr int kPieces = L::kRun / 16, kLoads = kChunk * kPieces / 64;  // of a key row; of a lane
+  u32x4_t next_k[kLoads], next_v;
+  float next_decay;
+  RowPointers<kLoads, const uint16_t> kp;
+  RowPointers<1, const uint16_t> vp;
+  const bool has_piece = lane < 32 * NT;
+  const int v_row = lane / (2 * NT) % 16, v_piece = lane % (2 * NT);
+  uint8_t* keys = m.lds + L::kKeys + w * kChunk * L::kKeyRow;
+  uint8_t* values = m.lds + L::kValues + w * 16 * L::kRow;
+  const int decay_at = lane < 16 ? Slot::kDecay + (16 * w + n) * 4
+                                 : (lane < 32 ? Slot::kLeft + (16 * w + n) * 4 : Slot::kDecay + 63 * 4);
+  uint4 ta[2][3];
   auto point = [&](int ch) {
     const int64_t row0 = m.first + (int64_t)ch * kChunk;
-    kp.at(a.k + m.hk * DK, row0, a.ldk, 16 * w + n, m.last_of(ch));
-    vp.at(a.v + m.col, row0, a.ldv, 16 * w + 4 * g, m.last_of(ch));
+    const int last = m.last_of(ch);
+#pragma unroll
+    for (int i = 0; i < kLoads; ++i)
+      kp.p[i] = a.k + (row0 + min((i * 64 + lane) / kPieces, last)) * a.ldk + m.hk * DK + w * (DK / 4) + lane % kPieces * 8;
+    vp.at(a.v + m.col + 8 * v_piece, row0, a.ldv, 16 * w + v_row, last);
   };
-  auto fetch_rows = [&](int ch) {
+  auto fetch_rows = [&](int ch) {  // where the pointers stand
 #pragma unroll
-    for (int s = 0; s < KS; ++s) ka[s] = m.run(kp.p[0], s);
-    const uint8_t* p = m.ws + ch * m.ws_step;
-    decay = *reinterpret_cast<const float4_t*>(p + Slot::kDecay + (16 * w + 4 * g) * 4);
-    left = *reinterpret_cast<const float4_t*>(p + Slot::kLeft + (16 * w + 4 * g) * 4);
-    whole = *reinterpret_cast<const float*>(p + Slot::kDecay + 63 * 4);
+    for (int i = 0; i < kLoads; ++i) next_k[i] = *reinterpret_cast<const u32x4_t*>(kp.p[i]);
+    next_decay = *reinterpret_cast<const float*>(m.ws + ch * m.ws_step + decay_at);
+    if (has_piece) next_v = *reinterpret_cast<const u32x4_t*>(vp.p[0]);
+  };
+  // the pointers stand at chunk `from`; on to the next, or to the last one again
+  auto on = [&](int from) {
+    const int to = min(from + 1, chunks - 1);
+    if (m.last_of(to) == kChunk - 1) {
+      if (to > from) kp.on(a.ldk * kChunk), vp.on(a.ldv * kChunk);
+    } else {
+      point(to);
+    }
+    return to;
+  };
+  uint32_t ka[4][2 * TW];  // left operand of K S: 4 TW elements of the key rows of tokens 16 i + n
+  float whole, next_whole;
+  auto sort_rows = [&](int ch) {  // chunk ch's rows into LDS, K's operands back
 #pragma unroll
-    for (int c = 0; c < NT; ++c)
+    for (int i = 0; i < kLoads; ++i)
+      *reinterpret_cast<u32x4_t*>(keys + (i * 64 + lane) / kPieces * L::kKeyRow + lane % kPieces * 16) = next_k[i];
+    if (has_piece) *reinterpret_cast<u32x4_t*>(values + v_row * L::kRow + 16 * v_piece) = next_v;
+    if (lane < 32) reinterpret_cast<float*>(m.lds + L::kDecays + (ch % 2 * 4 + w) * 128)[lane] = next_decay;
+    next_whole = __builtin_bit_cast(float, __builtin_amdgcn_readlane(__builtin_bit_cast(int, next_decay), 32));
+    if (DELTA) {
 #pragma unroll
-      for (int j = 0; j < 4; ++j) va[c][j] = vp.p[j][16 * c];
+      for (int i = 0; i < 4; ++i) {
+        const uint8_t* from = keys + (16 * i + n) * L::kKeyRow + g * 8 * TW;
+        if constexpr (TW == 2) {
+          const uint4 y = *reinterpret_cast<const uint4*>(from);
+          ka[i][0] = y.x, ka[i][1] = y.y, ka[i][2] = y.z, ka[i][3] = y.w;
+        } else {
+          const uint2 y = *reinterpret_cast<const uint2*>(from);
+          ka[i][0] = y.x, ka[i][1] = y.y;
+        }
+      }
+    }
   };
   auto fetch_t = [&](int ch) {
 #pragma unroll
@@ -400,61 +431,91 @@ __device__ __forceinline__ void carry_state(const StateWave<DK, NT, DELTA>& m, f
       for (int p = 0; p < 3; ++p)
         if (s < steps) ta[s][p] = m.block(ch, Slot::kT, p, s);
   };
+  int at = 0;  // where the pointers stand
   if (chunks > 0) {
     point(0);
     fetch_rows(0);
     if (DELTA) fetch_t(0);
-    put_state(x0);
-    __syncthreads();
+    sort_rows(0);
+    at = on(0);
+    fetch_rows(at);
   }
   for (int ch = 0; ch < chunks; ++ch) {
     const int next = min(ch + 1, chunks - 1);
-    // key rows for K^T
+    whole = next_whole;
+    // shares of K S from this wave's rows of S; two planes of S for the outputs
 #pragma unroll
-    for (int s = 0; s < KS; ++s) {
-      uint8_t* to = keys + (16 * w + n) * kKeyRow;
-      if constexpr (TW == 2) {
-        *reinterpret_cast<uint4*>(to + 64 * s + 16 * g) = ka[s];
-      } else {
-        *reinterpret_cast<uint2*>(to + 64 * s + 8 * g) = make_uint2(ka[s].x, ka[s].y);
-        *reinterpret_cast<uint2*>(to + 64 * s + 32 + 8 * g) = make_uint2(ka[s].z, ka[s].w);
+    for (int c = 0; c < NT; ++c) {
+      uint32_t z[2 * TW][DELTA ? 3 : 2];
+#pragma unroll
+      for (int e = 0; e < 2 * TW; ++e) {
+        const int f = 2 * e;
+        split_pair(S[c][f % TW][f / TW], S[c][(f + 1) % TW][(f + 1) / TW], z[e]);
+      }
+#pragma unroll
+      for (int p = 0; p < 2; ++p) {
+        if constexpr (TW == 2)
+          *reinterpret_cast<uint4*>(m.lds + L::kS + ((p * (DK / 32) + w) * NT + c) * 1024 + lane * 16) =
+              make_uint4(z[0][p], z[1][p], z[2][p], z[3][p]);
+        else
+          *reinterpret_cast<uint2*>(m.lds + L::kS + ((p * (DK / 32) + w / 2) * NT + c) * 1024 + lane * 16 + (w % 2) * 8) =
+              make_uint2(z[0][p], z[1][p]);
+      }
+      if (DELTA) {
+        float4_t ks[4];
+#pragma unroll
+        for (int i = 0; i < 4; ++i) ks[i] = {0, 0, 0, 0};
+#pragma unroll
+        for (int p = 2; p >= 0; --p)
+#pragma unroll
+          for (int i = 0; i < 4; ++i) {
+            constexpr int P = DELTA ? 3 : 2;
+            if constexpr (TW == 2)
+              ks[i] = mfma_bf16(make_uint4(ka[i][0], ka[i][1], ka[i][2], ka[i][3]),
+                                make_uint4(z[0][p % P], z[1][p % P], z[2][p % P], z[3][p % P]), ks[i]);
+            else
+              ks[i] = mfma_bf16_16(make_uint2(ka[i][0], ka[i][1]), make_uint2(z[0][p % P], z[1][p % P]), ks[i]);
+          }
+#pragma unroll
+        for (int i = 0; i < 4; ++i)
+          *reinterpret_cast<float4_t*>(m.lds + L::kShares + ((i * NT + c) * 4 + w) * 1024 + lane * 16) = ks[i];
       }
     }
+    const uint8_t* decays = m.lds + L::kDecays + (ch % 2 * 4 + w) * 128;
+    const float4_t decay = *reinterpret_cast<const float4_t*>(decays + 16 * g);
+    const float4_t left = *reinterpret_cast<const float4_t*>(decays + 64 + 16 * g);
     float4_t N[NT];
 #pragma unroll
     for (int c = 0; c < NT; ++c) {
 #pragma unroll
-      for (int r = 0; r < 4; ++r) N[c][r] = __uint_as_float((uint32_t)va[c][r] << 16);
-      if (DELTA) {
-        float4_t acc[3] = {{0, 0, 0, 0}, {0, 0, 0, 0}, {0, 0, 0, 0}};
-#pragma unroll
-        for (int s = 0; s < KS; ++s)
-#pragma unroll
-          for (int p = 0; p < 3; ++p) acc[p] = mfma_bf16(ka[s], m.get(x0, p % SP, KS, s, c), acc[p]);
-        N[c] -= decay * ((acc[2] + acc[1]) + acc[0]);
-        m.template put_rows<3>(y, c, N[c]);
-      } else {
-        m.template put_rows<3>(y, c, N[c] * left);
-        m.template put_rows<1>(y + L::kOut, c, N[c]);
+      for (int r = 0; r < 4; ++r)
+        N[c][r] = __uint_as_float(
+            (uint32_t) * reinterpret_cast<const uint16_t*>(values + (4 * g + r) * L::kRow + (16 * c + n) * 2) << 16);
+      if (!DELTA) {
+        m.template put_rows<3>(m.lds + L::kN, c, N[c] * left);
+        m.template put_rows<1>(m.lds + L::kN + L::kOut, c, N[c]);
       }
     }
     __syncthreads();
-    const float4_t left_now = left;
-    const float whole_now = whole;
-    if (m.last_of(next) == kChunk - 1) {
-      if (next > ch) kp.on(a.ldk * kChunk), vp.on(a.ldv * kChunk);
-    } else {
-      point(next);
+    if (DELTA) {  // R = V - e^G K S
+#pragma unroll
+      for (int c = 0; c < NT; ++c) {
+        float4_t sh[4];
+#pragma unroll
+        for (int i = 0; i < 4; ++i)
+          sh[i] = *reinterpret_cast<const float4_t*>(m.lds + L::kShares + ((w * NT + c) * 4 + i) * 1024 + lane * 16);
+        N[c] -= decay * ((sh[0] + sh[1]) + (sh[2] + sh[3]));
+        m.template put_rows<3>(m.lds + L::kR, c, N[c]);
+      }
     }
-    fetch_rows(next);
-    // this wave's rows of K^T: TW elements of 8 tokens' rows, transposed within the lane
+    // the wave's rows of K^T: TW elements of 8 tokens' rows, transposed within the lane
     uint4 kt[2][TW];
 #pragma unroll
     for (int s = 0; s < 2; ++s) {
       uint32_t z[8];
 #pragma unroll
       for (int j = 0; j < 8; ++j) {
-        const uint8_t* from = keys + (32 * s + (j / 4) * 16 + 4 * g + j % 4) * kKeyRow + (w * (DK / 4) + n * TW) * 2;
+        const uint8_t* from = keys + (32 * s + (j / 4) * 16 + 4 * g + j % 4) * L::kKeyRow + n * TW * 2;
         if constexpr (TW == 2)
           z[j] = *reinterpret_cast<const uint32_t*>(from);
         else
@@ -469,14 +530,18 @@ __device__ __forceinline__ void carry_state(const StateWave<DK, NT, DELTA>& m, f
         kt[s][i] = make_uint4(e[0], e[1], e[2], e[3]);
       }
     }
-    const uint8_t* np = y;
+    sort_rows(ch + 1);  // behind the last chunk: its rows again
+    at = on(at);
+    fetch_rows(at);
     if (DELTA) {  // N = T R
+      __syncthreads();
 #pragma unroll
       for (int c = 0; c < NT; ++c) {
         float4_t acc[3] = {{0, 0, 0, 0}, {0, 0, 0, 0}, {0, 0, 0, 0}};
 #pragma unroll
         for (int s = 0; s < 2; ++s) {
           if (s >= steps) continue;
+          const uint8_t* y = m.lds + L::kR;
           const uint4 r0 = m.get(y, 0, 2, s, c), r1 = m.get(y, 1, 2, s, c), r2 = m.get(y, 2, 2, s, c);
           acc[0] = mfma_bf16(ta[s][0], r0, acc[0]);
           acc[1] = mfma_bf16(ta[s][1], r0, acc[1]);
@@ -486,31 +551,27 @@ __device__ __forceinline__ void carry_state(const StateWave<DK, NT, DELTA>& m, f
           acc[2] = mfma_bf16(ta[s][0], r2, acc[2]);
         }
         N[c] = (acc[2] + acc[1]) + acc[0];
-        m.template put_rows<3>(x0, c, N[c] * left_now);
-        m.template put_rows<2>(x0 + L::kOut, c, N[c]);
+        m.template put_rows<3>(m.lds + L::kN, c, N[c] * left);
+        m.template put_rows<2>(m.lds + L::kN + L::kOut, c, N[c]);
       }
       fetch_t(next);
-      np = x0;
       __syncthreads();
     }
     // S' = e^G S + K^T (e^(G_64 - G) N)
 #pragma unroll
     for (int c = 0; c < NT; ++c) {
 #pragma unroll
-      for (int i = 0; i < TW; ++i) S[c][i] *= whole_now;
+      for (int i = 0; i < TW; ++i) S[c][i] *= whole;
 #pragma unroll
       for (int s = 0; s < 2; ++s)
 #pragma unroll
         for (int p = 2; p >= 0; --p) {
-          const uint4 u = m.get(np, p, 2, s, c);
+          const uint4 u = m.get(m.lds + L::kN, p, 2, s, c);
 #pragma unroll
           for (int i = 0; i < TW; ++i) S[c][i] = mfma_bf16(kt[s][i], u, S[c][i]);
         }
     }
-    put_state(x1);
-    uint8_t* t = x0;
-    x0 = x1, x1 = t;
-    __syncthreads();
+    if (!DELTA) __syncthreads();
   }
 #pragma unroll
   for (int c = 0; c < NT; ++c)
@@ -527,20 +588,30 @@ __device__ __forceinline__ void write_outputs(const StateWave<DK, NT, DELTA>& m)
   const GdnArgs& a = m.a;
   const int w = m.w, n = m.n, g = m.g, chunks = m.chunks;
   const int steps = w / 2 + 1;
-  const uint8_t* x0 = m.lds;
-  const uint8_t* x1 = m.lds + L::kX;
-  const uint8_t* y = m.lds + 2 * L::kX;
-  RowPointers<1, const uint16_t> qp;
-  RowPointers<4, uint16_t> op;
+  constexpr int kPieces = DK / 8, kLoads = 16 * kPieces / 64;  // of a query row; of a lane, as the chain's rows come
+  RowPointers<kLoads, const uint16_t> qp;
+  RowPointers<1, uint16_t> op;
+  u32x4_t next_q[kLoads];
   uint4 qa[KS], pa[2][2];
-  float4_t decay;
+  uint8_t* queries = m.lds + L::kQueries + w * 16 * L::kQueryRow;
+  const int o_row = m.lane / (2 * NT) % 16, o_piece = m.lane % (2 * NT);  // as the values come
+  uint8_t* results = m.lds + L::kResults + w * 16 * L::kRow;
   auto point = [&](int ch) {
-    qp.at(a.q + m.hk * DK, m.first + (int64_t)ch * kChunk, a.ldq, 16 * w + n, m.last_of(ch));
-  };
-  auto fetch_q = [&](int ch) {
 #pragma unroll
-    for (int s = 0; s < KS; ++s) qa[s] = m.run(qp.p[0], s);
-    decay = *reinterpret_cast<const float4_t*>(m.ws + ch * m.ws_step + Slot::kDecay + (16 * w + 4 * g) * 4);
+    for (int i = 0; i < kLoads; ++i)
+      qp.p[i] = a.q + (m.first + (int64_t)ch * kChunk + min(16 * w + (i * 64 + m.lane) / kPieces, m.last_of(ch))) * a.ldq +
+                m.hk * DK + m.lane % kPieces * 8;
+  };
+  auto fetch_q = [&] {  // where the pointers stand
+#pragma unroll
+    for (int i = 0; i < kLoads; ++i) next_q[i] = *reinterpret_cast<const u32x4_t*>(qp.p[i]);
+  };
+  auto sort_q = [&] {
+#pragma unroll
+    for (int i = 0; i < kLoads; ++i)
+      *reinterpret_cast<u32x4_t*>(queries + (i * 64 + m.lane) / kPieces * L::kQueryRow + m.lane % kPieces * 16) = next_q[i];
+#pragma unroll
+    for (int s = 0; s < KS; ++s) qa[s] = m.run(reinterpret_cast<const uint16_t*>(queries + n * L::kQueryRow), s);
   };
   auto fetch_p = [&](int ch) {
 #pragma unroll
@@ -549,23 +620,29 @@ __device__ __forceinline__ void write_outputs(const StateWave<DK, NT, DELTA>& m)
       for (int p = 0; p < 2; ++p)
         if (s < steps) pa[s][p] = m.block(ch, Slot::kP, p, s);
   };
+  auto on = [&](int from) {
+    const int to = min(from + 1, chunks - 1);
+    if (m.last_of(to) == kChunk - 1) {
+      if (to > from) qp.on(a.ldq * kChunk);
+    } else {
+      point(to);
+    }
+    return to;
+  };
+  int at = 0;
   if (chunks > 0) {
     point(0);
-    op.at(a.out + m.col, m.first, a.ldo, 16 * w + 4 * g, kChunk);
-    fetch_q(0);
+    op.at(a.out + m.col + 8 * o_piece, m.first, a.ldo, 16 * w + o_row, kChunk);
+    fetch_q();
     fetch_p(0);
-    __syncthreads();
+    sort_q();
+    at = on(0);
+    fetch_q();
   }
   for (int ch = 0; ch < chunks; ++ch) {
-    const int next = min(ch + 1, chunks - 1), last = m.last_of(ch);
-    uint4 sp[2][NT][KS];
-#pragma unroll
-    for (int c = 0; c < NT; ++c)
-#pragma unroll
-      for (int s = 0; s < KS; ++s)
-#pragma unroll
-        for (int p = 0; p < 2; ++p) sp[p][c][s] = m.get(x0, p, KS, s, c);
+    const int last = m.last_of(ch);
     __syncthreads();
+    const float4_t decay = *reinterpret_cast<const float4_t*>(m.lds + L::kDecays + (ch % 2 * 4 + w) * 128 + 16 * g);
     float4_t o[NT];
 #pragma unroll
     for (int c = 0; c < NT; ++c) {
@@ -573,49 +650,42 @@ __device__ __forceinline__ void write_outputs(const StateWave<DK, NT, DELTA>& m)
       o[c] = {0, 0, 0, 0};
 #pragma unroll
       for (int s = 0; s < KS; ++s) {
-        o[c] = mfma_bf16(qa[s], sp[0][c][s], o[c]);
-        lo = mfma_bf16(qa[s], sp[1][c][s], lo);
+        o[c] = mfma_bf16(qa[s], m.get(m.lds + L::kS, 0, KS, s, c), o[c]);
+        lo = mfma_bf16(qa[s], m.get(m.lds + L::kS, 1, KS, s, c), lo);
       }
       o[c] = (o[c] + lo) * (decay * a.scale);
     }
-    if (m.last_of(next) == kChunk - 1) {
-      if (next > ch) qp.on(a.ldq * kChunk);
-    } else {
-      point(next);
+    sort_q();  // the next chunk's
+    at = on(at);
+    fetch_q();
+    if (DELTA) {
+      __syncthreads();
+      __syncthreads();
     }
-    fetch_q(next);
-    if (DELTA) __syncthreads();
-    const uint8_t* np = (DELTA ? x0 : y) + L::kOut;
 #pragma unroll
     for (int c = 0; c < NT; ++c) {
       float4_t lo = {0, 0, 0, 0};
 #pragma unroll
       for (int s = 0; s < 2; ++s) {
         if (s >= steps) continue;
-        const uint4 n0 = m.get(np, 0, 2, s, c);
+        const uint4 n0 = m.get(m.lds + L::kN + L::kOut, 0, 2, s, c);
         o[c] = mfma_bf16(pa[s][0], n0, o[c]);
         lo = mfma_bf16(pa[s][1], n0, lo);
-        if (DELTA) lo = mfma_bf16(pa[s][0], m.get(np, 1, 2, s, c), lo);
+        if (DELTA) lo = mfma_bf16(pa[s][0], m.get(m.lds + L::kN + L::kOut, 1, 2, s, c), lo);
       }
       o[c] += lo;
     }
-    fetch_p(next);
-    if (last == kChunk - 1) {
+    fetch_p(min(ch + 1, chunks - 1));
+    if (!DELTA) __syncthreads();
 #pragma unroll
-      for (int c = 0; c < NT; ++c)
+    for (int c = 0; c < NT; ++c)
 #pragma unroll
-        for (int r = 0; r < 4; ++r) op.p[r][16 * c] = __builtin_bit_cast(uint16_t, (__bf16)o[c][r]);
-    } else {
-#pragma unroll
-      for (int c = 0; c < NT; ++c)
-#pragma unroll
-        for (int r = 0; r < 4; ++r)
-          if (16 * w + 4 * g + r <= last) op.p[r][16 * c] = __builtin_bit_cast(uint16_t, (__bf16)o[c][r]);
-    }
+      for (int r = 0; r < 4; ++r)
+        *reinterpret_cast<uint16_t*>(results + (4 * g + r) * L::kRow + (16 * c + n) * 2) =
+            __builtin_bit_cast(uint16_t, (__bf16)o[c][r]);
+    if (m.lane < 32 * NT && 16 * w + o_row <= last)
+      *reinterpret_cast<uint4*>(op.p[0]) = *reinterpret_cast<const uint4*>(results + o_row * L::kRow + 16 * o_piece);
     op.on(a.ldo * kChunk);
-    const uint8_t* t = x0;
-    x0 = x1, x1 = t;
-    __syncthreads();
   }
 }
 
@@ -639,8 +709,8 @@ __global__ __launch_bounds__(512, 2) void gdn_state_kernel(GdnArgs a) {
   const uint8_t* ws = static_cast<const uint8_t*>(a.workspace) + (rows.first / kChunk + b) * step +
                       h * (int64_t)(DELTA ? Slot::kBytesDelta : Slot::kBytesLinear);
   const StateWave<DK, NT, DELTA> m{a, lds, rows.first, rows.count, (rows.count + kChunk - 1) / kChunk,
-                                   h / (a.v_heads / a.k_heads), h * a.v_dim + slab * 16 * NT + n, ws, step, w, lane, n, g};
-  // both halves pass the same barriers: one before the chunks and three (two without beta) in each
+                                   h / (a.v_heads / a.k_heads), h * a.v_dim + slab * 16 * NT, ws, step, w, lane, n, g};
+  // both halves pass the same barriers: three (two without beta) in each chunk
   if (wave < 4)
     carry_state<DK, NT, DELTA>(m, a.state + ((slot * a.v_heads + h) * DK + w * (DK / 4) + 4 * g * (DK / 64)) * (int64_t)a.v_dim +
                                       slab * 16 * NT + n,
