@@ -80,8 +80,10 @@ struct Rows {
   int count;
 };
 __device__ __forceinline__ Rows rows_of(const GdnArgs& a, int b) {
-  const int64_t first = min(max((int64_t)a.cu[b], (int64_t)0), a.T);
-  return {first, (int)(min(max((int64_t)a.cu[b + 1], first), a.T) - first)};
+  // the same in every lane: held in scalar registers, with the addresses that follow from them
+  const int64_t lo = __builtin_amdgcn_readfirstlane(a.cu[b]), hi = __builtin_amdgcn_readfirstlane(a.cu[b + 1]);
+  const int64_t first = min(max(lo, (int64_t)0), a.T);
+  return {first, (int)(min(max(hi, first), a.T) - first)};
 }
 
 // ---- T and P of every chunk ------------------------------------------------------
@@ -251,8 +253,9 @@ __global__ __launch_bounds__(256) void gdn_chunk_kernel(GdnArgs a) {
 }
 
 // ---- the state from chunk to chunk -----------------------------------------------
-// A workgroup of eight waves carries 16 NT columns: four for the chain from state to
-// state, four for the outputs, which fill the chain's waits on the same SIMDs.
+// A workgroup of twelve waves carries 16 NT columns: four for the chain from state to
+// state, four for the outputs and four that feed the chain, which fill its waits on
+// the same SIMDs.
 //
 // Chain wave w owns a quarter of the state's rows, in registers throughout: a
 // product leaves row 4 g + r in register r, which is how the next product's right
@@ -261,27 +264,28 @@ __global__ __launch_bounds__(256) void gdn_chunk_kernel(GdnArgs a) {
 // wave's quarter of the key columns are shares of K S for all 64 tokens, which the
 // four waves add up through LDS, each for 16 tokens; R = V - e^G K S and N = T R pass
 // between the waves as planes in operand order (16 bytes for each lane, no bank
-// conflicts), and the update needs the wave's quarter of K^T only, transposed
-// through the wave's own corner of LDS.  Output wave w takes tokens 16 w .. 16 w + 15
-// of Q S and P N.  Left operands come from global memory into the registers that
-// their last use freed a chunk before.  Without beta N is V, known before the chunk.
+// conflicts), and the update needs the wave's quarter of K^T only.  Output wave w
+// takes tokens 16 w .. 16 w + 15 of Q S and P N.  Without beta N is V, known before
+// the chunk.
 //
 // Each area of LDS is written between one pair of barriers and read between the next.
 template <int DK, int NT, bool DELTA>
 struct StateLds {
   static constexpr int kRun = DK / 4 * 2;                           // bytes of a wave's quarter of a key row
   static constexpr int kKeyRow = kRun + 16;                         // rows fall on different banks
+  static constexpr int kTurned = DK / 64 * 2;                       // operand blocks of a wave's rows of K^T
   static constexpr int kS = 0;                                      // two planes of S, for the outputs
   static constexpr int kN = kS + 2 * (DK / 32) * NT * 1024;         // planes of e^(G_64 - G) N, then of N
   static constexpr int kOut = 6 * NT * 1024;                        // of the latter in kN
   static constexpr int kR = kN + kOut + (DELTA ? 2 : 1) * 2 * NT * 1024;
   static constexpr int kShares = kR + (DELTA ? 6 * NT * 1024 : 0);  // of K S: [token tile][column tile][wave]
   static constexpr int kKeys = kShares + (DELTA ? 16 * NT * 1024 : 0);
-  // corners of the waves: values and decays of a chain wave's 16 tokens, an output wave's results
+  static constexpr int kKeysT = kKeys + 4 * kChunk * kKeyRow;
+  // values and decays of the 16 tokens of a wave pair; an output wave's results and queries
   static constexpr int kRow = 32 * NT + 16;
-  static constexpr int kValues = kKeys + 4 * kChunk * kKeyRow;
-  static constexpr int kDecays = kValues + 4 * 16 * kRow;           // e^G, then e^(G_64 - G); of odd chunks behind
-  static constexpr int kResults = kDecays + 8 * 128;
+  static constexpr int kValues = kKeysT + 4 * kTurned * 1024;
+  static constexpr int kDecays = kValues + 4 * 16 * kRow;           // e^G, e^(G_64 - G), e^(G_64)
+  static constexpr int kResults = kDecays + 4 * 144;
   static constexpr int kQueryRow = DK * 2 + 16;
   static constexpr int kQueries = kResults + 4 * 16 * kRow;
   static constexpr int kBytes = kQueries + 4 * 16 * kQueryRow;
@@ -360,67 +364,21 @@ __device__ __forceinline__ void carry_state(const StateWave<DK, NT, DELTA>& m, f
 #pragma unroll
       for (int r = 0; r < 4; ++r) S[c][i][r] = load ? st[(int64_t)(r * TW + i) * a.v_dim + 16 * c] : 0.0f;
 
-  // What comes from memory for the next chunk: rows in pieces of 16 bytes, lanes side
-  // by side along a row, and the decays one to a lane.  (A load in operand order, 16
-  // rows side by side, takes one turn of the vector cache for each lane, four
-  // times as many; a load of 2 bytes a lane as many as one of 16.)  The wave sorts them
-  // in its corners of LDS a chunk ahead.
-  constexpr int kPieces = L::kRun / 16, kLoads = kChunk * kPieces / 64;  // of a key row; of a lane
-  u32x4_t next_k[kLoads], next_v;
-  float next_decay;
-  RowPointers<kLoads, const uint16_t> kp;
-  RowPointers<1, const uint16_t> vp;
-  const bool has_piece = lane < 32 * NT;
-  const int v_row = lane / (2 * NT) % 16, v_piece = lane % (2 * NT);
-  uint8_t* keys = m.lds + L::kKeys + w * kChunk * L::kKeyRow;
-  uint8_t* values = m.lds + L::kValues + w * 16 * L::kRow;
-  const int decay_at = lane < 16 ? Slot::kDecay + (16 * w + n) * 4
-                                 : (lane < 32 ? Slot::kLeft + (16 * w + n) * 4 : Slot::kDecay + 63 * 4);
+  const uint8_t* keys = m.lds + L::kKeys + w * kChunk * L::kKeyRow;
+  const uint8_t* values = m.lds + L::kValues + w * 16 * L::kRow;
+  const uint8_t* decays = m.lds + L::kDecays + w * 144;
   uint4 ta[2][3];
-  auto point = [&](int ch) {
-    const int64_t row0 = m.first + (int64_t)ch * kChunk;
-    const int last = m.last_of(ch);
-#pragma unroll
-    for (int i = 0; i < kLoads; ++i)
-      kp.p[i] = a.k + (row0 + min((i * 64 + lane) / kPieces, last)) * a.ldk + m.hk * DK + w * (DK / 4) + lane % kPieces * 8;
-    vp.at(a.v + m.col + 8 * v_piece, row0, a.ldv, 16 * w + v_row, last);
-  };
-  auto fetch_rows = [&](int ch) {  // where the pointers stand
-#pragma unroll
-    for (int i = 0; i < kLoads; ++i) next_k[i] = *reinterpret_cast<const u32x4_t*>(kp.p[i]);
-    next_decay = *reinterpret_cast<const float*>(m.ws + ch * m.ws_step + decay_at);
-    if (has_piece) next_v = *reinterpret_cast<const u32x4_t*>(vp.p[0]);
-  };
-  // the pointers stand at chunk `from`; on to the next, or to the last one again
-  auto on = [&](int from) {
-    const int to = min(from + 1, chunks - 1);
-    if (m.last_of(to) == kChunk - 1) {
-      if (to > from) kp.on(a.ldk * kChunk), vp.on(a.ldv * kChunk);
-    } else {
-      point(to);
-    }
-    return to;
-  };
   uint32_t ka[4][2 * TW];  // left operand of K S: 4 TW elements of the key rows of tokens 16 i + n
-  float whole, next_whole;
-  auto sort_rows = [&](int ch) {  // chunk ch's rows into LDS, K's operands back
+  auto get_keys = [&] {
 #pragma unroll
-    for (int i = 0; i < kLoads; ++i)
-      *reinterpret_cast<u32x4_t*>(keys + (i * 64 + lane) / kPieces * L::kKeyRow + lane % kPieces * 16) = next_k[i];
-    if (has_piece) *reinterpret_cast<u32x4_t*>(values + v_row * L::kRow + 16 * v_piece) = next_v;
-    if (lane < 32) reinterpret_cast<float*>(m.lds + L::kDecays + (ch % 2 * 4 + w) * 128)[lane] = next_decay;
-    next_whole = __builtin_bit_cast(float, __builtin_amdgcn_readlane(__builtin_bit_cast(int, next_decay), 32));
-    if (DELTA) {
-#pragma unroll
-      for (int i = 0; i < 4; ++i) {
-        const uint8_t* from = keys + (16 * i + n) * L::kKeyRow + g * 8 * TW;
-        if constexpr (TW == 2) {
-          const uint4 y = *reinterpret_cast<const uint4*>(from);
-          ka[i][0] = y.x, ka[i][1] = y.y, ka[i][2] = y.z, ka[i][3] = y.w;
-        } else {
-          const uint2 y = *reinterpret_cast<const uint2*>(from);
-          ka[i][0] = y.x, ka[i][1] = y.y;
-        }
+    for (int i = 0; i < 4; ++i) {
+      const uint8_t* from = keys + (16 * i + n) * L::kKeyRow + g * 8 * TW;
+      if constexpr (TW == 2) {
+        const uint4 y = *reinterpret_cast<const uint4*>(from);
+        ka[i][0] = y.x, ka[i][1] = y.y, ka[i][2] = y.z, ka[i][3] = y.w;
+      } else {
+        const uint2 y = *reinterpret_cast<const uint2*>(from);
+        ka[i][0] = y.x, ka[i][1] = y.y;
       }
     }
   };
@@ -431,18 +389,13 @@ __device__ __forceinline__ void carry_state(const StateWave<DK, NT, DELTA>& m, f
       for (int p = 0; p < 3; ++p)
         if (s < steps) ta[s][p] = m.block(ch, Slot::kT, p, s);
   };
-  int at = 0;  // where the pointers stand
   if (chunks > 0) {
-    point(0);
-    fetch_rows(0);
     if (DELTA) fetch_t(0);
-    sort_rows(0);
-    at = on(0);
-    fetch_rows(at);
+    __syncthreads();
   }
   for (int ch = 0; ch < chunks; ++ch) {
     const int next = min(ch + 1, chunks - 1);
-    whole = next_whole;
+    if (DELTA) get_keys();
     // shares of K S from this wave's rows of S; two planes of S for the outputs
 #pragma unroll
     for (int c = 0; c < NT; ++c) {
@@ -481,9 +434,10 @@ __device__ __forceinline__ void carry_state(const StateWave<DK, NT, DELTA>& m, f
           *reinterpret_cast<float4_t*>(m.lds + L::kShares + ((i * NT + c) * 4 + w) * 1024 + lane * 16) = ks[i];
       }
     }
-    const uint8_t* decays = m.lds + L::kDecays + (ch % 2 * 4 + w) * 128;
+    __syncthreads();
     const float4_t decay = *reinterpret_cast<const float4_t*>(decays + 16 * g);
     const float4_t left = *reinterpret_cast<const float4_t*>(decays + 64 + 16 * g);
+    const float whole = *reinterpret_cast<const float*>(decays + 128);
     float4_t N[NT];
 #pragma unroll
     for (int c = 0; c < NT; ++c) {
@@ -491,50 +445,30 @@ __device__ __forceinline__ void carry_state(const StateWave<DK, NT, DELTA>& m, f
       for (int r = 0; r < 4; ++r)
         N[c][r] = __uint_as_float(
             (uint32_t) * reinterpret_cast<const uint16_t*>(values + (4 * g + r) * L::kRow + (16 * c + n) * 2) << 16);
-      if (!DELTA) {
-        m.template put_rows<3>(m.lds + L::kN, c, N[c] * left);
-        m.template put_rows<1>(m.lds + L::kN + L::kOut, c, N[c]);
-      }
-    }
-    __syncthreads();
-    if (DELTA) {  // R = V - e^G K S
-#pragma unroll
-      for (int c = 0; c < NT; ++c) {
+      if (DELTA) {  // R = V - e^G K S
         float4_t sh[4];
 #pragma unroll
         for (int i = 0; i < 4; ++i)
           sh[i] = *reinterpret_cast<const float4_t*>(m.lds + L::kShares + ((w * NT + c) * 4 + i) * 1024 + lane * 16);
         N[c] -= decay * ((sh[0] + sh[1]) + (sh[2] + sh[3]));
         m.template put_rows<3>(m.lds + L::kR, c, N[c]);
+      } else {
+        m.template put_rows<3>(m.lds + L::kN, c, N[c] * left);
+        m.template put_rows<1>(m.lds + L::kN + L::kOut, c, N[c]);
       }
     }
-    // the wave's rows of K^T: TW elements of 8 tokens' rows, transposed within the lane
     uint4 kt[2][TW];
+    auto get_turned = [&] {
 #pragma unroll
-    for (int s = 0; s < 2; ++s) {
-      uint32_t z[8];
+      for (int s = 0; s < 2; ++s)
 #pragma unroll
-      for (int j = 0; j < 8; ++j) {
-        const uint8_t* from = keys + (32 * s + (j / 4) * 16 + 4 * g + j % 4) * L::kKeyRow + n * TW * 2;
-        if constexpr (TW == 2)
-          z[j] = *reinterpret_cast<const uint32_t*>(from);
-        else
-          z[j] = *reinterpret_cast<const uint16_t*>(from);
-      }
-#pragma unroll
-      for (int i = 0; i < TW; ++i) {
-        uint32_t e[4];
-#pragma unroll
-        for (int j = 0; j < 4; ++j)
-          e[j] = i ? high_halves(z[2 * j], z[2 * j + 1]) : low_halves(z[2 * j], z[2 * j + 1]);
-        kt[s][i] = make_uint4(e[0], e[1], e[2], e[3]);
-      }
-    }
-    sort_rows(ch + 1);  // behind the last chunk: its rows again
-    at = on(at);
-    fetch_rows(at);
+        for (int i = 0; i < TW; ++i)
+          kt[s][i] = *reinterpret_cast<const uint4*>(m.lds + L::kKeysT + (w * L::kTurned + s * TW + i) * 1024 + lane * 16);
+    };
+    if (!DELTA) get_turned();  // before the chunk's last barrier: then the next chunk's are put there
+    __syncthreads();
+    if (DELTA) get_turned();
     if (DELTA) {  // N = T R
-      __syncthreads();
 #pragma unroll
       for (int c = 0; c < NT; ++c) {
         float4_t acc[3] = {{0, 0, 0, 0}, {0, 0, 0, 0}, {0, 0, 0, 0}};
@@ -571,7 +505,6 @@ __device__ __forceinline__ void carry_state(const StateWave<DK, NT, DELTA>& m, f
           for (int i = 0; i < TW; ++i) S[c][i] = mfma_bf16(kt[s][i], u, S[c][i]);
         }
     }
-    if (!DELTA) __syncthreads();
   }
 #pragma unroll
   for (int c = 0; c < NT; ++c)
@@ -581,37 +514,133 @@ __device__ __forceinline__ void carry_state(const StateWave<DK, NT, DELTA>& m, f
       for (int r = 0; r < 4; ++r) st[(int64_t)(r * TW + i) * a.v_dim + 16 * c] = S[c][i][r];
 }
 
+// What comes from memory is fetched a chunk ahead as rows in pieces of 16 bytes,
+// lanes side by side along a row, and the decays one to a lane, and sorted through
+// LDS.  (A load in operand order, 16 rows side by side, takes one turn of the vector
+// cache for each lane, four times as many; a load of 2 bytes a lane as many as one
+// of 16.)
+//
+// Feeding wave w: the chain's left operands, w's quarter of the key rows as they
+// are and transposed, its 16 rows of values and its decays.
+template <int DK, int NT, bool DELTA>
+__device__ __forceinline__ void feed_chain(const StateWave<DK, NT, DELTA>& m) {
+  using L = StateLds<DK, NT, DELTA>;
+  constexpr int TW = DK / 64;
+  constexpr int kPieces = L::kRun / 16, kLoads = kChunk * kPieces / 64;  // of a key row; of a lane
+  const GdnArgs& a = m.a;
+  const int w = m.w, n = m.n, g = m.g, lane = m.lane, chunks = m.chunks;
+  RowPointers<kLoads, const uint16_t> kp;
+  RowPointers<1, const uint16_t> vp;
+  u32x4_t next_k[kLoads], next_v;
+  float next_decay;
+  uint4 kt[2][TW];
+  uint8_t* keys = m.lds + L::kKeys + w * kChunk * L::kKeyRow;
+  const bool has_piece = lane < 32 * NT;
+  const int v_row = lane / (2 * NT) % 16, v_piece = lane % (2 * NT);  // of a row of values
+  const int decay_at = lane < 16 ? Slot::kDecay + (16 * w + n) * 4
+                                 : (lane < 32 ? Slot::kLeft + (16 * w + n) * 4 : Slot::kDecay + 63 * 4);
+  auto point = [&](int ch) {
+    const int64_t row0 = m.first + (int64_t)ch * kChunk;
+    const int last = m.last_of(ch);
+#pragma unroll
+    for (int i = 0; i < kLoads; ++i)
+      kp.p[i] = a.k + (row0 + min((i * 64 + lane) / kPieces, last)) * a.ldk + m.hk * DK + w * (DK / 4) + lane % kPieces * 8;
+    vp.at(a.v + m.col + 8 * v_piece, row0, a.ldv, 16 * w + v_row, last);
+  };
+  auto fetch = [&](int ch) {  // where the pointers stand
+#pragma unroll
+    for (int i = 0; i < kLoads; ++i) next_k[i] = *reinterpret_cast<const u32x4_t*>(kp.p[i]);
+    if (has_piece) next_v = *reinterpret_cast<const u32x4_t*>(vp.p[0]);
+    next_decay = *reinterpret_cast<const float*>(m.ws + ch * m.ws_step + decay_at);
+  };
+  // key rows into LDS; this wave's rows of K^T: TW elements of 8 tokens' rows, transposed within the lane
+  auto sort_keys = [&] {
+#pragma unroll
+    for (int i = 0; i < kLoads; ++i)
+      *reinterpret_cast<u32x4_t*>(keys + (i * 64 + lane) / kPieces * L::kKeyRow + lane % kPieces * 16) = next_k[i];
+#pragma unroll
+    for (int s = 0; s < 2; ++s) {
+      uint32_t z[8];
+#pragma unroll
+      for (int j = 0; j < 8; ++j) {
+        const uint8_t* from = keys + (32 * s + (j / 4) * 16 + 4 * g + j % 4) * L::kKeyRow + n * TW * 2;
+        if constexpr (TW == 2)
+          z[j] = *reinterpret_cast<const uint32_t*>(from);
+        else
+          z[j] = *reinterpret_cast<const uint16_t*>(from);
+      }
+#pragma unroll
+      for (int i = 0; i < TW; ++i) {
+        uint32_t e[4];
+#pragma unroll
+        for (int j = 0; j < 4; ++j)
+          e[j] = i ? high_halves(z[2 * j], z[2 * j + 1]) : low_halves(z[2 * j], z[2 * j + 1]);
+        kt[s][i] = make_uint4(e[0], e[1], e[2], e[3]);
+      }
+    }
+  };
+  auto put_rest = [&] {  // K^T, values and decays, once the chain has read those of the chunk before
+#pragma unroll
+    for (int s = 0; s < 2; ++s)
+#pragma unroll
+      for (int i = 0; i < TW; ++i)
+        *reinterpret_cast<uint4*>(m.lds + L::kKeysT + (w * L::kTurned + s * TW + i) * 1024 + lane * 16) = kt[s][i];
+    if (has_piece) *reinterpret_cast<u32x4_t*>(m.lds + L::kValues + (w * 16 + v_row) * L::kRow + 16 * v_piece) = next_v;
+    if (lane <= 32) reinterpret_cast<float*>(m.lds + L::kDecays + w * 144)[lane] = next_decay;
+  };
+  auto on = [&](int from) {  // the pointers to the next chunk, or to the last one again
+    const int to = min(from + 1, chunks - 1);
+    if (m.last_of(to) == kChunk - 1) {
+      if (to > from) kp.on(a.ldk * kChunk), vp.on(a.ldv * kChunk);
+    } else {
+      point(to);
+    }
+    return to;
+  };
+  if (chunks == 0) return;
+  point(0);
+  fetch(0);
+  sort_keys();
+  put_rest();
+  int at = on(0);  // where the pointers stand
+  fetch(at);
+  __syncthreads();
+  for (int ch = 0; ch < chunks; ++ch) {
+    __syncthreads();
+    __syncthreads();
+    sort_keys();  // the next chunk's; behind the last chunk its own again
+    if (DELTA) __syncthreads();
+    put_rest();
+    at = on(at);
+    fetch(at);
+  }
+}
+
+// Output wave w: tokens 16 w .. 16 w + 15.
 template <int DK, int NT, bool DELTA>
 __device__ __forceinline__ void write_outputs(const StateWave<DK, NT, DELTA>& m) {
   using L = StateLds<DK, NT, DELTA>;
   constexpr int KS = DK / 32;
+  constexpr int kPieces = DK / 8, kLoads = 16 * kPieces / 64;  // of a query row; of a lane
   const GdnArgs& a = m.a;
-  const int w = m.w, n = m.n, g = m.g, chunks = m.chunks;
+  const int w = m.w, n = m.n, g = m.g, lane = m.lane, chunks = m.chunks;
   const int steps = w / 2 + 1;
-  constexpr int kPieces = DK / 8, kLoads = 16 * kPieces / 64;  // of a query row; of a lane, as the chain's rows come
   RowPointers<kLoads, const uint16_t> qp;
   RowPointers<1, uint16_t> op;
   u32x4_t next_q[kLoads];
   uint4 qa[KS], pa[2][2];
   uint8_t* queries = m.lds + L::kQueries + w * 16 * L::kQueryRow;
-  const int o_row = m.lane / (2 * NT) % 16, o_piece = m.lane % (2 * NT);  // as the values come
   uint8_t* results = m.lds + L::kResults + w * 16 * L::kRow;
+  const int o_row = lane / (2 * NT) % 16, o_piece = lane % (2 * NT);  // of a row of results
   auto point = [&](int ch) {
 #pragma unroll
     for (int i = 0; i < kLoads; ++i)
-      qp.p[i] = a.q + (m.first + (int64_t)ch * kChunk + min(16 * w + (i * 64 + m.lane) / kPieces, m.last_of(ch))) * a.ldq +
-                m.hk * DK + m.lane % kPieces * 8;
+      qp.p[i] = a.q + (m.first + (int64_t)ch * kChunk + min(16 * w + (i * 64 + lane) / kPieces, m.last_of(ch))) * a.ldq +
+                m.hk * DK + lane % kPieces * 8;
   };
   auto fetch_q = [&] {  // where the pointers stand
 #pragma unroll
     for (int i = 0; i < kLoads; ++i) next_q[i] = *reinterpret_cast<const u32x4_t*>(qp.p[i]);
-  };
-  auto sort_q = [&] {
-#pragma unroll
-    for (int i = 0; i < kLoads; ++i)
-      *reinterpret_cast<u32x4_t*>(queries + (i * 64 + m.lane) / kPieces * L::kQueryRow + m.lane % kPieces * 16) = next_q[i];
-#pragma unroll
-    for (int s = 0; s < KS; ++s) qa[s] = m.run(reinterpret_cast<const uint16_t*>(queries + n * L::kQueryRow), s);
   };
   auto fetch_p = [&](int ch) {
 #pragma unroll
@@ -619,6 +648,13 @@ __device__ __forceinline__ void write_outputs(const StateWave<DK, NT, DELTA>& m)
 #pragma unroll
       for (int p = 0; p < 2; ++p)
         if (s < steps) pa[s][p] = m.block(ch, Slot::kP, p, s);
+  };
+  auto sort_queries = [&] {
+#pragma unroll
+    for (int i = 0; i < kLoads; ++i)
+      *reinterpret_cast<u32x4_t*>(queries + (i * 64 + lane) / kPieces * L::kQueryRow + lane % kPieces * 16) = next_q[i];
+#pragma unroll
+    for (int s = 0; s < KS; ++s) qa[s] = m.run(reinterpret_cast<const uint16_t*>(queries + n * L::kQueryRow), s);
   };
   auto on = [&](int from) {
     const int to = min(from + 1, chunks - 1);
@@ -629,20 +665,19 @@ __device__ __forceinline__ void write_outputs(const StateWave<DK, NT, DELTA>& m)
     }
     return to;
   };
-  int at = 0;
-  if (chunks > 0) {
-    point(0);
-    op.at(a.out + m.col + 8 * o_piece, m.first, a.ldo, 16 * w + o_row, kChunk);
-    fetch_q();
-    fetch_p(0);
-    sort_q();
-    at = on(0);
-    fetch_q();
-  }
+  if (chunks == 0) return;
+  point(0);
+  op.at(a.out + m.col + 8 * o_piece, m.first, a.ldo, 16 * w + o_row, kChunk);
+  fetch_q();
+  fetch_p(0);
+  sort_queries();
+  int at = on(0);  // where the pointers stand
+  fetch_q();
+  __syncthreads();
   for (int ch = 0; ch < chunks; ++ch) {
     const int last = m.last_of(ch);
     __syncthreads();
-    const float4_t decay = *reinterpret_cast<const float4_t*>(m.lds + L::kDecays + (ch % 2 * 4 + w) * 128 + 16 * g);
+    const float4_t decay = *reinterpret_cast<const float4_t*>(m.lds + L::kDecays + w * 144 + 16 * g);
     float4_t o[NT];
 #pragma unroll
     for (int c = 0; c < NT; ++c) {
@@ -655,13 +690,11 @@ __device__ __forceinline__ void write_outputs(const StateWave<DK, NT, DELTA>& m)
       }
       o[c] = (o[c] + lo) * (decay * a.scale);
     }
-    sort_q();  // the next chunk's
+    __syncthreads();
+    sort_queries();  // the next chunk's; behind the last chunk its own again
     at = on(at);
     fetch_q();
-    if (DELTA) {
-      __syncthreads();
-      __syncthreads();
-    }
+    if (DELTA) __syncthreads();
 #pragma unroll
     for (int c = 0; c < NT; ++c) {
       float4_t lo = {0, 0, 0, 0};
@@ -676,21 +709,20 @@ __device__ __forceinline__ void write_outputs(const StateWave<DK, NT, DELTA>& m)
       o[c] += lo;
     }
     fetch_p(min(ch + 1, chunks - 1));
-    if (!DELTA) __syncthreads();
 #pragma unroll
     for (int c = 0; c < NT; ++c)
 #pragma unroll
       for (int r = 0; r < 4; ++r)
         *reinterpret_cast<uint16_t*>(results + (4 * g + r) * L::kRow + (16 * c + n) * 2) =
             __builtin_bit_cast(uint16_t, (__bf16)o[c][r]);
-    if (m.lane < 32 * NT && 16 * w + o_row <= last)
+    if (lane < 32 * NT && 16 * w + o_row <= last)
       *reinterpret_cast<uint4*>(op.p[0]) = *reinterpret_cast<const uint4*>(results + o_row * L::kRow + 16 * o_piece);
     op.on(a.ldo * kChunk);
   }
 }
 
 template <int DK, int NT, bool DELTA>
-__global__ __launch_bounds__(512, 2) void gdn_state_kernel(GdnArgs a) {
+__global__ __launch_bounds__(768, 3) void gdn_state_kernel(GdnArgs a) {
   using L = StateLds<DK, NT, DELTA>;
   __shared__ __align__(16) uint8_t lds[L::kBytes];
   const int slabs = a.v_dim / (16 * NT);
@@ -700,7 +732,7 @@ __global__ __launch_bounds__(512, 2) void gdn_state_kernel(GdnArgs a) {
   const int slab = (int)(turn % slabs);
   if (pair >= a.B * a.v_heads) return;
   const int b = (int)(pair / a.v_heads), h = (int)(pair % a.v_heads);
-  const int64_t slot = a.index ? a.index[b] : b;
+  const int64_t slot = a.index ? __builtin_amdgcn_readfirstlane(a.index[b]) : b;
   if (slot < 0 || slot >= a.num_states) return;
   const int lane = threadIdx.x % 64, n = lane % 16, g = lane / 16;
   const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x / 64), w = wave % 4;
@@ -710,13 +742,17 @@ __global__ __launch_bounds__(512, 2) void gdn_state_kernel(GdnArgs a) {
                       h * (int64_t)(DELTA ? Slot::kBytesDelta : Slot::kBytesLinear);
   const StateWave<DK, NT, DELTA> m{a, lds, rows.first, rows.count, (rows.count + kChunk - 1) / kChunk,
                                    h / (a.v_heads / a.k_heads), h * a.v_dim + slab * 16 * NT, ws, step, w, lane, n, g};
-  // both halves pass the same barriers: three (two without beta) in each chunk
-  if (wave < 4)
-    carry_state<DK, NT, DELTA>(m, a.state + ((slot * a.v_heads + h) * DK + w * (DK / 4) + 4 * g * (DK / 64)) * (int64_t)a.v_dim +
-                                      slab * 16 * NT + n,
-                               a.has_state && a.has_state[b] != 0);
-  else
+  // all pass the same barriers: one before the chunks and three (two without beta) in each
+  if (wave < 4) {
+    __builtin_amdgcn_s_setprio(3);  // the chain first: the others have time
+    float* st = a.state + ((slot * a.v_heads + h) * DK + w * (DK / 4) + 4 * g * (DK / 64)) * (int64_t)a.v_dim +
+                slab * 16 * NT + n;
+    carry_state<DK, NT, DELTA>(m, st, a.has_state && a.has_state[b] != 0);
+  } else if (wave < 8) {
     write_outputs<DK, NT, DELTA>(m);
+  } else {
+    feed_chain<DK, NT, DELTA>(m);
+  }
 }
 
 size_t gdn_prefill_workspace(int64_t T, int64_t B, int, int v_heads, int, int) {
@@ -734,9 +770,9 @@ static hipError_t launch_prefill(const GdnArgs& a, hipStream_t stream) {
   const bool two = pairs * (a.v_dim / 16) > 4 * kCUs;
   const unsigned grid = (unsigned)(pairs * (a.v_dim / (two ? 32 : 16)));
   if (two)
-    gdn_state_kernel<DK, 2, DELTA><<<grid, 512, 0, stream>>>(a);
+    gdn_state_kernel<DK, 2, DELTA><<<grid, 768, 0, stream>>>(a);
   else
-    gdn_state_kernel<DK, 1, DELTA><<<grid, 512, 0, stream>>>(a);
+    gdn_state_kernel<DK, 1, DELTA><<<grid, 768, 0, stream>>>(a);
   return hipGetLastError();
 }
 
