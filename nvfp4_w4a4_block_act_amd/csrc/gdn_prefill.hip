@@ -17,6 +17,8 @@
 // matrix the six of the nine plane products that are above 2^-24.  What only
 // reaches the bf16 output keeps two planes (16 bits).  Sums accumulate in binary32.
 // G is summed in binary64, so that differences of far decays keep their digits.
+#include <limits.h>
+
 #include <algorithm>
 
 #include "common.hpp"
@@ -86,20 +88,59 @@ __device__ __forceinline__ Rows rows_of(const GdnArgs& a, int b) {
   return {first, (int)(min(max(hi, first), a.T) - first)};
 }
 
+// The sequence that is r-th by length, longest first: workgroups start in turn, and a
+// long sequence that starts late is waited for alone.  (Every order is right; beyond
+// 64 sequences their own is taken.)
+__device__ __forceinline__ int by_length(const GdnArgs& a, int r) {
+  if (a.B > 64) return r;
+  const int lane = threadIdx.x % 64;
+  const int mine = lane < a.B ? a.cu[lane + 1] - a.cu[lane] : INT_MIN;
+  int rank = 0;
+  for (int i = 0; i < (int)a.B; ++i) {
+    const int other = __builtin_amdgcn_readlane(mine, i);
+    rank += other > mine || (other == mine && i < lane) ? 1 : 0;
+  }
+  return __ffsll((unsigned long long)__ballot(lane < a.B && rank == r)) - 1;
+}
+
 // ---- T and P of every chunk ------------------------------------------------------
-// A workgroup takes one chunk of one query/key head and its value heads in turn.
-// Wave w holds rows 16 w .. 16 w + 15 of K K^T and Q K^T.  The inverse: the four
-// 16 x 16 diagonal blocks by substitution, all at once in one wave (lane (n, g):
-// column n of block g), then the blocks below them, T_ij = -T_ii sum_k A_ik T_kj,
-// one diagonal after the other, as fp32 matrix products.
+// A workgroup takes one chunk of one value head; wave w holds rows 16 w .. 16 w + 15 of
+// K K^T and Q K^T.  The inverse: the four 16 x 16 diagonal blocks by substitution,
+// all at once in one wave (lane (n, g): column n of block g), then the blocks below
+// them, T_ij = -T_ii sum_k A_ik T_kj, one diagonal after the other, as fp32 matrix
+// products.  A wave's rows of P and T become operand blocks through LDS rows that no
+// other wave touches meanwhile.
 constexpr int kLd = 68;  // row stride of the 64 x 64 matrices in LDS
+constexpr float kLog2e = 1.44269504088896340736f;
+
+// e^x of a sum of log decays.  x log2(e) is rounded, |x| 2^-24 relative; x e^x is at most
+// 0.37, so the factor is off by 2^-25 of its largest value.
+__device__ __forceinline__ float fade_of(double x) { return __builtin_amdgcn_exp2f((float)x * kLog2e); }
+
+// Four rows' columns 32 s + 4 g + 0 .. 3 and 32 s + 16 + 4 g + 0 .. 3 as operand planes at `to`.
+template <int P>
+__device__ __forceinline__ void put_block(uint8_t* to, int blk, int lane, float4_t x, float4_t y) {
+  uint32_t z[4][P];
+  split_pair(x[0], x[1], z[0]);
+  split_pair(x[2], x[3], z[1]);
+  split_pair(y[0], y[1], z[2]);
+  split_pair(y[2], y[3], z[3]);
+#pragma unroll
+  for (int p = 0; p < P; ++p)
+    *reinterpret_cast<uint4*>(to + (p * kBlocks + blk) * kBlockBytes + lane * 16) =
+        make_uint4(z[0][p], z[1][p], z[2][p], z[3][p]);
+}
 
 template <int DK, bool DELTA>
-__global__ __launch_bounds__(256) void gdn_chunk_kernel(GdnArgs a) {
-  __shared__ float mat[kChunk * kLd], inv[DELTA ? kChunk * kLd : 1];
+__global__ __launch_bounds__(256, 4) void gdn_chunk_kernel(GdnArgs a) {
+  constexpr int kRow = DK * 2 + 16, kPieces = DK / 8, kLoads = kChunk * kPieces / 256;
+  static_assert(kChunk * kRow <= kChunk * kLd * 4, "key and query rows lie where the matrices come");
+  __shared__ __align__(16) float mat[kChunk * kLd], inv[kChunk * kLd];
   __shared__ double sums[kChunk];
-  __shared__ float betas[kChunk];
-  const int hk = blockIdx.y, lane = threadIdx.x % 64, w = threadIdx.x / 64, n = lane % 16, g = lane / 16;
+  __shared__ __align__(16) float betas[kChunk];
+  const int lane = threadIdx.x % 64, n = lane % 16, g = lane / 16;
+  const int w = __builtin_amdgcn_readfirstlane(threadIdx.x / 64);
+  const int hv = blockIdx.y, hk = hv / (a.v_heads / a.k_heads);
   // the sequence whose slots this chunk's index falls into
   const int64_t slot = blockIdx.x;
   int b = -1;
@@ -114,142 +155,144 @@ __global__ __launch_bounds__(256) void gdn_chunk_kernel(GdnArgs a) {
   const int count = min(kChunk, rows.count - chunk * kChunk);
   if (chunk < 0 || count <= 0) return;
   const int64_t row0 = rows.first + (int64_t)chunk * kChunk;
+  uint8_t* to = static_cast<uint8_t*>(a.workspace) +
+                (slot * a.v_heads + hv) * (int64_t)(DELTA ? Slot::kBytesDelta : Slot::kBytesLinear);
+
+  uint8_t* keys = reinterpret_cast<uint8_t*>(mat);
+  uint8_t* queries = reinterpret_cast<uint8_t*>(inv);
+#pragma unroll
+  for (int i = 0; i < kLoads; ++i) {
+    const int r = (i * 256 + (int)threadIdx.x) / kPieces, c = threadIdx.x % kPieces;
+    const int64_t from = row0 + min(r, count - 1);
+    *reinterpret_cast<u32x4_t*>(keys + r * kRow + c * 16) =
+        *reinterpret_cast<const u32x4_t*>(a.k + from * a.ldk + hk * DK + c * 8);
+    *reinterpret_cast<u32x4_t*>(queries + r * kRow + c * 16) =
+        *reinterpret_cast<const u32x4_t*>(a.q + from * a.ldq + hk * DK + c * 8);
+  }
+  if (w == 0) {
+    const int64_t r = row0 + min(lane, count - 1);
+    // below -1000 a factor is 0 in binary32 either way, and the sums stay finite
+    const float step = lane < count ? a.g[r * a.ldg + hv] : 0.0f;
+    double sum = step < -1000.0f ? -1000.0 : (double)step;
+#pragma unroll
+    for (int d = 1; d < 64; d *= 2) {
+      const double x = __shfl_up(sum, d);
+      if (lane >= d) sum += x;
+    }
+    sums[lane] = sum;
+    betas[lane] = DELTA && lane < count ? a.beta[r * a.ldb + hv] : 0.0f;
+    const double all = __shfl(sum, 63);
+    reinterpret_cast<float*>(to + Slot::kDecay)[lane] = fade_of(sum);
+    reinterpret_cast<float*>(to + Slot::kLeft)[lane] = lane < count ? fade_of(all - sum) : 0.0f;
+  }
+  __syncthreads();
 
   // rows 16 w + .. of K K^T and Q K^T against column blocks 0 .. w
   float4_t kk[4], qk[4];
   {
     uint4 ka[DK / 32], qa[DK / 32];
-    const int64_t r = row0 + min(16 * w + n, count - 1);
 #pragma unroll
     for (int s = 0; s < DK / 32; ++s) {
-      ka[s] = *reinterpret_cast<const uint4*>(a.k + r * a.ldk + hk * DK + s * 32 + g * 8);
-      qa[s] = *reinterpret_cast<const uint4*>(a.q + r * a.ldq + hk * DK + s * 32 + g * 8);
+      ka[s] = *reinterpret_cast<const uint4*>(keys + (16 * w + n) * kRow + s * 64 + g * 16);
+      qa[s] = *reinterpret_cast<const uint4*>(queries + (16 * w + n) * kRow + s * 64 + g * 16);
     }
 #pragma unroll
     for (int j = 0; j < 4; ++j) {
       kk[j] = qk[j] = {0, 0, 0, 0};
       if (j > w) continue;
-      const int64_t c = row0 + min(16 * j + n, count - 1);
 #pragma unroll
       for (int s = 0; s < DK / 32; ++s) {
-        const uint4 kb = *reinterpret_cast<const uint4*>(a.k + c * a.ldk + hk * DK + s * 32 + g * 8);
+        const uint4 kb = *reinterpret_cast<const uint4*>(keys + (16 * j + n) * kRow + s * 64 + g * 16);
         if (DELTA) kk[j] = mfma_bf16(ka[s], kb, kk[j]);
         qk[j] = mfma_bf16(qa[s], kb, qk[j]);
       }
     }
   }
-  const int many = a.v_heads / a.k_heads;
-  for (int hv = hk * many; hv < (hk + 1) * many; ++hv) {
-    uint8_t* to = static_cast<uint8_t*>(a.workspace) +
-                  (slot * a.v_heads + hv) * (int64_t)(DELTA ? Slot::kBytesDelta : Slot::kBytesLinear);
-    if (w == 0) {
-      const int64_t r = row0 + min(lane, count - 1);
-      // below -1000 a factor is 0 in binary32 either way, and the sums stay finite
-      const float step = lane < count ? a.g[r * a.ldg + hv] : 0.0f;
-      double sum = step < -1000.0f ? -1000.0 : (double)step;
+  __syncthreads();
+  // P through this wave's rows, then A into them
+  double mine[4];
+  float beta[4];
 #pragma unroll
-      for (int d = 1; d < 64; d *= 2) {
-        const double x = __shfl_up(sum, d);
-        if (lane >= d) sum += x;
-      }
-      sums[lane] = sum;
-      if (DELTA) betas[lane] = lane < count ? a.beta[r * a.ldb + hv] : 0.0f;
-      const double all = __shfl(sum, 63);
-      reinterpret_cast<float*>(to + Slot::kDecay)[lane] = expf((float)sum);
-      reinterpret_cast<float*>(to + Slot::kLeft)[lane] = lane < count ? expf((float)(all - sum)) : 0.0f;
-    }
-    __syncthreads();
-    // A into mat, rows of this wave; P stays in registers
-    float4_t p[4];
-#pragma unroll
-    for (int j = 0; j < 4; ++j) {
-      p[j] = {0, 0, 0, 0};
-      if (j > w) continue;
-#pragma unroll
-      for (int r = 0; r < 4; ++r) {
-        const int row = 16 * w + 4 * g + r, col = 16 * j + n;
-        const float fade = row >= col && row < count ? expf((float)(sums[row] - sums[col])) : 0.0f;
-        p[j][r] = row >= col && row < count ? a.scale * qk[j][r] * fade : 0.0f;
-        if (DELTA) mat[row * kLd + col] = row > col ? betas[row] * kk[j][r] * fade : 0.0f;
-      }
-    }
-    if (DELTA) {
-      __syncthreads();
-      if (w == 0) {  // block g, column n of the diagonal blocks' inverses
-        const float* blk = mat + (16 * g) * kLd + 16 * g;
-        float x[16];
-#pragma unroll
-        for (int i = 0; i < 16; ++i) {
-          float s = i == n ? 1.0f : 0.0f;
-#pragma unroll
-          for (int j = 0; j < i; ++j) s = __builtin_fmaf(-blk[i * kLd + j], x[j], s);
-          x[i] = s;
-        }
-#pragma unroll
-        for (int i = 0; i < 16; ++i) inv[(16 * g + i) * kLd + 16 * g + n] = x[i];
-      }
-      __syncthreads();
-#pragma unroll
-      for (int d = 1; d < 4; ++d) {  // blocks (i, i - d)
-        const int i = w, j = w - d;
-        if (j >= 0) {
-          float4_t m = {0, 0, 0, 0}, t = {0, 0, 0, 0};
-          for (int k = j; k < i; ++k)
-#pragma unroll
-            for (int s = 0; s < 4; ++s)
-              m = __builtin_amdgcn_mfma_f32_16x16x4f32(mat[(16 * i + n) * kLd + 16 * k + 4 * s + g],
-                                                       inv[(16 * k + 4 * s + g) * kLd + 16 * j + n], m, 0, 0, 0);
-          // rows 4 g + r of m are where step r of the next product wants them
-#pragma unroll
-          for (int r = 0; r < 4; ++r)
-            t = __builtin_amdgcn_mfma_f32_16x16x4f32(inv[(16 * i + n) * kLd + 16 * i + 4 * g + r], m[r], t, 0, 0, 0);
-#pragma unroll
-          for (int r = 0; r < 4; ++r) inv[(16 * i + 4 * g + r) * kLd + 16 * j + n] = -t[r];
-        }
-        __syncthreads();
-      }
-    }
-    // P to LDS (over A), then both matrices as operand blocks
-#pragma unroll
-    for (int j = 0; j < 4; ++j) {
-      if (j > w && j / 2 > w / 2) continue;  // a block's second half may lie above the diagonal: zeros
-#pragma unroll
-      for (int r = 0; r < 4; ++r) {
-        mat[(16 * w + 4 * g + r) * kLd + 16 * j + n] = p[j][r];
-        if (DELTA && j > w) inv[(16 * w + 4 * g + r) * kLd + 16 * j + n] = 0.0f;
-      }
-    }
-    __syncthreads();
-#pragma unroll
-    for (int s = 0; s < 2; ++s) {
-      if (s == 1 && w < 2) continue;
-      const int blk = block_of(w, s);
-      const int at = (16 * w + n) * kLd + 32 * s + 4 * g;
-      uint32_t pl[4][kPPlanes], tl[4][kTPlanes];
-#pragma unroll
-      for (int h = 0; h < 2; ++h) {
-        const float4 x = *reinterpret_cast<const float4*>(mat + at + 16 * h);
-        split_pair(x.x, x.y, pl[2 * h]);
-        split_pair(x.z, x.w, pl[2 * h + 1]);
-        if (DELTA) {
-          const float4 y = *reinterpret_cast<const float4*>(inv + at + 16 * h);
-          const float4 bt = *reinterpret_cast<const float4*>(betas + 32 * s + 4 * g + 16 * h);
-          split_pair(y.x * bt.x, y.y * bt.y, tl[2 * h]);
-          split_pair(y.z * bt.z, y.w * bt.w, tl[2 * h + 1]);
-        }
-      }
-#pragma unroll
-      for (int q = 0; q < kPPlanes; ++q)
-        *reinterpret_cast<uint4*>(to + Slot::kP + (q * kBlocks + blk) * kBlockBytes + lane * 16) =
-            make_uint4(pl[0][q], pl[1][q], pl[2][q], pl[3][q]);
-      if (DELTA)
-#pragma unroll
-        for (int q = 0; q < kTPlanes; ++q)
-          *reinterpret_cast<uint4*>(to + Slot::kT + (q * kBlocks + blk) * kBlockBytes + lane * 16) =
-              make_uint4(tl[0][q], tl[1][q], tl[2][q], tl[3][q]);
-    }
-    __syncthreads();
+  for (int r = 0; r < 4; ++r) {
+    mine[r] = sums[16 * w + 4 * g + r];
+    beta[r] = betas[16 * w + 4 * g + r];
   }
+#pragma unroll
+  for (int j = 0; j < 4; ++j) {
+    if (j / 2 > w / 2) continue;  // (a step's second half may lie above the diagonal: zeros)
+    const int col = 16 * j + n;
+    const double theirs = sums[col];
+#pragma unroll
+    for (int r = 0; r < 4; ++r) {
+      const int row = 16 * w + 4 * g + r;
+      const float fade = row >= col && row < count ? fade_of(mine[r] - theirs) : 0.0f;
+      mat[row * kLd + col] = fade != 0.0f ? a.scale * qk[j][r] * fade : 0.0f;
+      kk[j][r] = row > col && fade != 0.0f ? beta[r] * kk[j][r] * fade : 0.0f;
+    }
+  }
+  const int at = (16 * w + n) * kLd + 4 * g;
+#pragma unroll
+  for (int s = 0; s < 2; ++s)
+    if (s <= w / 2)
+      put_block<kPPlanes>(to + Slot::kP, block_of(w, s), lane, *reinterpret_cast<const float4_t*>(mat + at + 32 * s),
+                          *reinterpret_cast<const float4_t*>(mat + at + 32 * s + 16));
+  if (!DELTA) return;
+#pragma unroll
+  for (int j = 0; j < 4; ++j) {
+    if (j / 2 > w / 2) continue;
+#pragma unroll
+    for (int r = 0; r < 4; ++r) {
+      mat[(16 * w + 4 * g + r) * kLd + 16 * j + n] = kk[j][r];
+      if (j > w) inv[(16 * w + 4 * g + r) * kLd + 16 * j + n] = 0.0f;
+    }
+  }
+  __syncthreads();
+  if (w == 0) {  // column n of the inverse of diagonal block g
+    const float* blk = mat + (16 * g) * kLd + 16 * g;
+    float x[16];
+#pragma unroll
+    for (int i = 0; i < 16; ++i) {
+      float s = i == n ? 1.0f : 0.0f;
+#pragma unroll
+      for (int j = 0; j < i; j += 4) {
+        const float4_t l = *reinterpret_cast<const float4_t*>(blk + i * kLd + j);
+#pragma unroll
+        for (int e = 0; e < 4; ++e)
+          if (j + e < i) s = __builtin_fmaf(-l[e], x[j + e], s);
+      }
+      x[i] = s;
+    }
+#pragma unroll
+    for (int i = 0; i < 16; ++i) inv[(16 * g + i) * kLd + 16 * g + n] = x[i];
+  }
+  __syncthreads();
+#pragma unroll
+  for (int d = 1; d < 4; ++d) {  // blocks (w, w - d)
+    const int j = w - d;
+    if (j >= 0) {
+      float4_t m = {0, 0, 0, 0}, t = {0, 0, 0, 0};
+      for (int k = j; k < w; ++k)
+#pragma unroll
+        for (int s = 0; s < 4; ++s)
+          m = __builtin_amdgcn_mfma_f32_16x16x4f32(mat[(16 * w + n) * kLd + 16 * k + 4 * s + g],
+                                                   inv[(16 * k + 4 * s + g) * kLd + 16 * j + n], m, 0, 0, 0);
+      // rows 4 g + r of m are where step r of the next product wants them
+#pragma unroll
+      for (int r = 0; r < 4; ++r)
+        t = __builtin_amdgcn_mfma_f32_16x16x4f32(inv[(16 * w + n) * kLd + 16 * w + 4 * g + r], m[r], t, 0, 0, 0);
+#pragma unroll
+      for (int r = 0; r < 4; ++r) inv[(16 * w + 4 * g + r) * kLd + 16 * j + n] = -t[r];
+    }
+    if (d < 3) __syncthreads();
+  }
+#pragma unroll
+  for (int s = 0; s < 2; ++s)
+    if (s <= w / 2)
+      put_block<kTPlanes>(to + Slot::kT, block_of(w, s), lane,
+                          *reinterpret_cast<const float4_t*>(inv + at + 32 * s) *
+                              *reinterpret_cast<const float4_t*>(betas + 32 * s + 4 * g),
+                          *reinterpret_cast<const float4_t*>(inv + at + 32 * s + 16) *
+                              *reinterpret_cast<const float4_t*>(betas + 32 * s + 16 + 4 * g));
 }
 
 // ---- the state from chunk to chunk -----------------------------------------------
@@ -731,7 +774,7 @@ __global__ __launch_bounds__(768, 3) void gdn_state_kernel(GdnArgs a) {
   const int64_t pair = (turn / slabs) * 8 + blockIdx.x % 8;
   const int slab = (int)(turn % slabs);
   if (pair >= a.B * a.v_heads) return;
-  const int b = (int)(pair / a.v_heads), h = (int)(pair % a.v_heads);
+  const int b = by_length(a, (int)(pair / a.v_heads)), h = (int)(pair % a.v_heads);
   const int64_t slot = a.index ? __builtin_amdgcn_readfirstlane(a.index[b]) : b;
   if (slot < 0 || slot >= a.num_states) return;
   const int lane = threadIdx.x % 64, n = lane % 16, g = lane / 16;
@@ -762,7 +805,7 @@ size_t gdn_prefill_workspace(int64_t T, int64_t B, int, int v_heads, int, int) {
 template <int DK, bool DELTA>
 static hipError_t launch_prefill(const GdnArgs& a, hipStream_t stream) {
   if (a.T > 0) {
-    gdn_chunk_kernel<DK, DELTA><<<dim3((unsigned)chunk_slots(a.T, a.B), a.k_heads), 256, 0, stream>>>(a);
+    gdn_chunk_kernel<DK, DELTA><<<dim3((unsigned)chunk_slots(a.T, a.B), a.v_heads), 256, 0, stream>>>(a);
     const hipError_t e = hipGetLastError();
     if (e != hipSuccess) return e;
   }
