@@ -557,7 +557,7 @@ __device__ __forceinline__ void carry_state(const StateWave<DK, NT, DELTA>& m, f
       for (int r = 0; r < 4; ++r) st[(int64_t)(r * TW + i) * a.v_dim + 16 * c] = S[c][i][r];
 }
 
-// What comes from memory is fetched a chunk ahead as rows in pieces of 16 bytes,
+// What comes from memory is fetched two chunks ahead as rows in pieces of 16 bytes,
 // lanes side by side along a row, and the decays one to a lane, and sorted through
 // LDS.  (A load in operand order, 16 rows side by side, takes one turn of the vector
 // cache for each lane, four times as many; a load of 2 bytes a lane as many as one
@@ -570,16 +570,20 @@ __device__ __forceinline__ void feed_chain(const StateWave<DK, NT, DELTA>& m) {
   using L = StateLds<DK, NT, DELTA>;
   constexpr int TW = DK / 64;
   constexpr int kPieces = L::kRun / 16, kLoads = kChunk * kPieces / 64;  // of a key row; of a lane
+  constexpr int kValuePieces = 2 * NT, kValueLoads = (32 * NT + 63) / 64;  // of a row of values; of a lane
   const GdnArgs& a = m.a;
   const int w = m.w, n = m.n, g = m.g, lane = m.lane, chunks = m.chunks;
   RowPointers<kLoads, const uint16_t> kp;
-  RowPointers<1, const uint16_t> vp;
-  u32x4_t next_k[kLoads], next_v;
-  float next_decay;
+  RowPointers<kValueLoads, const uint16_t> vp;
+  struct Fetched {
+    u32x4_t k[kLoads], v[kValueLoads];
+    float decay;
+  };
+  Fetched even, odd;
   uint4 kt[2][TW];
   uint8_t* keys = m.lds + L::kKeys + w * kChunk * L::kKeyRow;
   const bool has_piece = lane < 32 * NT;
-  const int v_row = lane / (2 * NT) % 16, v_piece = lane % (2 * NT);  // of a row of values
+  const int v_row = lane / kValuePieces % 16, v_piece = lane % kValuePieces;
   const int decay_at = lane < 16 ? Slot::kDecay + (16 * w + n) * 4
                                  : (lane < 32 ? Slot::kLeft + (16 * w + n) * 4 : Slot::kDecay + 63 * 4);
   auto point = [&](int ch) {
@@ -588,19 +592,25 @@ __device__ __forceinline__ void feed_chain(const StateWave<DK, NT, DELTA>& m) {
 #pragma unroll
     for (int i = 0; i < kLoads; ++i)
       kp.p[i] = a.k + (row0 + min((i * 64 + lane) / kPieces, last)) * a.ldk + m.hk * DK + w * (DK / 4) + lane % kPieces * 8;
-    vp.at(a.v + m.col + 8 * v_piece, row0, a.ldv, 16 * w + v_row, last);
-  };
-  auto fetch = [&](int ch) {  // where the pointers stand
 #pragma unroll
-    for (int i = 0; i < kLoads; ++i) next_k[i] = *reinterpret_cast<const u32x4_t*>(kp.p[i]);
-    if (has_piece) next_v = *reinterpret_cast<const u32x4_t*>(vp.p[0]);
-    next_decay = *reinterpret_cast<const float*>(m.ws + ch * m.ws_step + decay_at);
+    for (int i = 0; i < kValueLoads; ++i)
+      vp.p[i] = a.v + m.col + 8 * v_piece + (row0 + min(16 * w + i * (64 / kValuePieces) + v_row, last)) * a.ldv;
   };
-  // key rows into LDS; this wave's rows of K^T: TW elements of 8 tokens' rows, transposed within the lane
-  auto sort_keys = [&] {
+  auto fetch = [&](Fetched& x, int ch) {  // where the pointers stand
+#pragma unroll
+    for (int i = 0; i < kLoads; ++i) x.k[i] = *reinterpret_cast<const u32x4_t*>(kp.p[i]);
+#pragma unroll
+    for (int i = 0; i < kValueLoads; ++i)
+      if (has_piece) x.v[i] = *reinterpret_cast<const u32x4_t*>(vp.p[i]);
+    x.decay = *reinterpret_cast<const float*>(m.ws + ch * m.ws_step + decay_at);
+  };
+  auto put_keys = [&](const Fetched& x) {
 #pragma unroll
     for (int i = 0; i < kLoads; ++i)
-      *reinterpret_cast<u32x4_t*>(keys + (i * 64 + lane) / kPieces * L::kKeyRow + lane % kPieces * 16) = next_k[i];
+      *reinterpret_cast<u32x4_t*>(keys + (i * 64 + lane) / kPieces * L::kKeyRow + lane % kPieces * 16) = x.k[i];
+  };
+  // the wave's rows of K^T: TW elements of 8 tokens' rows, transposed within the lane
+  auto turn_keys = [&] {
 #pragma unroll
     for (int s = 0; s < 2; ++s) {
       uint32_t z[8];
@@ -622,14 +632,18 @@ __device__ __forceinline__ void feed_chain(const StateWave<DK, NT, DELTA>& m) {
       }
     }
   };
-  auto put_rest = [&] {  // K^T, values and decays, once the chain has read those of the chunk before
+  auto put_rest = [&](const Fetched& x) {  // K^T, values and decays, once the chain has read those of the chunk before
 #pragma unroll
     for (int s = 0; s < 2; ++s)
 #pragma unroll
       for (int i = 0; i < TW; ++i)
         *reinterpret_cast<uint4*>(m.lds + L::kKeysT + (w * L::kTurned + s * TW + i) * 1024 + lane * 16) = kt[s][i];
-    if (has_piece) *reinterpret_cast<u32x4_t*>(m.lds + L::kValues + (w * 16 + v_row) * L::kRow + 16 * v_piece) = next_v;
-    if (lane <= 32) reinterpret_cast<float*>(m.lds + L::kDecays + w * 144)[lane] = next_decay;
+#pragma unroll
+    for (int i = 0; i < kValueLoads; ++i)
+      if (has_piece)
+        *reinterpret_cast<u32x4_t*>(m.lds + L::kValues + (w * 16 + i * (64 / kValuePieces) + v_row) * L::kRow +
+                                    16 * v_piece) = x.v[i];
+    if (lane <= 32) reinterpret_cast<float*>(m.lds + L::kDecays + w * 144)[lane] = x.decay;
   };
   auto on = [&](int from) {  // the pointers to the next chunk, or to the last one again
     const int to = min(from + 1, chunks - 1);
@@ -642,20 +656,28 @@ __device__ __forceinline__ void feed_chain(const StateWave<DK, NT, DELTA>& m) {
   };
   if (chunks == 0) return;
   point(0);
-  fetch(0);
-  sort_keys();
-  put_rest();
+  fetch(even, 0);
   int at = on(0);  // where the pointers stand
-  fetch(at);
+  fetch(odd, at);
+  put_keys(even);
+  turn_keys();
+  put_rest(even);
+  at = on(at);
+  fetch(even, at);
   __syncthreads();
-  for (int ch = 0; ch < chunks; ++ch) {
+  auto chunk = [&](Fetched& next) {  // behind the last chunk, its own again
     __syncthreads();
     __syncthreads();
-    sort_keys();  // the next chunk's; behind the last chunk its own again
+    put_keys(next);
+    turn_keys();
     if (DELTA) __syncthreads();
-    put_rest();
+    put_rest(next);
     at = on(at);
-    fetch(at);
+    fetch(next, at);
+  };
+  for (int ch = 0; ch < chunks; ch += 2) {
+    chunk(odd);
+    if (ch + 1 < chunks) chunk(even);
   }
 }
 
@@ -669,21 +691,25 @@ __device__ __forceinline__ void write_outputs(const StateWave<DK, NT, DELTA>& m)
   const int w = m.w, n = m.n, g = m.g, lane = m.lane, chunks = m.chunks;
   const int steps = w / 2 + 1;
   RowPointers<kLoads, const uint16_t> qp;
-  RowPointers<1, uint16_t> op;
-  u32x4_t next_q[kLoads];
+  constexpr int kOutPieces = 2 * NT, kOutStores = (32 * NT + 63) / 64;  // of a row of results; of a lane
+  RowPointers<kOutStores, uint16_t> op;
+  struct Fetched {
+    u32x4_t q[kLoads];
+  };
+  Fetched even, odd;
   uint4 qa[KS], pa[2][2];
   uint8_t* queries = m.lds + L::kQueries + w * 16 * L::kQueryRow;
   uint8_t* results = m.lds + L::kResults + w * 16 * L::kRow;
-  const int o_row = lane / (2 * NT) % 16, o_piece = lane % (2 * NT);  // of a row of results
+  const int o_row = lane / kOutPieces % 16, o_piece = lane % kOutPieces;
   auto point = [&](int ch) {
 #pragma unroll
     for (int i = 0; i < kLoads; ++i)
       qp.p[i] = a.q + (m.first + (int64_t)ch * kChunk + min(16 * w + (i * 64 + lane) / kPieces, m.last_of(ch))) * a.ldq +
                 m.hk * DK + lane % kPieces * 8;
   };
-  auto fetch_q = [&] {  // where the pointers stand
+  auto fetch_q = [&](Fetched& x) {  // where the pointers stand
 #pragma unroll
-    for (int i = 0; i < kLoads; ++i) next_q[i] = *reinterpret_cast<const u32x4_t*>(qp.p[i]);
+    for (int i = 0; i < kLoads; ++i) x.q[i] = *reinterpret_cast<const u32x4_t*>(qp.p[i]);
   };
   auto fetch_p = [&](int ch) {
 #pragma unroll
@@ -692,10 +718,10 @@ __device__ __forceinline__ void write_outputs(const StateWave<DK, NT, DELTA>& m)
       for (int p = 0; p < 2; ++p)
         if (s < steps) pa[s][p] = m.block(ch, Slot::kP, p, s);
   };
-  auto sort_queries = [&] {
+  auto sort_queries = [&](const Fetched& x) {
 #pragma unroll
     for (int i = 0; i < kLoads; ++i)
-      *reinterpret_cast<u32x4_t*>(queries + (i * 64 + lane) / kPieces * L::kQueryRow + lane % kPieces * 16) = next_q[i];
+      *reinterpret_cast<u32x4_t*>(queries + (i * 64 + lane) / kPieces * L::kQueryRow + lane % kPieces * 16) = x.q[i];
 #pragma unroll
     for (int s = 0; s < KS; ++s) qa[s] = m.run(reinterpret_cast<const uint16_t*>(queries + n * L::kQueryRow), s);
   };
@@ -710,14 +736,18 @@ __device__ __forceinline__ void write_outputs(const StateWave<DK, NT, DELTA>& m)
   };
   if (chunks == 0) return;
   point(0);
-  op.at(a.out + m.col + 8 * o_piece, m.first, a.ldo, 16 * w + o_row, kChunk);
-  fetch_q();
+#pragma unroll
+  for (int i = 0; i < kOutStores; ++i)
+    op.p[i] = a.out + m.col + 8 * o_piece + (m.first + 16 * w + i * (64 / kOutPieces) + o_row) * a.ldo;
+  fetch_q(even);
   fetch_p(0);
-  sort_queries();
   int at = on(0);  // where the pointers stand
-  fetch_q();
+  fetch_q(odd);
+  sort_queries(even);
+  at = on(at);
+  fetch_q(even);
   __syncthreads();
-  for (int ch = 0; ch < chunks; ++ch) {
+  auto chunk = [&](int ch, Fetched& next) {
     const int last = m.last_of(ch);
     __syncthreads();
     const float4_t decay = *reinterpret_cast<const float4_t*>(m.lds + L::kDecays + w * 144 + 16 * g);
@@ -734,9 +764,9 @@ __device__ __forceinline__ void write_outputs(const StateWave<DK, NT, DELTA>& m)
       o[c] = (o[c] + lo) * (decay * a.scale);
     }
     __syncthreads();
-    sort_queries();  // the next chunk's; behind the last chunk its own again
+    sort_queries(next);  // behind the last chunk, its own again
     at = on(at);
-    fetch_q();
+    fetch_q(next);
     if (DELTA) __syncthreads();
 #pragma unroll
     for (int c = 0; c < NT; ++c) {
@@ -758,9 +788,17 @@ __device__ __forceinline__ void write_outputs(const StateWave<DK, NT, DELTA>& m)
       for (int r = 0; r < 4; ++r)
         *reinterpret_cast<uint16_t*>(results + (4 * g + r) * L::kRow + (16 * c + n) * 2) =
             __builtin_bit_cast(uint16_t, (__bf16)o[c][r]);
-    if (lane < 32 * NT && 16 * w + o_row <= last)
-      *reinterpret_cast<uint4*>(op.p[0]) = *reinterpret_cast<const uint4*>(results + o_row * L::kRow + 16 * o_piece);
+#pragma unroll
+    for (int i = 0; i < kOutStores; ++i) {
+      const int row = i * (64 / kOutPieces) + o_row;
+      if (lane < 32 * NT && 16 * w + row <= last)
+        *reinterpret_cast<uint4*>(op.p[i]) = *reinterpret_cast<const uint4*>(results + row * L::kRow + 16 * o_piece);
+    }
     op.on(a.ldo * kChunk);
+  };
+  for (int ch = 0; ch < chunks; ch += 2) {
+    chunk(ch, odd);
+    if (ch + 1 < chunks) chunk(ch + 1, even);
   }
 }
 
@@ -811,6 +849,12 @@ static hipError_t launch_prefill(const GdnArgs& a, hipStream_t stream) {
   }
   const int64_t pairs = (a.B * a.v_heads + 7) / 8 * 8;
   const bool two = pairs * (a.v_dim / 16) > 4 * kCUs;
+  if constexpr (!DELTA) {
+    if (a.v_dim % 64 == 0 && two) {
+      gdn_state_kernel<DK, 4, DELTA><<<(unsigned)(pairs * (a.v_dim / 64)), 768, 0, stream>>>(a);
+      return hipGetLastError();
+    }
+  }
   const unsigned grid = (unsigned)(pairs * (a.v_dim / (two ? 32 : 16)));
   if (two)
     gdn_state_kernel<DK, 2, DELTA><<<grid, 768, 0, stream>>>(a);
