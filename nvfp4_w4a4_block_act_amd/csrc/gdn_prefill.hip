@@ -847,19 +847,19 @@ static hipError_t launch_prefill(const GdnArgs& a, hipStream_t stream) {
     const hipError_t e = hipGetLastError();
     if (e != hipSuccess) return e;
   }
+  // A workgroup fills a CU's LDS or its waves, so the launch runs in rounds of one for
+  // each CU; one of 32 columns takes about 1.4 times as long as one of 16, and without
+  // beta one of 64 about 1.6 times as long as one of 32.  As few columns as fit in one round.
   const int64_t pairs = (a.B * a.v_heads + 7) / 8 * 8;
-  const bool two = pairs * (a.v_dim / 16) > 4 * kCUs;
-  if constexpr (!DELTA) {
-    if (a.v_dim % 64 == 0 && two) {
-      gdn_state_kernel<DK, 4, DELTA><<<(unsigned)(pairs * (a.v_dim / 64)), 768, 0, stream>>>(a);
-      return hipGetLastError();
-    }
-  }
-  const unsigned grid = (unsigned)(pairs * (a.v_dim / (two ? 32 : 16)));
-  if (two)
-    gdn_state_kernel<DK, 2, DELTA><<<grid, 768, 0, stream>>>(a);
-  else
+  const bool one_round = pairs * (a.v_dim / 16) <= kCUs;
+  const bool wide = !DELTA && a.v_dim % 64 == 0 && pairs * (a.v_dim / 32) > kCUs;
+  const unsigned grid = (unsigned)(pairs * (a.v_dim / (wide ? 64 : (one_round ? 16 : 32))));
+  if (one_round)
     gdn_state_kernel<DK, 1, DELTA><<<grid, 768, 0, stream>>>(a);
+  else if (!wide)
+    gdn_state_kernel<DK, 2, DELTA><<<grid, 768, 0, stream>>>(a);
+  else if constexpr (!DELTA)
+    gdn_state_kernel<DK, 4, DELTA><<<grid, 768, 0, stream>>>(a);
   return hipGetLastError();
 }
 
