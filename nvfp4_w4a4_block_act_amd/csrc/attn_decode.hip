@@ -59,38 +59,47 @@ static Splits attn_splits(int64_t B, int q_heads, int kv_heads, int64_t max_len,
   return {(int)std::max<int64_t>(1, (span + tokens - 1) / tokens), (int)tokens};
 }
 
+// 16 tokens' keys and values on their way: rows in pieces of 16 bytes, lanes side by side
+// along a row.
 template <int DIM, bool FP8>
 struct Tile {
-  static constexpr int kDwords = DIM * (FP8 ? 1 : 2) / 16;  // of a lane, for keys and for values
-  uint32_t k[kDwords];
-  uint32_t v[4][kDwords / 4];
+  static constexpr int kRow = DIM * (FP8 ? 1 : 2);          // bytes
+  static constexpr int kLanes = kRow / 16;                  // of a row
+  static constexpr int kLoads = kLanes / 4;                 // of a lane, for keys and for values
+  static constexpr int kLdsRow = kRow + 16;                 // 16 rows' pieces fall on different banks
+  static constexpr int kLdsBytes = 2 * 16 * kLdsRow;
+  u32x4_t k[kLoads], v[kLoads];
 };
 
-// 16 tokens' keys and values: `base` is the element offset of the tile's first row.
+// A row of whole cache lines is read once and hinted so (67 x 4099 of 128 bytes: 77 us
+// against 84; 6 x 32768 of 512: 111 against 116); rows of 64 bytes share lines with the
+// next head's, which the hint would drop (95 us against 83).
+template <int ROW>
+__device__ __forceinline__ u32x4_t load_piece(const uint8_t* p) {
+  if constexpr (ROW >= 128) return __builtin_nontemporal_load(reinterpret_cast<const u32x4_t*>(p));
+  return *reinterpret_cast<const u32x4_t*>(p);
+}
+
+// k, v: the tile's first row; offset: the lane's piece of it; step: bytes between a lane's rows.
 template <int DIM, bool FP8>
-__device__ __forceinline__ void load_tile(Tile<DIM, FP8>& t, const uint8_t* k, const uint8_t* v, uint32_t k_off,
-                                          uint32_t v_off, uint32_t v_step) {
-  constexpr int ES = FP8 ? 1 : 2;
+__device__ __forceinline__ void load_tile(Tile<DIM, FP8>& t, const uint8_t* k, const uint8_t* v, uint32_t offset,
+                                          uint32_t step) {
 #pragma unroll
-  for (int i = 0; i < DIM * ES / 64; ++i) {
-    const uint4 w = *reinterpret_cast<const uint4*>(k + k_off + i * 64);
-    t.k[4 * i] = w.x, t.k[4 * i + 1] = w.y, t.k[4 * i + 2] = w.z, t.k[4 * i + 3] = w.w;
-  }
+  for (int i = 0; i < Tile<DIM, FP8>::kLoads; ++i) t.k[i] = load_piece<Tile<DIM, FP8>::kRow>(k + (offset + i * step));
 #pragma unroll
-  for (int r = 0; r < 4; ++r) {
-    const uint8_t* p = v + v_off + r * v_step;
-    if constexpr (DIM * ES == 64) {
-      t.v[r][0] = *reinterpret_cast<const uint32_t*>(p);
-    } else if constexpr (DIM * ES == 128) {
-      const uint2 w = *reinterpret_cast<const uint2*>(p);
-      t.v[r][0] = w.x, t.v[r][1] = w.y;
-    } else {
+  for (int i = 0; i < Tile<DIM, FP8>::kLoads; ++i) t.v[i] = load_piece<Tile<DIM, FP8>::kRow>(v + (offset + i * step));
+}
+
+// The tile into the wave's corner of LDS, keys then values.
+template <int DIM, bool FP8>
+__device__ __forceinline__ void put_tile(const Tile<DIM, FP8>& t, uint8_t* lds) {
+  using Ti = Tile<DIM, FP8>;
+  const int lane = threadIdx.x % 64;
+  uint8_t* to = lds + lane / Ti::kLanes * Ti::kLdsRow + lane % Ti::kLanes * 16;
 #pragma unroll
-      for (int h = 0; h < DIM * ES / 256; ++h) {
-        const uint4 w = *reinterpret_cast<const uint4*>(p + h * 256);
-        t.v[r][4 * h] = w.x, t.v[r][4 * h + 1] = w.y, t.v[r][4 * h + 2] = w.z, t.v[r][4 * h + 3] = w.w;
-      }
-    }
+  for (int i = 0; i < Ti::kLoads; ++i) {
+    *reinterpret_cast<u32x4_t*>(to + i * (64 / Ti::kLanes) * Ti::kLdsRow) = t.k[i];
+    *reinterpret_cast<u32x4_t*>(to + (16 + i * (64 / Ti::kLanes)) * Ti::kLdsRow) = t.v[i];
   }
 }
 
@@ -120,29 +129,51 @@ struct Running {
 // One tile into the running softmax and the outputs.  first, last: tokens of the
 // tile that count.
 template <int DIM, bool FP8>
-__device__ __forceinline__ void take_tile(Tile<DIM, FP8>& t, const bf16x8_t (&q)[DIM / 32], float factor, int first,
+__device__ __forceinline__ void take_tile(const uint8_t* lds, const bf16x8_t (&q)[DIM / 32], float factor, int first,
                                           int last, Running& run, float4_t (&o)[DIM / 16]) {
-  const int g = (threadIdx.x % 64) / 16;
+  using Ti = Tile<DIM, FP8>;
+  constexpr int kValues = Ti::kRow / 64;  // dwords of a lane's run of a value row
+  const int r = threadIdx.x % 16, g = (threadIdx.x % 64) / 16;
   float4_t s = {0, 0, 0, 0};
 #pragma unroll
-  for (int i = 0; i < DIM / 32; ++i) {
-    bf16x8_t a;
-    if constexpr (FP8)
-      a = octet(fp8_pair(t.k[2 * i], false), fp8_pair(t.k[2 * i], true), fp8_pair(t.k[2 * i + 1], false),
-                fp8_pair(t.k[2 * i + 1], true));
-    else
-      a = octet(t.k[4 * i], t.k[4 * i + 1], t.k[4 * i + 2], t.k[4 * i + 3]);
-    s = __builtin_amdgcn_mfma_f32_16x16x32_bf16(a, q[i], s, 0, 0, 0);
+  for (int i = 0; i < Ti::kRow / 64; ++i) {
+    const uint4 w = *reinterpret_cast<const uint4*>(lds + r * Ti::kLdsRow + i * 64 + g * 16);
+    if constexpr (FP8) {
+      s = __builtin_amdgcn_mfma_f32_16x16x32_bf16(
+          octet(fp8_pair(w.x, false), fp8_pair(w.x, true), fp8_pair(w.y, false), fp8_pair(w.y, true)), q[2 * i], s, 0, 0, 0);
+      s = __builtin_amdgcn_mfma_f32_16x16x32_bf16(
+          octet(fp8_pair(w.z, false), fp8_pair(w.z, true), fp8_pair(w.w, false), fp8_pair(w.w, true)), q[2 * i + 1], s, 0, 0,
+          0);
+    } else {
+      s = __builtin_amdgcn_mfma_f32_16x16x32_bf16(octet(w.x, w.y, w.z, w.w), q[i], s, 0, 0, 0);
+    }
+  }
+  uint32_t v[4][kValues];
+#pragma unroll
+  for (int j = 0; j < 4; ++j) {
+    const uint8_t* p = lds + (16 + g * 4 + j) * Ti::kLdsRow + (Ti::kRow < 256 ? Ti::kRow / 16 : 16) * r;
+    if constexpr (kValues == 1) {
+      v[j][0] = *reinterpret_cast<const uint32_t*>(p);
+    } else if constexpr (kValues == 2) {
+      const uint2 w = *reinterpret_cast<const uint2*>(p);
+      v[j][0] = w.x, v[j][1] = w.y;
+    } else {
+#pragma unroll
+      for (int h = 0; h < kValues / 4; ++h) {
+        const uint4 w = *reinterpret_cast<const uint4*>(p + h * 256);
+        v[j][4 * h] = w.x, v[j][4 * h + 1] = w.y, v[j][4 * h + 2] = w.z, v[j][4 * h + 3] = w.w;
+      }
+    }
   }
 #pragma unroll
-  for (int r = 0; r < 4; ++r) s[r] *= factor;
+  for (int j = 0; j < 4; ++j) s[j] *= factor;
   if (first > 0 || last < 16) {  // uniform: the tiles at either end
 #pragma unroll
-    for (int r = 0; r < 4; ++r) {
-      if (g * 4 + r < first || g * 4 + r >= last) {
-        s[r] = -INFINITY;
+    for (int j = 0; j < 4; ++j) {
+      if (g * 4 + j < first || g * 4 + j >= last) {
+        s[j] = -INFINITY;
 #pragma unroll
-        for (int x = 0; x < Tile<DIM, FP8>::kDwords / 4; ++x) t.v[r][x] = 0;  // whatever the row holds, 0 times it is 0
+        for (int x = 0; x < kValues; ++x) v[j][x] = 0;  // whatever the row holds, 0 times it is 0
       }
     }
   }
@@ -158,9 +189,9 @@ __device__ __forceinline__ void take_tile(Tile<DIM, FP8>& t, const bf16x8_t (&q)
   }
   float p[4], rest[4];
 #pragma unroll
-  for (int r = 0; r < 4; ++r) {
-    p[r] = __builtin_amdgcn_exp2f(s[r] - run.m);
-    run.l += p[r];
+  for (int j = 0; j < 4; ++j) {
+    p[j] = __builtin_amdgcn_exp2f(s[j] - run.m);
+    run.l += p[j];
   }
   const f32x2_t p01 = {p[0], p[1]}, p23 = {p[2], p[3]};
   const uint32_t h01 = __builtin_bit_cast(uint32_t, __builtin_convertvector(p01, bf16x2_t));
@@ -173,23 +204,23 @@ __device__ __forceinline__ void take_tile(Tile<DIM, FP8>& t, const bf16x8_t (&q)
       short4_t, make_uint2(__builtin_bit_cast(uint32_t, __builtin_convertvector(r01, bf16x2_t)),
                            __builtin_bit_cast(uint32_t, __builtin_convertvector(r23, bf16x2_t))));
   auto product = [&](int i, uint32_t v01, uint32_t v23) {
-    const short4_t v = __builtin_bit_cast(short4_t, make_uint2(v01, v23));
-    o[i] = __builtin_amdgcn_mfma_f32_16x16x16bf16_1k(v, lo, o[i], 0, 0, 0);
-    o[i] = __builtin_amdgcn_mfma_f32_16x16x16bf16_1k(v, hi, o[i], 0, 0, 0);
+    const short4_t x = __builtin_bit_cast(short4_t, make_uint2(v01, v23));
+    o[i] = __builtin_amdgcn_mfma_f32_16x16x16bf16_1k(x, lo, o[i], 0, 0, 0);
+    o[i] = __builtin_amdgcn_mfma_f32_16x16x16bf16_1k(x, hi, o[i], 0, 0, 0);
   };
 #pragma unroll
-  for (int x = 0; x < Tile<DIM, FP8>::kDwords / 4; ++x) {
+  for (int x = 0; x < kValues; ++x) {
     if constexpr (FP8) {
       uint32_t a[4], b[4];
 #pragma unroll
-      for (int r = 0; r < 4; ++r) a[r] = fp8_pair(t.v[r][x], false), b[r] = fp8_pair(t.v[r][x], true);
+      for (int j = 0; j < 4; ++j) a[j] = fp8_pair(v[j][x], false), b[j] = fp8_pair(v[j][x], true);
       product(4 * x, low_halves(a[0], a[1]), low_halves(a[2], a[3]));
       product(4 * x + 1, high_halves(a[0], a[1]), high_halves(a[2], a[3]));
       product(4 * x + 2, low_halves(b[0], b[1]), low_halves(b[2], b[3]));
       product(4 * x + 3, high_halves(b[0], b[1]), high_halves(b[2], b[3]));
     } else {
-      product(2 * x, low_halves(t.v[0][x], t.v[1][x]), low_halves(t.v[2][x], t.v[3][x]));
-      product(2 * x + 1, high_halves(t.v[0][x], t.v[1][x]), high_halves(t.v[2][x], t.v[3][x]));
+      product(2 * x, low_halves(v[0][x], v[1][x]), low_halves(v[2][x], v[3][x]));
+      product(2 * x + 1, high_halves(v[0][x], v[1][x]), high_halves(v[2][x], v[3][x]));
     }
   }
 }
@@ -208,13 +239,17 @@ __device__ __forceinline__ int64_t part_row(const AttnArgs& a, int b, int head, 
 }
 
 template <int DIM, bool FP8, int kWaves>
-__global__ __launch_bounds__(kWaves * 64) void attn_decode_kernel(AttnArgs a, int splits, int split_tokens) {
+__global__ __launch_bounds__(kWaves * 64, 2) void attn_decode_kernel(AttnArgs a, int splits, int split_tokens) {
   constexpr int ES = FP8 ? 1 : 2, PAD = DIM + 4;
   const int group = a.q_heads / a.cache.kv_heads, per = (group + 15) / 16;
-  const int kvh = blockIdx.x / per, head0 = kvh * group + (blockIdx.x % per) * 16;
+  const int gx = a.cache.kv_heads * per;
+  const uint32_t xcd_turn = blockIdx.x / 8, which = xcd_turn % gx, item = (xcd_turn / gx) * 8 + blockIdx.x % 8;
+  const int kvh = which / per, head0 = kvh * group + (which % per) * 16;
   const int heads = min(16, (kvh + 1) * group - head0);
-  const int split = blockIdx.y, b = blockIdx.z;
-  const int lane = threadIdx.x % 64, wave = threadIdx.x / 64, r = lane % 16, g = lane / 16;
+  const int split = item % splits, b = item / splits;
+  if (b >= a.B) return;
+  const int lane = threadIdx.x % 64, r = lane % 16, g = lane / 16;
+  const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x / 64);
   const nvfp4_kv_cache& c = a.cache;
 
   const int len = min(max(a.lens[b], 0), a.max_len);
@@ -236,11 +271,13 @@ __global__ __launch_bounds__(kWaves * 64) void attn_decode_kernel(AttnArgs a, in
   const float factor = a.scale * (FP8 ? *c.k_amax / 448.0f : 1.0f) * kLog2e;
   const uint8_t* kc = static_cast<const uint8_t*>(c.k) + (int64_t)kvh * c.head_stride * ES;
   const uint8_t* vc = static_cast<const uint8_t*>(c.v) + (int64_t)kvh * c.head_stride * ES;
+  using Ti = Tile<DIM, FP8>;
   const uint32_t row = (uint32_t)c.token_stride * ES;
-  const uint32_t k_off = r * row + g * 16;
-  const uint32_t v_off = g * 4 * row + (uint32_t)min(DIM * ES / 16, 16) * r;
+  const uint32_t offset = lane / Ti::kLanes * row + lane % Ti::kLanes * 16, step = 64 / Ti::kLanes * row;
   const int tiles_per_page = c.page_size / 16;
 
+  extern __shared__ float4_t dynamic_lds[];
+  uint8_t* corner = reinterpret_cast<uint8_t*>(dynamic_lds) + wave * Ti::kLdsBytes;  // the wave's own, for one tile
   Running run = {kNone, 0};
   float4_t o[DIM / 16];
 #pragma unroll
@@ -248,7 +285,7 @@ __global__ __launch_bounds__(kWaves * 64) void attn_decode_kernel(AttnArgs a, in
 
   // tiles of this wave: from / 16 + wave + kWaves * n
   const int tile0 = from / 16 + wave, tile_end = (to + 15) / 16;
-  const int mine = tile0 < tile_end ? (tile_end - tile0 + kWaves - 1) / kWaves : 0;
+  const int mine = tile0 < tile_end && c.num_pages > 0 ? (tile_end - tile0 + kWaves - 1) / kWaves : 0;
   for (int n0 = 0; n0 < mine; n0 += 64) {
     // page and place in it of 64 tiles ahead, one in each lane
     const int ahead = min(n0 + lane, mine - 1) * kWaves + tile0;
@@ -256,27 +293,22 @@ __global__ __launch_bounds__(kWaves * 64) void attn_decode_kernel(AttnArgs a, in
     const int page = a.table[(int64_t)b * a.ldt + page_index];
     const int inside = ahead - page_index * tiles_per_page;
     const int count = min(64, mine - n0);
-    Tile<DIM, FP8> buf[2];
-    auto fetch = [&](Tile<DIM, FP8>& t, int n) {
+    // loads are unconditional (of the last tile again behind the end, and of page 0 for a
+    // page outside the pool, whose tokens are masked): the next tile's are in flight
+    // while one is computed
+    Ti tile;
+    auto fetch = [&](int n) {
       const int p = __builtin_amdgcn_readlane(page, n), in = __builtin_amdgcn_readlane(inside, n);
-      if (p < 0 || p >= c.num_pages) return;
-      const int64_t at = ((int64_t)p * c.page_stride + (int64_t)in * 16 * c.token_stride) * ES;
-      load_tile<DIM, FP8>(t, kc + at, vc + at, k_off, v_off, row);
+      const int64_t at = ((int64_t)(p < 0 || p >= c.num_pages ? 0 : p) * c.page_stride + (int64_t)in * 16 * c.token_stride) * ES;
+      load_tile<DIM, FP8>(tile, kc + at, vc + at, offset, step);
     };
-    auto take = [&](Tile<DIM, FP8>& t, int n) {
+    fetch(0);
+    for (int n = 0; n < count; ++n) {
       const int p = __builtin_amdgcn_readlane(page, n);
-      if (p < 0 || p >= c.num_pages) return;
       const int start = (tile0 + (n0 + n) * kWaves) * 16;
-      take_tile<DIM, FP8>(t, q, factor, begin - start, len - start, run, o);
-    };
-    fetch(buf[0], 0);
-    for (int n = 0; n < count; n += 2) {
-      if (n + 1 < count) fetch(buf[1], n + 1);
-      take(buf[0], n);
-      if (n + 1 < count) {
-        if (n + 2 < count) fetch(buf[0], n + 2);
-        take(buf[1], n + 1);
-      }
+      put_tile<DIM, FP8>(tile, corner);
+      fetch(min(n + 1, count - 1));
+      take_tile<DIM, FP8>(corner, q, factor, begin - start, p < 0 || p >= c.num_pages ? 0 : len - start, run, o);
     }
   }
   run.l += __shfl_xor(run.l, 16);
@@ -284,8 +316,8 @@ __global__ __launch_bounds__(kWaves * 64) void attn_decode_kernel(AttnArgs a, in
 
   // the waves' results, joined in LDS
   __shared__ float ms[kWaves][16], ls[kWaves][16];
-  extern __shared__ float4_t dynamic_lds[];
-  float* os = reinterpret_cast<float*>(dynamic_lds);  // [wave][heads][PAD]
+  float* os = reinterpret_cast<float*>(dynamic_lds);  // [wave][heads][PAD], over the waves' corners
+  __syncthreads();
   if (r < heads) {
     if (g == 0) ms[wave][r] = run.m, ls[wave][r] = run.l;
 #pragma unroll
@@ -299,7 +331,7 @@ __global__ __launch_bounds__(kWaves * 64) void attn_decode_kernel(AttnArgs a, in
   __syncthreads();
   const float vg = FP8 ? *c.v_amax / 448.0f : 1.0f;
   float* parts = static_cast<float*>(a.workspace);
-  float2* heads_ml = reinterpret_cast<float2*>(parts + part_row(a, (int)gridDim.z, 0, splits, 0) * DIM);
+  float2* heads_ml = reinterpret_cast<float2*>(parts + part_row(a, (int)a.B, 0, splits, 0) * DIM);
   for (int e = threadIdx.x * 4; e < heads * DIM; e += kWaves * 64 * 4) {
     const int h = e / DIM, d = e % DIM;
     float top = kNone, sum = 0;
@@ -325,11 +357,11 @@ __global__ __launch_bounds__(kWaves * 64) void attn_decode_kernel(AttnArgs a, in
   }
 }
 
-// Joins the splits of one query head: each counts 2^(its m - the largest m).  Sixteen
-// groups of DIM / 4 threads take the splits in turn, then one group their sums.
-template <int DIM, bool FP8>
-__global__ __launch_bounds__(DIM * 4) void attn_join_kernel(AttnArgs a, int splits, int split_tokens) {
-  constexpr int kLanes = DIM / 4, kGroups = 16;
+// Joins the splits of one query head: each counts 2^(its m - the largest m).  Groups of
+// DIM / 4 threads take the splits in turn, then one group their sums.
+template <int DIM, bool FP8, int kGroups>
+__global__ __launch_bounds__(DIM / 4 * kGroups) void attn_join_kernel(AttnArgs a, int splits, int split_tokens) {
+  constexpr int kLanes = DIM / 4;
   const int h = blockIdx.x, b = blockIdx.y, d = threadIdx.x % kLanes, grp = threadIdx.x / kLanes;
   const int len = min(max(a.lens[b], 0), a.max_len);
   const int start = a.window > 0 ? max(0, len - a.window) / 16 * 16 : 0;
@@ -378,8 +410,9 @@ size_t attn_decode_workspace(int64_t B, int q_heads, int kv_heads, int head_dim,
 template <int DIM, bool FP8, int kWaves>
 static hipError_t launch_waves(const AttnArgs& a, const Splits& s, hipStream_t stream) {
   const int group = a.q_heads / a.cache.kv_heads;
-  const dim3 grid(a.cache.kv_heads * ((group + 15) / 16), s.count, (unsigned)a.B);
-  const size_t lds = (size_t)kWaves * std::min(group, 16) * (DIM + 4) * sizeof(float);
+  const dim3 grid((unsigned)(a.cache.kv_heads * ((group + 15) / 16) * ((a.B * s.count + 7) / 8 * 8)));
+  const size_t lds = std::max<size_t>((size_t)kWaves * std::min(group, 16) * (DIM + 4) * sizeof(float),
+                                      (size_t)kWaves * Tile<DIM, FP8>::kLdsBytes);
   hipError_t e = hipSuccess;
   if (lds > 48 * 1024)  // above the default bound of dynamic LDS: many heads of 256
     e = hipFuncSetAttribute(reinterpret_cast<const void*>(&attn_decode_kernel<DIM, FP8, kWaves>),
@@ -396,7 +429,11 @@ static hipError_t launch_dim(const AttnArgs& a, hipStream_t stream) {
   const bool few = s.count == 1 && a.B * a.q_heads <= 2 * kCUs;
   hipError_t e = few ? launch_waves<DIM, FP8, 8>(a, s, stream) : launch_waves<DIM, FP8, 4>(a, s, stream);
   if (e != hipSuccess || s.count == 1) return e;
-  attn_join_kernel<DIM, FP8><<<dim3(a.q_heads, (unsigned)a.B), DIM * 4, 0, stream>>>(a, s.count, s.tokens);
+  const dim3 rows(a.q_heads, (unsigned)a.B);
+  if (s.count <= 16)
+    attn_join_kernel<DIM, FP8, 4><<<rows, DIM, 0, stream>>>(a, s.count, s.tokens);
+  else
+    attn_join_kernel<DIM, FP8, 16><<<rows, DIM * 4, 0, stream>>>(a, s.count, s.tokens);
   return hipGetLastError();
 }
 
