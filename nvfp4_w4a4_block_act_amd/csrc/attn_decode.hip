@@ -44,15 +44,20 @@ constexpr float kSlack = 8.0f;
 constexpr float kLog2e = 1.44269504088896340736f, kLn2 = 0.69314718055994530942f;
 constexpr int kSplitTokens = 512;          // fewest tokens of a split
 
-// Splits of a sequence, from sizes the host knows: about sixteen workgroups for each
-// CU (uneven lengths even out over them), none with fewer than kSplitTokens tokens.
+// Splits of a sequence, from sizes the host knows: about eight workgroups for each CU
+// (uneven lengths even out over them), none with fewer than kSplitTokens tokens.
+// Sixteen for each CU took 60 us against 51 for 160 sequences of up to 1024 and 78
+// against 77 for 67 of up to 4099; splits of 256 or 1024 tokens 86 and 90 us there.
+// Equal shares of all sequences' tiles, as many as the GPU holds at once, taken from the
+// lengths on the device, were no faster there (81 us) and slower for few sequences (one of
+// 32768: 27 us against 22).
 struct Splits {
   int count, tokens;  // tokens of one split: a multiple of 16
 };
 static Splits attn_splits(int64_t B, int q_heads, int kv_heads, int64_t max_len, int64_t window) {
   const int64_t span = window > 0 && window < max_len ? window + 15 : max_len;
   const int64_t rows = B * kv_heads * ((q_heads / kv_heads + 15) / 16);
-  const int64_t want = std::max<int64_t>(1, (int64_t)kCUs * 16 / rows);
+  const int64_t want = std::max<int64_t>(1, (int64_t)kCUs * 8 / rows);
   const int64_t most = std::max<int64_t>(1, span / kSplitTokens);
   const int64_t n = std::min(want, most);
   const int64_t tokens = std::max<int64_t>(16, (span + n - 1) / n + 15) / 16 * 16;
