@@ -73,9 +73,34 @@ class Case:
         assert np.array_equal(state[kept], self.state[kept].astype(np.float64)), f"{what}: other states changed"
 
 
+@pytest.mark.parametrize("batch", [40, 140])
+def test_step_of_large_states(batch):
+    """States of 80 MB (hinted loads) and 280 MB (stores too): the first and last sequences
+    against the oracle, and all of them against the same tokens one sequence at a time."""
+    g = torch.Generator(DEV).manual_seed(batch)
+    c = Case(2, 16, 32, 128, 128, True, 2, seed=batch)
+    small = c.dev()
+    rep = [x.repeat_interleave(batch // 2, 0).contiguous() for x in small]
+    order = torch.randperm(batch, device=DEV, generator=g).int()
+    state = torch.empty_like(rep[5])
+    state[order.long()] = rep[5]
+    out = nv.gdn_step(*rep[:5], state, state_index=order)
+    one = nv.gdn_step(*small)
+    torch.cuda.synchronize()
+    c.check(one, small[5], None, [0, 1, 2], np.ones(2), 128 ** -0.5)
+    # the sums of the rows are taken in another order than for two sequences: a few roundings apart
+    want = small[5].repeat_interleave(batch // 2, 0)
+    d = (state[order.long()] - want).flatten(1).norm(dim=1)
+    assert (d <= 16 * 2.0 ** -24 * want.flatten(1).norm(dim=1)).all()
+    for b in range(batch):
+        assert torch.equal(out[b], out[b // (batch // 2) * (batch // 2)])
+    d = (out.double() - one.repeat_interleave(batch // 2, 0).double()).abs()
+    assert (d <= 2.0 ** -7 * out.double().abs() + 1e-5).all()
+
+
 @pytest.mark.parametrize("delta", [True, False])
 @pytest.mark.parametrize("B,Hk,Hv,Dk,Dv", [(1, 16, 32, 128, 128), (5, 2, 6, 64, 32), (33, 4, 4, 128, 64), (3, 1, 2, 128, 1024),
-                                           (7, 2, 2, 64, 96)])
+                                           (7, 2, 2, 64, 96), (130, 2, 4, 64, 128), (70, 8, 8, 128, 256)])
 def test_step(B, Hk, Hv, Dk, Dv, delta):
     say(f"[gdn] step B={B} heads={Hk}/{Hv} dims={Dk}x{Dv} delta={delta}")
     c = Case(B, Hk, Hv, Dk, Dv, delta, B + 2, seed=B + Dv, wide=B % 2 == 1)
