@@ -7,8 +7,13 @@
 // one item: 16-byte loads, x1' = fl(fl(x1 c) - fl(x2 s)), x2' = fl(fl(x2 c) +
 // fl(x1 s)) (contraction is off, so results are bit-exact), a rounding to bf16
 // (the cache codec's input type, and what the attention reads), and for an E4M3
-// cache the codec's own steps.  Bound by HBM: the rows in, the rows out and one
-// table row for each token; a token's heads find the table row in the caches.
+// cache the codec's own steps.  A workgroup takes one token, a thread for each item
+// (up to 512), so that no wave runs a second, partly empty trip.  Bound by HBM: the
+// rows in, the rows out and one table row for each token; a token's heads find the table
+// row in the caches.  32768 tokens of 40 + 2 x 8 heads of 128, fp32 to FP8: 221 us,
+// 6.1 TB/s (245 us with 256 threads a token; hinted loads 254, stores too 242).
+#include <algorithm>
+
 #include "common.hpp"
 #include "kv_codec.hpp"
 #include "mixers.hpp"
@@ -52,7 +57,7 @@ __device__ __forceinline__ uint2 coded_run(uint4 w, float g) {
 }
 
 template <bool F32, bool FP8>
-__global__ __launch_bounds__(256) void kv_append_kernel(AppendArgs a) {
+__global__ __launch_bounds__(512) void kv_append_kernel(AppendArgs a) {
   const int64_t t = blockIdx.x;
   const nvfp4_kv_cache& c = a.cache;
   const int64_t slot = a.slots[t];
@@ -122,7 +127,8 @@ __global__ __launch_bounds__(256) void kv_append_kernel(AppendArgs a) {
 }
 
 hipError_t launch_kv_append(const AppendArgs& a, hipStream_t stream) {
-  const dim3 grid((unsigned)a.T), block(256);
+  const int64_t items = (int64_t)((a.q ? a.q_heads : 0) + 2 * a.cache.kv_heads) * (a.cache.head_dim / 16);
+  const dim3 grid((unsigned)a.T), block((unsigned)std::min<int64_t>(512, (items + 63) / 64 * 64));
   const bool fp8 = a.cache.dtype == NVFP4_E4M3;
   if (a.src_f32 && fp8)
     kv_append_kernel<true, true><<<grid, block, 0, stream>>>(a);
