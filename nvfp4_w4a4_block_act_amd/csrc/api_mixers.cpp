@@ -15,6 +15,7 @@ using namespace nvfp4::checks;
 
 constexpr int64_t kMaxStride = (int64_t)1 << 40;  // cache strides, in elements: extents stay inside int64
 constexpr int kMaxHeads = 1 << 16;
+constexpr int64_t kMaxGroups = 1 << 22;  // workgroups of a launch: at most 2^32 threads
 
 size_t cache_elem(const nvfp4_kv_cache& c) { return c.dtype == NVFP4_E4M3 ? 1 : 2; }
 
@@ -76,6 +77,7 @@ nvfp4_status check_append(const nvfp4::AppendArgs& a, int32_t src_dtype, const n
   if (a.rot < 0 || a.rot > dim || a.rot % 16 != 0 || a.T >= kMaxDim || a.max_pos >= kMaxDim || a.q_heads > kMaxHeads)
     return NVFP4_ESHAPE;
   if (!ld_ok(a.ldk, kv) || !ld_ok(a.ldv, kv) || (a.q && (!ld_ok(a.ldq, qw) || !ld_ok(a.ldqo, qw)))) return NVFP4_ESHAPE;
+  if (a.T > kMaxGroups) return NVFP4_ESHAPE;
   if (a.T == 0) return NVFP4_OK;
   if (!a.k || !a.v || !a.slots || (a.rot > 0 && (!a.rope || !a.positions))) return NVFP4_EINVAL;
   const int elem = src_dtype == NVFP4_F32 ? 4 : 2, unit = 16 / elem;
@@ -106,8 +108,7 @@ nvfp4_status check_attn(const nvfp4::AttnArgs& a, const nvfp4_kv_cache* cache, i
       window >= kMaxDim || !ld_ok(a.ldq, width) || !ld_ok(a.ldo, width) || a.ldt < 0 || a.ldt >= kMaxDim ||
       a.ldt < (max_len + cache->page_size - 1) / cache->page_size)
     return NVFP4_ESHAPE;
-  // the launch's grid: a workgroup for each sequence and key-value head
-  if (a.B > 65535) return NVFP4_ESHAPE;
+  if (a.B > 65535 || (a.B + 7) * a.q_heads > kMaxGroups) return NVFP4_ESHAPE;
   if (a.B == 0) return NVFP4_OK;
   if (!a.q || !a.out || !a.lens || (max_len > 0 && !a.table)) return NVFP4_EINVAL;
   if (!all_aligned({a.q, a.out, a.lse, a.lens, a.table})) return NVFP4_EALIGN;
@@ -138,7 +139,7 @@ nvfp4_status check_gdn(const nvfp4::GdnArgs& a, bool prefill, size_t workspace_b
   if ((a.k_dim != 64 && a.k_dim != 128) || a.v_dim < 32 || a.v_dim > 1024 || a.v_dim % 32 != 0) return NVFP4_ESHAPE;
   if (a.v_heads % a.k_heads != 0 || a.v_heads > 65535 || rows >= kMaxDim || a.B > 65535 || a.num_states >= kMaxDim)
     return NVFP4_ESHAPE;
-  if (a.B * a.v_heads * (a.v_dim / 16) >= kMaxDim) return NVFP4_ESHAPE;  // workgroups of a launch
+  if ((a.B * a.v_heads + 7) * (a.v_dim / 16) > kMaxGroups || a.T / 64 > kMaxGroups) return NVFP4_ESHAPE;
   if (!a.index && a.num_states < a.B) return NVFP4_ESHAPE;
   const int64_t kw = (int64_t)a.k_heads * a.k_dim, vw = (int64_t)a.v_heads * a.v_dim;
   if (!ld_ok(a.ldq, kw) || !ld_ok(a.ldk, kw) || !ld_ok(a.ldv, vw) || !ld_ok(a.ldo, vw) || !ld_ok(a.ldg, a.v_heads) ||
