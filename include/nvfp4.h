@@ -404,7 +404,7 @@ nvfp4_status nvfp4_kv_append(const void* q, const void* k, const void* v, int32_
  *   q          bf16 [B][q_heads][head_dim], row stride ldq (multiple of 8).
  *   block_table int32 [B][ldt], ldt >= ceil(max_len / page_size).
  *   max_len    upper bound of the lengths, known on the host (a looser bound
- *              costs little); below 2^31.
+ *              costs little); at most 2^30.
  *   out        bf16, row stride ldo (multiple of 8); lse fp32 [B][q_heads] or NULL.
  *   workspace  device scratch of nvfp4_attn_decode_workspace_bytes (contents need
  *              no setup; NULL allowed when that is 0): the partial results of long

@@ -15,6 +15,7 @@ using namespace nvfp4::checks;
 
 constexpr int64_t kMaxStride = (int64_t)1 << 40;  // cache strides, in elements: extents stay inside int64
 constexpr int kMaxHeads = 1 << 16;
+constexpr int64_t kMaxLen = (int64_t)1 << 30;     // token index plus a split's tokens stay inside int32
 constexpr int64_t kMaxGroups = 1 << 22;  // workgroups of a launch: at most 2^32 threads
 
 size_t cache_elem(const nvfp4_kv_cache& c) { return c.dtype == NVFP4_E4M3 ? 1 : 2; }
@@ -104,7 +105,7 @@ nvfp4_status check_attn(const nvfp4::AttnArgs& a, const nvfp4_kv_cache* cache, i
   if (s != NVFP4_OK) return s;
   if (a.B < 0 || a.q_heads < 1 || max_len < 0 || window < 0 || !isfinite(a.scale)) return NVFP4_EINVAL;
   const int64_t width = (int64_t)a.q_heads * cache->head_dim;
-  if (a.q_heads % cache->kv_heads != 0 || a.q_heads > kMaxHeads || a.B >= kMaxDim || max_len >= kMaxDim ||
+  if (a.q_heads % cache->kv_heads != 0 || a.q_heads > kMaxHeads || a.B >= kMaxDim || max_len > kMaxLen ||
       window >= kMaxDim || !ld_ok(a.ldq, width) || !ld_ok(a.ldo, width) || a.ldt < 0 || a.ldt >= kMaxDim ||
       a.ldt < (max_len + cache->page_size - 1) / cache->page_size)
     return NVFP4_ESHAPE;
@@ -194,7 +195,7 @@ nvfp4_status nvfp4_kv_append(const void* q, const void* k, const void* v, int32_
 size_t nvfp4_attn_decode_workspace_bytes(int64_t B, int32_t q_heads, int32_t kv_heads, int32_t head_dim,
                                          int64_t max_len, int64_t window) {
   if (B < 1 || B > 65535 || kv_heads < 1 || q_heads < kv_heads || q_heads % kv_heads != 0 || q_heads > kMaxHeads ||
-      head_dim < 1 || head_dim > 256 || max_len < 0 || window < 0 || max_len >= kMaxDim || window >= kMaxDim)
+      head_dim < 1 || head_dim > 256 || max_len < 0 || window < 0 || max_len > kMaxLen || window >= kMaxDim)
     return 0;
   return nvfp4::attn_decode_workspace(B, q_heads, kv_heads, head_dim, max_len, window);
 }

@@ -7,18 +7,18 @@
 // holds 2^kSlack with ease, and most tiles then need no exchange between lanes.
 //
 // Layout.  A wave takes tiles of 16 tokens (a page holds whole tiles) for up to 16
-// query heads that share a key-value head, and both products run on the matrix
-// cores straight from registers, no LDS:
+// query heads that share a key-value head.  Lanes load whole rows side by side, 16
+// bytes each -- a load in operand order, 16 rows side by side, costs the vector cache
+// one access a lane, four times as many (67 sequences of up to 4099: 89 us against 78,
+// hints below included) -- and the tile passes through a corner of LDS that only its wave uses:
 //  * scores: S^T = K Q^T (16 x 16 x 32, bf16): lane (r, g) = (lane % 16, lane / 16)
-//    loads 16-byte pieces of token r's key row, four lanes 64 contiguous bytes;
-//    which elements of the row a step multiplies is free as long as q is taken in
-//    the same order;
+//    takes 16-byte pieces of token r's key row; which elements of the row a step
+//    multiplies is free as long as q is taken in the same order;
 //  * S^T leaves token 4 g + j of head r in register j of lane (r, g), which is
 //    where P^T must be for O^T = V^T P^T (16 x 16 x 16): the weights need no move;
-//  * V^T: lane (c, g) loads its head_dim / 16 elements of the value rows of
-//    tokens 4 g .. 4 g + 3 -- 16 lanes read whole rows -- and the transposition is
-//    four rows' worth of byte permutes within the lane; output tile i then holds
-//    element i of every lane's run.
+//  * V^T: lane (c, g) takes its head_dim / 16 elements of the value rows of tokens
+//    4 g .. 4 g + 3, and the transposition is four rows' worth of byte permutes within
+//    the lane; output tile i then holds element i of every lane's run.
 // A weight enters as the sum of two bf16 values (16 significant bits, two matrix
 // instructions), so that its rounding (2^-17) is far below that of the output.
 // E4M3 codes widen to bf16 exactly; k's scale goes into the scores' factor, v's
@@ -27,6 +27,12 @@
 // The tokens of a sequence are split over workgroups of four waves (wave w takes
 // tiles w, w + 4, ...), joined through LDS, and over splits, whose partial results
 // a second kernel joins in a fixed order.
+//
+// Bound by memory: each key and value once.  67 sequences of up to 4099 (350 MB of E4M3,
+// 8 heads of 128) take 75 us, 4.7 TB/s; 6 of up to 32768 (541 MB of bf16, 2 heads of 256)
+// 110 us, 4.9 TB/s; one of 517 tokens 10 us, which is the call.  Bare reads of as many
+// bytes take 51 to 56 and 78 us; rows in scattered places, two streams a workgroup,
+// account for most of the rest, and more tiles or waves in flight made it slower.
 #include <algorithm>
 
 #include "common.hpp"
@@ -312,8 +318,10 @@ __global__ __launch_bounds__(kWaves * 64, 2) void attn_decode_kernel(AttnArgs a,
       const int p = __builtin_amdgcn_readlane(page, n);
       const int start = (tile0 + (n0 + n) * kWaves) * 16;
       put_tile<DIM, FP8>(tile, corner);
+      wave_lds_fence();
       fetch(min(n + 1, count - 1));
       take_tile<DIM, FP8>(corner, q, factor, begin - start, p < 0 || p >= c.num_pages ? 0 : len - start, run, o);
+      wave_lds_fence();
     }
   }
   run.l += __shfl_xor(run.l, 16);

@@ -7,8 +7,11 @@
 //   O = scale (e^G Q S + P N),  P_ij = (q_i . k_j) e^(G_i - G_j)  (i >= j),
 //   S' = e^(G_64) S + K^T (e^(G_64 - G) N).
 // Two kernels: the first computes T and P of every chunk at once, the second
-// carries the state from chunk to chunk, a workgroup for 16 (or 32) of its columns,
-// which touch no other column.
+// carries the state from chunk to chunk, a workgroup for 16, 32 or 64 of its columns,
+// which touch no other column.  Bound by the latency of that chain: 8192 tokens of 32
+// heads of 128 x 128 take 248 us, of which the first kernel is 55 and 128 chunks one
+// after the other, at 1.5 us (three exchanges through LDS and their barriers), the rest;
+// 6 x 8192 without beta 426 us.  Memory's part of the former is 40 us.
 //
 // Precision.  The state is binary32 and its path keeps binary32's accuracy on the
 // bf16 matrix cores (fp32 matrix products run at 1/16 of their rate): q, k and v are
@@ -230,6 +233,7 @@ __global__ __launch_bounds__(256, 4) void gdn_chunk_kernel(GdnArgs a) {
       kk[j][r] = row > col && fade != 0.0f ? beta[r] * kk[j][r] * fade : 0.0f;
     }
   }
+  wave_lds_fence();
   const int at = (16 * w + n) * kLd + 4 * g;
 #pragma unroll
   for (int s = 0; s < 2; ++s)
@@ -237,6 +241,7 @@ __global__ __launch_bounds__(256, 4) void gdn_chunk_kernel(GdnArgs a) {
       put_block<kPPlanes>(to + Slot::kP, block_of(w, s), lane, *reinterpret_cast<const float4_t*>(mat + at + 32 * s),
                           *reinterpret_cast<const float4_t*>(mat + at + 32 * s + 16));
   if (!DELTA) return;
+  wave_lds_fence();
 #pragma unroll
   for (int j = 0; j < 4; ++j) {
     if (j / 2 > w / 2) continue;
@@ -285,6 +290,7 @@ __global__ __launch_bounds__(256, 4) void gdn_chunk_kernel(GdnArgs a) {
     }
     if (d < 3) __syncthreads();
   }
+  wave_lds_fence();
 #pragma unroll
   for (int s = 0; s < 2; ++s)
     if (s <= w / 2)
@@ -660,6 +666,7 @@ __device__ __forceinline__ void feed_chain(const StateWave<DK, NT, DELTA>& m) {
   int at = on(0);  // where the pointers stand
   fetch(odd, at);
   put_keys(even);
+  wave_lds_fence();
   turn_keys();
   put_rest(even);
   at = on(at);
@@ -669,6 +676,7 @@ __device__ __forceinline__ void feed_chain(const StateWave<DK, NT, DELTA>& m) {
     __syncthreads();
     __syncthreads();
     put_keys(next);
+    wave_lds_fence();
     turn_keys();
     if (DELTA) __syncthreads();
     put_rest(next);
@@ -722,6 +730,7 @@ __device__ __forceinline__ void write_outputs(const StateWave<DK, NT, DELTA>& m)
 #pragma unroll
     for (int i = 0; i < kLoads; ++i)
       *reinterpret_cast<u32x4_t*>(queries + (i * 64 + lane) / kPieces * L::kQueryRow + lane % kPieces * 16) = x.q[i];
+    wave_lds_fence();
 #pragma unroll
     for (int s = 0; s < KS; ++s) qa[s] = m.run(reinterpret_cast<const uint16_t*>(queries + n * L::kQueryRow), s);
   };
@@ -788,6 +797,7 @@ __device__ __forceinline__ void write_outputs(const StateWave<DK, NT, DELTA>& m)
       for (int r = 0; r < 4; ++r)
         *reinterpret_cast<uint16_t*>(results + (4 * g + r) * L::kRow + (16 * c + n) * 2) =
             __builtin_bit_cast(uint16_t, (__bf16)o[c][r]);
+    wave_lds_fence();
 #pragma unroll
     for (int i = 0; i < kOutStores; ++i) {
       const int row = i * (64 / kOutPieces) + o_row;
@@ -849,7 +859,10 @@ static hipError_t launch_prefill(const GdnArgs& a, hipStream_t stream) {
   }
   // A workgroup fills a CU's LDS or its waves, so the launch runs in rounds of one for
   // each CU; one of 32 columns takes about 1.4 times as long as one of 16, and without
-  // beta one of 64 about 1.6 times as long as one of 32.  As few columns as fit in one round.
+  // beta one of 64 about 1.6 times as long as one of 32.  16 columns where they fit in one
+  // round (32 heads of 128, 2 x 4096 tokens: 182 us against 191 with 32), else 32 (3 x
+  // 4096: 318 against 345 with 16; 4 x 4096: 297 against 364), or 64 without beta where
+  // 32 would not fit in one (6 x 8192: 428 us against 467 with 32).
   const int64_t pairs = (a.B * a.v_heads + 7) / 8 * 8;
   const bool one_round = pairs * (a.v_dim / 16) <= kCUs;
   const bool wide = !DELTA && a.v_dim % 64 == 0 && pairs * (a.v_dim / 32) > kCUs;

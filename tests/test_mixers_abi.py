@@ -172,3 +172,13 @@ def test_conveniences_refuse_other_things_than_cuda_tensors():
         nv.attn_decode(x, None, None, None, stream=7)
     with pytest.raises(AssertionError):
         nv.PagedKVCache(x.view(2, 1, 8, 128), x.view(2, 1, 8, 128))
+
+
+def test_calls_larger_than_a_launch_are_refused():
+    assert append(T=(1 << 22) + 1) == 2
+    assert attn(B=65535, heads=72, ldq=72 * 128, ldo=72 * 128) == 2
+    assert attn(max_len=(1 << 30) + 1, ldt=1 << 30) == 2
+    assert nv.nvfp4_attn_decode_workspace_bytes(1, 40, 8, 128, (1 << 30) + 1, 0) == 0
+    assert gdn(False, B=65535, n=1 << 17) == 2
+    assert gdn(True, T=(1 << 28) + 64) == 2
+    assert gdn(True, B=65535, n=1 << 17) == 2
