@@ -691,7 +691,7 @@ def attn_decode(q, cache, block_table, seq_lens, max_len=None, scale=None, windo
     ldo = _rows3(out, dev, torch.bfloat16, B, H, D, "out")
     ws = workspace if workspace is not None else Workspace(q.device)
     buf, nbytes = ws.get(nvfp4_attn_decode_workspace_bytes(B, H, cache.kv_heads, D, max_len, window))
-    nvfp4_attn_decode(q, B, H, ldq, cache.desc, block_table, max(block_table.stride(0), pages), seq_lens, max_len,
+    nvfp4_attn_decode(q, B, H, ldq, cache.desc, block_table, block_table.stride(0) if B > 1 else pages, seq_lens, max_len,
                       D ** -0.5 if scale is None else scale, window, out, ldo, lse, buf, nbytes, stream)
     return out, lse
 

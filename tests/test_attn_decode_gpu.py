@@ -209,6 +209,8 @@ def test_refusals():
         nv.attn_decode(c.q, c.cache, c.dev_table, c.dev_lens[:1])
     with pytest.raises(nv.NVFP4Error):
         nv.attn_decode(c.q[:, :9], c.cache, c.dev_table, c.dev_lens)
+    with pytest.raises(nv.NVFP4Error):                     # one row of pages for all: its stride is 0
+        nv.attn_decode(c.q, c.cache, c.dev_table[:1].expand(2, -1), c.dev_lens)
     with pytest.raises(nv.NVFP4Error):
         c.run(scale=float("nan"))
     with pytest.raises(TypeError):

@@ -150,6 +150,43 @@ def test_prompt_layouts(Hk, Hv, Dk, Dv, delta):
     assert sum(lens) == 200
 
 
+# Many heads: workgroups of 32 columns, and of 64 without beta; batches around the 64 sequences
+# that are put in order by length.
+@pytest.mark.parametrize("B,Hk,Hv,Dk,Dv", [(3, 2, 16, 64, 128), (3, 4, 16, 128, 128), (5, 8, 16, 128, 128), (5, 4, 16, 64, 128),
+                                           (6, 2, 12, 64, 96), (64, 1, 6, 64, 64), (65, 1, 5, 128, 64), (80, 2, 4, 128, 192)])
+@pytest.mark.parametrize("delta", [True, False])
+def test_prompts_of_many_heads(B, Hk, Hv, Dk, Dv, delta):
+    say(f"[gdn] prompts B={B} heads={Hk}/{Hv} dims={Dk}x{Dv} delta={delta}")
+    rng = np.random.default_rng(B + Dv)
+    lens = rng.integers(0, 9 if B > 10 else 150, B)
+    lens[B // 2] = 130
+    ends = np.concatenate([[0], np.cumsum(lens)])
+    T = int(ends[-1]) + 2
+    c = Case(T, Hk, Hv, Dk, Dv, delta, B + 2, seed=T)
+    index = rng.permutation(B + 2)[:B].astype(np.int32)
+    index[1] = -1                                          # a padded row
+    has = rng.integers(0, 2, B).astype(np.int32)
+    q, k, v, g, b, state = c.dev()
+    out = torch.full(v.shape, 77.0, dtype=torch.bfloat16, device=DEV)
+    to = lambda a: torch.from_numpy(np.asarray(a, np.int32)).to(DEV)  # noqa: E731
+    nv.gdn_prefill(q, k, v, g, b, state, to(ends), has_state=to(has), state_index=to(index), out=out)
+    torch.cuda.synchronize()
+    c.check(out, state, index, ends, has, 128 ** -0.5 if Dk == 128 else 0.125)
+    assert (out[ends[-1]:] == 77).all() and (out[ends[1]:ends[2]] == 77).all()
+
+
+def test_one_state_twice_disturbs_no_other():
+    """Two sequences of one state: its contents are unspecified, every other state and output is right."""
+    c = Case(90, 2, 4, 64, 32, True, 4, seed=14)
+    q, k, v, g, b, state = c.dev()
+    to = lambda a: torch.tensor(a, dtype=torch.int32, device=DEV)  # noqa: E731
+    out = nv.gdn_prefill(q, k, v, g, b, state, to([0, 40, 70, 90]), state_index=to([1, 1, 3]))
+    alone_state = torch.from_numpy(c.state).to(DEV)
+    alone = nv.gdn_prefill(q[70:], k[70:], v[70:], g[70:], b[70:], alone_state, to([0, 20]), state_index=to([3]))
+    torch.cuda.synchronize()
+    assert torch.equal(out[70:], alone) and torch.equal(state[[0, 2, 3]], alone_state[[0, 2, 3]])
+
+
 @pytest.mark.parametrize("rate", [0.0, 0.002, 5.0, 1000.0])
 def test_prompt_decays(rate):
     """No decay at all, slow ones, and ones that underflow within a chunk; some of -inf."""
