@@ -325,8 +325,9 @@ nvfp4_status nvfp4_kv_fp8_decode(const uint8_t* codes, int64_t n, const float* a
  * indices) cannot be checked on the host: the kernels check each one against the
  * sizes given here and never read or write outside the buffers (what an invalid
  * one does is said at each call).  Calls of more workgroups than a launch can hold
- * are refused (NVFP4_ESHAPE): T > 2^22 (append), T > 2^28 (prompts), B > 65535, or
- * B times the heads (times v_dim / 16 in a recurrent layer) above 2^22.
+ * are refused (NVFP4_ESHAPE): T > 2^22 (append), B > 65535, B times the heads (times
+ * v_dim / 16 in a recurrent layer) above 2^22, or as many chunks of 64 tokens (T / 64
+ * + B + 8, times v_heads / k_heads).
  * Non-finite inputs never fault; what they give is unspecified in every output they
  * reach (in a prompt, from the start of their chunk of 64 tokens on).
  * ------------------------------------------------------------------------- */

@@ -140,7 +140,8 @@ nvfp4_status check_gdn(const nvfp4::GdnArgs& a, bool prefill, size_t workspace_b
   if ((a.k_dim != 64 && a.k_dim != 128) || a.v_dim < 32 || a.v_dim > 1024 || a.v_dim % 32 != 0) return NVFP4_ESHAPE;
   if (a.v_heads % a.k_heads != 0 || a.v_heads > 65535 || rows >= kMaxDim || a.B > 65535 || a.num_states >= kMaxDim)
     return NVFP4_ESHAPE;
-  if ((a.B * a.v_heads + 7) * (a.v_dim / 16) > kMaxGroups || a.T / 64 > kMaxGroups) return NVFP4_ESHAPE;
+  if ((a.B * a.v_heads + 7) * (a.v_dim / 16) > kMaxGroups) return NVFP4_ESHAPE;
+  if (prefill && (a.T / 64 + a.B + 8) * (a.v_heads / a.k_heads) > kMaxGroups) return NVFP4_ESHAPE;
   if (!a.index && a.num_states < a.B) return NVFP4_ESHAPE;
   const int64_t kw = (int64_t)a.k_heads * a.k_dim, vw = (int64_t)a.v_heads * a.v_dim;
   if (!ld_ok(a.ldq, kw) || !ld_ok(a.ldk, kw) || !ld_ok(a.ldv, vw) || !ld_ok(a.ldo, vw) || !ld_ok(a.ldg, a.v_heads) ||

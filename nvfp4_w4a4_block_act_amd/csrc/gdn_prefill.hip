@@ -9,9 +9,9 @@
 // Two kernels: the first computes T and P of every chunk at once, the second
 // carries the state from chunk to chunk, a workgroup for 16, 32 or 64 of its columns,
 // which touch no other column.  Bound by the latency of that chain: 8192 tokens of 32
-// heads of 128 x 128 take 248 us, of which the first kernel is 55 and 128 chunks one
+// heads of 128 x 128 take 244 us, of which the first kernel is 48 and 128 chunks one
 // after the other, at 1.5 us (three exchanges through LDS and their barriers), the rest;
-// 6 x 8192 without beta 426 us.  Memory's part of the former is 40 us.
+// 6 of up to 8192 without beta 416 us, 86 of them the first kernel.  Memory's part of the former is 40 us.
 //
 // Precision.  The state is binary32 and its path keeps binary32's accuracy on the
 // bf16 matrix cores (fp32 matrix products run at 1/16 of their rate): q, k and v are
@@ -143,9 +143,12 @@ __global__ __launch_bounds__(256, 4) void gdn_chunk_kernel(GdnArgs a) {
   __shared__ __align__(16) float betas[kChunk];
   const int lane = threadIdx.x % 64, n = lane % 16, g = lane / 16;
   const int w = __builtin_amdgcn_readfirstlane(threadIdx.x / 64);
-  const int hv = blockIdx.y, hk = hv / (a.v_heads / a.k_heads);
+  // the value heads of a key head run one after the other on one XCD (workgroups go round
+  // the eight in turn), so that its L2 has the keys and queries for all but the first
+  // (two value heads to a key head: 48 us against 57, without beta 86 against 98)
+  const int group = a.v_heads / a.k_heads, hk = blockIdx.y, hv = hk * group + blockIdx.x / 8 % group;
+  const int64_t slot = (int64_t)(blockIdx.x / 8 / group) * 8 + blockIdx.x % 8;
   // the sequence whose slots this chunk's index falls into
-  const int64_t slot = blockIdx.x;
   int b = -1;
   for (int64_t b0 = 0; b0 < a.B; b0 += 64) {
     const int64_t i = b0 + lane;
@@ -853,7 +856,9 @@ size_t gdn_prefill_workspace(int64_t T, int64_t B, int, int v_heads, int, int) {
 template <int DK, bool DELTA>
 static hipError_t launch_prefill(const GdnArgs& a, hipStream_t stream) {
   if (a.T > 0) {
-    gdn_chunk_kernel<DK, DELTA><<<dim3((unsigned)chunk_slots(a.T, a.B), a.v_heads), 256, 0, stream>>>(a);
+    const int64_t slots = (chunk_slots(a.T, a.B) + 7) / 8 * 8;
+    const dim3 grid((unsigned)(slots * (a.v_heads / a.k_heads)), a.k_heads);
+    gdn_chunk_kernel<DK, DELTA><<<grid, 256, 0, stream>>>(a);
     const hipError_t e = hipGetLastError();
     if (e != hipSuccess) return e;
   }

@@ -111,6 +111,7 @@ int main() {
       {"prompt", [] { return prompt(); }, NVFP4_OK},
       {"prompt T max", [=] { return prompt(big); }, NVFP4_ESHAPE},
       {"prompt T 2^28 + 64", [] { return prompt((1 << 28) + 64); }, NVFP4_ESHAPE},
+      {"prompt T 2^27, two value heads to a key head", [] { return prompt(1 << 27); }, NVFP4_ESHAPE},
       {"prompt workspace", [] { return prompt(4096, 4, 32, 8, 1024); }, NVFP4_EWORKSPACE},
       {"prompt no sequences", [] { return prompt(64, 0); }, NVFP4_OK},
   };

@@ -180,5 +180,5 @@ def test_calls_larger_than_a_launch_are_refused():
     assert attn(max_len=(1 << 30) + 1, ldt=1 << 30) == 2
     assert nv.nvfp4_attn_decode_workspace_bytes(1, 40, 8, 128, (1 << 30) + 1, 0) == 0
     assert gdn(False, B=65535, n=1 << 17) == 2
-    assert gdn(True, T=(1 << 28) + 64) == 2
+    assert gdn(True, T=(1 << 28) + 64) == 2 and gdn(True, T=1 << 27) == 2 and gdn(True, hk=2, T=1 << 24) == 2
     assert gdn(True, B=65535, n=1 << 17) == 2
