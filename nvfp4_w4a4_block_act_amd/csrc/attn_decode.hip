@@ -37,13 +37,9 @@
 
 #include "common.hpp"
 #include "mixers.hpp"
+#include "mixers_device.hpp"
 
 namespace nvfp4 {
-
-typedef __bf16 bf16x2_t __attribute__((ext_vector_type(2)));
-typedef __bf16 bf16x8_t __attribute__((ext_vector_type(8)));
-typedef short short4_t __attribute__((ext_vector_type(4)));
-typedef float f32x2_t __attribute__((ext_vector_type(2)));
 
 constexpr float kNone = -3.402823466e38f;  // reference before any token: finite, so that differences are numbers
 constexpr float kSlack = 8.0f;
@@ -119,18 +115,12 @@ __device__ __forceinline__ uint32_t fp8_pair(uint32_t w, bool high) {
                                            : __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(w, 1.0f, false));
 }
 
-// The low (high) halves of two dwords as one, the first in the low half.
-__device__ __forceinline__ uint32_t low_halves(uint32_t a, uint32_t b) { return __builtin_amdgcn_perm(b, a, 0x05040100u); }
-__device__ __forceinline__ uint32_t high_halves(uint32_t a, uint32_t b) { return __builtin_amdgcn_perm(b, a, 0x07060302u); }
-
 __device__ __forceinline__ bf16x8_t octet(uint32_t a, uint32_t b, uint32_t c, uint32_t d) {
   return __builtin_bit_cast(bf16x8_t, make_uint4(a, b, c, d));
 }
 
 __device__ __forceinline__ void store_out(uint16_t* to, float4_t x) {
-  const f32x2_t lo = {x[0], x[1]}, hi = {x[2], x[3]};
-  *reinterpret_cast<uint2*>(to) = make_uint2(__builtin_bit_cast(uint32_t, __builtin_convertvector(lo, bf16x2_t)),
-                                             __builtin_bit_cast(uint32_t, __builtin_convertvector(hi, bf16x2_t)));
+  *reinterpret_cast<uint2*>(to) = make_uint2(bf16_pair(x[0], x[1]), bf16_pair(x[2], x[3]));
 }
 
 struct Running {
@@ -204,16 +194,11 @@ __device__ __forceinline__ void take_tile(const uint8_t* lds, const bf16x8_t (&q
     p[j] = __builtin_amdgcn_exp2f(s[j] - run.m);
     run.l += p[j];
   }
-  const f32x2_t p01 = {p[0], p[1]}, p23 = {p[2], p[3]};
-  const uint32_t h01 = __builtin_bit_cast(uint32_t, __builtin_convertvector(p01, bf16x2_t));
-  const uint32_t h23 = __builtin_bit_cast(uint32_t, __builtin_convertvector(p23, bf16x2_t));
+  const uint32_t h01 = bf16_pair(p[0], p[1]), h23 = bf16_pair(p[2], p[3]);
   rest[0] = p[0] - __uint_as_float(h01 << 16), rest[1] = p[1] - __uint_as_float(h01 & 0xFFFF0000u);
   rest[2] = p[2] - __uint_as_float(h23 << 16), rest[3] = p[3] - __uint_as_float(h23 & 0xFFFF0000u);
-  const f32x2_t r01 = {rest[0], rest[1]}, r23 = {rest[2], rest[3]};
   const short4_t hi = __builtin_bit_cast(short4_t, make_uint2(h01, h23));
-  const short4_t lo = __builtin_bit_cast(
-      short4_t, make_uint2(__builtin_bit_cast(uint32_t, __builtin_convertvector(r01, bf16x2_t)),
-                           __builtin_bit_cast(uint32_t, __builtin_convertvector(r23, bf16x2_t))));
+  const short4_t lo = __builtin_bit_cast(short4_t, make_uint2(bf16_pair(rest[0], rest[1]), bf16_pair(rest[2], rest[3])));
   auto product = [&](int i, uint32_t v01, uint32_t v23) {
     const short4_t x = __builtin_bit_cast(short4_t, make_uint2(v01, v23));
     o[i] = __builtin_amdgcn_mfma_f32_16x16x16bf16_1k(x, lo, o[i], 0, 0, 0);

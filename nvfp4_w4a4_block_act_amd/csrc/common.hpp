@@ -16,14 +16,6 @@
 
 namespace nvfp4 {
 
-// Between a wave's LDS writes and its lanes' reads of each other's: the hardware keeps a
-// wave's LDS accesses in order, this keeps the compiler from moving them.
-__device__ __forceinline__ void wave_lds_fence() {
-  __builtin_amdgcn_fence(__ATOMIC_RELEASE, "wavefront", "local");
-  __builtin_amdgcn_wave_barrier();
-  __builtin_amdgcn_fence(__ATOMIC_ACQUIRE, "wavefront", "local");
-}
-
 __device__ __forceinline__ int seg_of(const SegTable& st, int n) {
   int s = 0;
 #pragma unroll

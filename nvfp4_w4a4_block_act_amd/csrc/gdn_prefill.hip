@@ -26,13 +26,9 @@
 
 #include "common.hpp"
 #include "mixers.hpp"
+#include "mixers_device.hpp"
 
 namespace nvfp4 {
-
-typedef __bf16 bf16x2_t __attribute__((ext_vector_type(2)));
-typedef __bf16 bf16x8_t __attribute__((ext_vector_type(8)));
-typedef float f32x2_t __attribute__((ext_vector_type(2)));
-typedef short short4_t __attribute__((ext_vector_type(4)));
 
 constexpr int kChunk = 64;
 
@@ -51,17 +47,12 @@ struct Slot {
 // Chunk slots: sequence b's chunks start at cu[b] / 64 + b, so no two share one.
 __host__ __device__ inline int64_t chunk_slots(int64_t T, int64_t B) { return T / kChunk + B; }
 
-__device__ __forceinline__ uint32_t pack_bf16(float a, float b) {
-  const f32x2_t v = {a, b};
-  return __builtin_bit_cast(uint32_t, __builtin_convertvector(v, bf16x2_t));
-}
-
 // Two binary32 values as N bf16 planes: what a plane leaves goes to the next.
 template <int N>
 __device__ __forceinline__ void split_pair(float a, float b, uint32_t (&out)[N]) {
 #pragma unroll
   for (int p = 0; p < N; ++p) {
-    out[p] = pack_bf16(a, b);
+    out[p] = bf16_pair(a, b);
     a -= __uint_as_float(out[p] << 16);
     b -= __uint_as_float(out[p] & 0xFFFF0000u);
   }
@@ -76,9 +67,6 @@ __device__ __forceinline__ float4_t mfma_bf16_16(uint2 a, uint2 b, float4_t c) {
   return __builtin_amdgcn_mfma_f32_16x16x16bf16_1k(__builtin_bit_cast(short4_t, a), __builtin_bit_cast(short4_t, b), c, 0,
                                                    0, 0);
 }
-
-__device__ __forceinline__ uint32_t low_halves(uint32_t a, uint32_t b) { return __builtin_amdgcn_perm(b, a, 0x05040100u); }
-__device__ __forceinline__ uint32_t high_halves(uint32_t a, uint32_t b) { return __builtin_amdgcn_perm(b, a, 0x07060302u); }
 
 struct Rows {
   int64_t first;  // row of the sequence's first token

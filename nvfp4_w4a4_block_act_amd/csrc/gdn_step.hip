@@ -16,14 +16,13 @@
 // both, 49 with neither).
 #include "common.hpp"
 #include "mixers.hpp"
+#include "mixers_device.hpp"
 
 namespace nvfp4 {
 
 typedef float floatx4_t __attribute__((ext_vector_type(4)));
 
 __device__ __forceinline__ float bf16_value(uint16_t b) { return __uint_as_float((uint32_t)b << 16); }
-
-__device__ __forceinline__ uint16_t bf16_bits(float v) { return __builtin_bit_cast(uint16_t, (__bf16)v); }
 
 // Adds each value up over the row groups of a wave (lanes STEP, 2 STEP, ... apart).
 template <int STEP>
@@ -94,9 +93,8 @@ __global__ __launch_bounds__(256) void gdn_step_kernel(GdnArgs a) {
   }
   if (rg == 0) {
     const floatx4_t o = a.scale * (qs + qk * u);
-    const uint32_t lo = bf16_bits(o[0]) | ((uint32_t)bf16_bits(o[1]) << 16);
-    const uint32_t hi = bf16_bits(o[2]) | ((uint32_t)bf16_bits(o[3]) << 16);
-    *reinterpret_cast<uint2*>(a.out + b * a.ldo + (int64_t)h * a.v_dim + col) = make_uint2(lo, hi);
+    *reinterpret_cast<uint2*>(a.out + b * a.ldo + (int64_t)h * a.v_dim + col) =
+        make_uint2(bf16_pair(o[0], o[1]), bf16_pair(o[2], o[3]));
   }
 }
 

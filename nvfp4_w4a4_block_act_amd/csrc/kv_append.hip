@@ -17,17 +17,9 @@
 #include "common.hpp"
 #include "kv_codec.hpp"
 #include "mixers.hpp"
+#include "mixers_device.hpp"
 
 namespace nvfp4 {
-
-typedef __bf16 bf16x2_t __attribute__((ext_vector_type(2)));
-typedef float floatx2_t __attribute__((ext_vector_type(2)));
-
-// Two binary32 values rounded to bf16 (nearest, ties to even), the first in the low half.
-__device__ __forceinline__ uint32_t bf16_pair(float a, float b) {
-  const floatx2_t v = {a, b};
-  return __builtin_bit_cast(uint32_t, __builtin_convertvector(v, bf16x2_t));
-}
 
 template <bool F32>
 __device__ __forceinline__ void load8(const void* p, int64_t at, float (&x)[8]) {
