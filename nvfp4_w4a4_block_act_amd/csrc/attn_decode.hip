@@ -304,7 +304,7 @@ __global__ __launch_bounds__(kWaves * 64, 2) void attn_decode_kernel(AttnArgs a,
       const int start = (tile0 + (n0 + n) * kWaves) * 16;
       put_tile<DIM, FP8>(tile, corner);
       wave_lds_fence();
-      fetch(min(n + 1, count - 1));
+      if (n + 1 < count) fetch(n + 1);
       take_tile<DIM, FP8>(corner, q, factor, begin - start, p < 0 || p >= c.num_pages ? 0 : len - start, run, o);
       wave_lds_fence();
     }
