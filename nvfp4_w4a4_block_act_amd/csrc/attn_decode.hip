@@ -29,8 +29,8 @@
 // a second kernel joins in a fixed order.
 //
 // Bound by memory: each key and value once.  67 sequences of up to 4099 (350 MB of E4M3,
-// 8 heads of 128) take 75 us, 4.7 TB/s; 6 of up to 32768 (541 MB of bf16, 2 heads of 256)
-// 110 us, 4.9 TB/s; one of 517 tokens 10 us, which is the call.  Bare reads of as many
+// 8 heads of 128) take 71 us, 4.9 TB/s; 6 of up to 32768 (541 MB of bf16, 4 heads of 256)
+// 100 us, 5.4 TB/s; one of 517 tokens 10 us, which is the call.  Bare reads of as many
 // bytes take 51 to 56 and 78 us; rows in scattered places, two streams a workgroup,
 // account for most of the rest, and more tiles or waves in flight made it slower.
 #include <algorithm>
@@ -44,24 +44,25 @@ namespace nvfp4 {
 constexpr float kNone = -3.402823466e38f;  // reference before any token: finite, so that differences are numbers
 constexpr float kSlack = 8.0f;
 constexpr float kLog2e = 1.44269504088896340736f, kLn2 = 0.69314718055994530942f;
-constexpr int kSplitTokens = 512;          // fewest tokens of a split
 
-// Splits of a sequence, from sizes the host knows: about eight workgroups for each CU
-// (uneven lengths even out over them), none with fewer than kSplitTokens tokens.
-// Sixteen for each CU took 60 us against 51 for 160 sequences of up to 1024 and 78
-// against 77 for 67 of up to 4099; splits of 256 or 1024 tokens 86 and 90 us there.
-// Equal shares of all sequences' tiles, as many as the GPU holds at once, taken from the
-// lengths on the device, were no faster there (81 us) and slower for few sequences (one of
-// 32768: 27 us against 22).
+// Splits of a sequence, from sizes the host knows: about twelve workgroups for each CU
+// (uneven lengths even out over them), none with fewer than 512 tokens -- or 256 where
+// there would be less than two workgroups for each CU, but no split, and no second
+// kernel, for less than 1024.  8 heads of 128, E4M3: 67 sequences of up to 4099 take 73 us
+// (eight for each CU 80, sixteen 75), 128 of up to 4096 129 us (132, 125), 160 of up to
+// 1024 49 us (48, 49); 24 of up to 2000, 4 heads of 256 in bf16, 30 us (39 with splits of
+// 512), one of 32768 20 us (23 with splits of 256).  Equal shares of all sequences' tiles,
+// as many as the GPU holds at once, taken from the lengths on the device, were no faster
+// and slower for few sequences (one of 32768: 27 us against 22).
 struct Splits {
   int count, tokens;  // tokens of one split: a multiple of 16
 };
 static Splits attn_splits(int64_t B, int q_heads, int kv_heads, int64_t max_len, int64_t window) {
   const int64_t span = window > 0 && window < max_len ? window + 15 : max_len;
   const int64_t rows = B * kv_heads * ((q_heads / kv_heads + 15) / 16);
-  const int64_t want = std::max<int64_t>(1, (int64_t)kCUs * 8 / rows);
-  const int64_t most = std::max<int64_t>(1, span / kSplitTokens);
-  const int64_t n = std::min(want, most);
+  const int64_t want = std::max<int64_t>(1, (int64_t)kCUs * 12 / rows);
+  int64_t n = std::min(want, std::max<int64_t>(1, span / 512));
+  if (n > 1 && rows * n < 2 * kCUs) n = std::min((2 * kCUs + rows - 1) / rows, span / 256);
   const int64_t tokens = std::max<int64_t>(16, (span + n - 1) / n + 15) / 16 * 16;
   return {(int)std::max<int64_t>(1, (span + tokens - 1) / tokens), (int)tokens};
 }
@@ -242,7 +243,10 @@ __global__ __launch_bounds__(kWaves * 64, 2) void attn_decode_kernel(AttnArgs a,
   const uint32_t xcd_turn = blockIdx.x / 8, which = xcd_turn % gx, item = (xcd_turn / gx) * 8 + blockIdx.x % 8;
   const int kvh = which / per, head0 = kvh * group + (which % per) * 16;
   const int heads = min(16, (kvh + 1) * group - head0);
-  const int split = item % splits, b = item / splits;
+  // The later splits of shorter sequences are empty, so each XCD has to get all of them
+  // alike: where their number and eight have a factor in common, they move on by one each
+  // time the pattern would repeat (16 sequences of up to 8192 in bf16: 67 us against 74).
+  const int b = item / splits, split = (item % splits + b / (8 / min(8, splits & -splits))) % splits;
   if (b >= a.B) return;
   const int lane = threadIdx.x % 64, r = lane % 16, g = lane / 16;
   const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x / 64);
