@@ -23,6 +23,7 @@ Modules:
     nvfp4   -- tensor quantize (encode), dequantize (decode), per-segment
                weight quantize.
     gemm    -- fp64 GEMM on decoded operands, exact int64 GEMM, error bound.
+    mixers  -- paged cache append, decode attention and the gated delta rule, in 64 bits.
 
 Parity status: every function is pinned by the CPU tests in
 ``tests/test_oracle_*.py`` (brute force over all code pairs, library casts,
