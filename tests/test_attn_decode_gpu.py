@@ -122,6 +122,20 @@ def test_long_sequences_are_joined(lens, heads, kv, dim, page, fp8):
     assert torch.equal(got[0], again[0]) and torch.equal(got[1], again[1]), "the result depends on timing"
 
 
+@pytest.mark.parametrize("lens,heads,kv,dim", [
+    ([2048, 5, 1024, 700, 1, 2047, 300, 0, 1500], 4, 1, 64),                                  # eight splits
+    ([1024, 3, 513, 512, 511, 0, 900, 64, 1, 1000, 700, 17, 256, 1023, 640, 800], 16, 16, 64),  # two
+    ([1600, 40, 1599, 0, 900, 533, 534, 1067, 1, 16], 32, 16, 128),                           # four, rows in short supply
+    ([1300, 1, 900, 433, 434, 867, 0, 1299], 8, 2, 256)])
+def test_uneven_lengths_in_few_splits(lens, heads, kv, dim):
+    say(f"[attn] uneven lens={lens}")
+    for fp8 in (False, True):
+        c = Case(lens, heads, kv, dim, 16, fp8, seed=len(lens))
+        got = c.run()
+        torch.cuda.synchronize()
+        c.check(got, dim ** -0.5)
+
+
 def test_long_window_and_loose_bound():
     """A bound far above the lengths, and a window whose start lies inside a page and a split."""
     c = Case([6000, 12, 2500, 0], 10, 2, 128, 64, True, seed=3, max_len=40000)
