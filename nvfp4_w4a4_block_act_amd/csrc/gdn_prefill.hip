@@ -7,8 +7,8 @@
 //   O = scale (e^G Q S + P N),  P_ij = (q_i . k_j) e^(G_i - G_j)  (i >= j),
 //   S' = e^(G_64) S + K^T (e^(G_64 - G) N).
 // Two kernels: the first computes T and P of every chunk at once, the second
-// carries the state from chunk to chunk, a workgroup for 16, 32 or 64 of its columns,
-// which touch no other column.  Bound by the latency of that chain: 8192 tokens of 32
+// carries the state from chunk to chunk, a workgroup for 16, 32 or 64 of its columns, or
+// for 128 where there are heads enough; columns touch no other column.  Bound by the latency of that chain: 8192 tokens of 32
 // heads of 128 x 128 take 244 us, of which the first kernel is 48 and 128 chunks one
 // after the other, at 1.5 us (three exchanges through LDS and their barriers), the rest;
 // 6 of up to 8192 without beta 416 us, 86 of them the first kernel.  Memory's part of the former is 40 us.
@@ -92,6 +92,33 @@ __device__ __forceinline__ int by_length(const GdnArgs& a, int r) {
     rank += other > mine || (other == mine && i < lane) ? 1 : 0;
   }
   return __ffsll((unsigned long long)__ballot(lane < a.B && rank == r)) - 1;
+}
+
+// Whether a sequence has more than one and a half times a CU's fair share of the work of a
+// launch of whole heads: alone it would outlast the rest (see launch_prefill).
+__device__ __forceinline__ bool is_long(const GdnArgs& a, int count) {
+  return (int64_t)count * (2 * kCUs) > 3 * a.T * a.v_heads * (a.v_dim / 128);
+}
+
+// The r-th of the long sequences; -1 if there are fewer.
+__device__ __forceinline__ int long_sequence(const GdnArgs& a, int r) {
+  const int lane = threadIdx.x % 64;
+  for (int64_t b0 = 0; b0 < a.B; b0 += 64) {
+    const int64_t b = b0 + lane;
+    int count = 0;
+    if (b < a.B) {
+      const int64_t first = min(max((int64_t)a.cu[b], (int64_t)0), a.T);
+      count = (int)(min(max((int64_t)a.cu[b + 1], first), a.T) - first);
+    }
+    unsigned long long found = __ballot(is_long(a, count));
+    if (r >= __popcll(found)) {
+      r -= __popcll(found);
+      continue;
+    }
+    for (; r > 0; --r) found &= found - 1;
+    return (int)b0 + __ffsll(found) - 1;
+  }
+  return -1;
 }
 
 // ---- T and P of every chunk ------------------------------------------------------
@@ -804,7 +831,7 @@ __device__ __forceinline__ void write_outputs(const StateWave<DK, NT, DELTA>& m)
 }
 
 template <int DK, int NT, bool DELTA>
-__global__ __launch_bounds__(768, 3) void gdn_state_kernel(GdnArgs a) {
+__global__ __launch_bounds__(768, 3) void gdn_state_kernel(GdnArgs a, bool long_only) {
   using L = StateLds<DK, NT, DELTA>;
   __shared__ __align__(16) uint8_t lds[L::kBytes];
   const int slabs = a.v_dim / (16 * NT);
@@ -813,7 +840,8 @@ __global__ __launch_bounds__(768, 3) void gdn_state_kernel(GdnArgs a) {
   const int64_t pair = (turn / slabs) * 8 + blockIdx.x % 8;
   const int slab = (int)(turn % slabs);
   if (pair >= a.B * a.v_heads) return;
-  const int b = by_length(a, (int)(pair / a.v_heads)), h = (int)(pair % a.v_heads);
+  const int r = (int)(pair / a.v_heads), b = long_only ? long_sequence(a, r) : by_length(a, r), h = (int)(pair % a.v_heads);
+  if (b < 0) return;
   const int64_t slot = a.index ? __builtin_amdgcn_readfirstlane(a.index[b]) : b;
   if (slot < 0 || slot >= a.num_states) return;
   const int lane = threadIdx.x % 64, n = lane % 16, g = lane / 16;
@@ -837,6 +865,262 @@ __global__ __launch_bounds__(768, 3) void gdn_state_kernel(GdnArgs a) {
   }
 }
 
+// ---- whole heads ------------------------------------------------------------------
+// Where there are sequences and heads enough, a workgroup of eight waves carries 128
+// columns, a wave 16 of them over all rows of the state: every product then leaves its
+// rows where the next product's right operand wants them, and nothing passes between
+// waves but what all of them read, the chunk's left operands in LDS.
+template <int DK, bool DELTA>
+struct HeadLds {
+  static constexpr int kRow = DK * 2 + 16, kValueRow = 128 * 2 + 16;
+  static constexpr int kSlot = 0, kSlotBytes = DELTA ? Slot::kBytesDelta : Slot::kBytesLinear;
+  static constexpr int kTurned = kSlot + kSlotBytes;             // K^T: [step][tile of the state's rows]
+  static constexpr int kQueries = kTurned + DK / 16 * 2 * 1024;
+  static constexpr int kKeys = kQueries + kChunk * kRow;
+  static constexpr int kValues = kKeys + kChunk * kRow;          // then the results
+  static constexpr int kBytes = kValues + kChunk * kValueRow;
+};
+
+template <int DK, bool DELTA>
+__global__ __launch_bounds__(512, 2) void gdn_head_kernel(GdnArgs a) {
+  using L = HeadLds<DK, DELTA>;
+  constexpr int TW = DK / 64, KS = DK / 32, P = DELTA ? 3 : 2;
+  constexpr int kPieces = DK / 8, kLoads = DK / 64;              // of a key row; of a thread
+  constexpr int kSlotPieces = L::kSlotBytes / 16, kSlotLoads = (kSlotPieces + 511) / 512;
+  __shared__ __align__(16) uint8_t lds[L::kBytes];
+  const int slabs = a.v_dim / 128;
+  const int64_t turn = blockIdx.x / 8, pair = (turn / slabs) * 8 + blockIdx.x % 8;
+  const int slab = (int)(turn % slabs);
+  if (pair >= a.B * a.v_heads) return;
+  const int b = by_length(a, (int)(pair / a.v_heads)), h = (int)(pair % a.v_heads), hk = h / (a.v_heads / a.k_heads);
+  const int64_t index = a.index ? __builtin_amdgcn_readfirstlane(a.index[b]) : b;
+  if (index < 0 || index >= a.num_states) return;
+  const int t = threadIdx.x, lane = t % 64, n = lane % 16, g = lane / 16;
+  const int w = __builtin_amdgcn_readfirstlane(t / 64);
+  const Rows rows = rows_of(a, b);
+  if (is_long(a, rows.count)) return;
+  const int chunks = (rows.count + kChunk - 1) / kChunk;
+  const int64_t col = (int64_t)h * a.v_dim + slab * 128;
+  const int64_t ws_step = (int64_t)a.v_heads * L::kSlotBytes;
+  const uint8_t* ws = static_cast<const uint8_t*>(a.workspace) + (rows.first / kChunk + b) * ws_step +
+                      (int64_t)h * L::kSlotBytes;
+
+  // tile q TW + i, register r: state row q DK / 4 + (4 g + r) TW + i
+  float* st = a.state + (index * a.v_heads + h) * DK * (int64_t)a.v_dim + slab * 128 + 16 * w + n;
+  auto state_at = [&](int x, int r) { return st + (int64_t)(x / TW * (DK / 4) + (4 * g + r) * TW + x % TW) * a.v_dim; };
+  float4_t S[DK / 16];
+  const bool load = a.has_state && a.has_state[b] != 0;
+#pragma unroll
+  for (int x = 0; x < DK / 16; ++x)
+#pragma unroll
+    for (int r = 0; r < 4; ++r) S[x][r] = load ? *state_at(x, r) : 0.0f;
+
+  struct {
+    u32x4_t k[kLoads], q[kLoads], v[2], s[kSlotLoads];
+  } next;
+  auto fetch = [&](int ch) {
+    const int64_t row0 = rows.first + (int64_t)ch * kChunk;
+    const int last = min(kChunk, rows.count - ch * kChunk) - 1;
+#pragma unroll
+    for (int i = 0; i < kLoads; ++i) {
+      const int64_t r = row0 + min((i * 512 + t) / kPieces, last);
+      const int at = hk * DK + t % kPieces * 8;
+      next.k[i] = *reinterpret_cast<const u32x4_t*>(a.k + r * a.ldk + at);
+      next.q[i] = *reinterpret_cast<const u32x4_t*>(a.q + r * a.ldq + at);
+    }
+#pragma unroll
+    for (int i = 0; i < 2; ++i)
+      next.v[i] = *reinterpret_cast<const u32x4_t*>(a.v + (row0 + min(i * 32 + t / 16, last)) * a.ldv + col + t % 16 * 8);
+#pragma unroll
+    for (int i = 0; i < kSlotLoads; ++i)
+      next.s[i] = *reinterpret_cast<const u32x4_t*>(ws + ch * ws_step + min(i * 512 + t, kSlotPieces - 1) * 16);
+  };
+  auto put = [&] {
+#pragma unroll
+    for (int i = 0; i < kLoads; ++i) {
+      const int at = (i * 512 + t) / kPieces * L::kRow + t % kPieces * 16;
+      *reinterpret_cast<u32x4_t*>(lds + L::kKeys + at) = next.k[i];
+      *reinterpret_cast<u32x4_t*>(lds + L::kQueries + at) = next.q[i];
+    }
+#pragma unroll
+    for (int i = 0; i < 2; ++i)
+      *reinterpret_cast<u32x4_t*>(lds + L::kValues + (i * 32 + t / 16) * L::kValueRow + t % 16 * 16) = next.v[i];
+#pragma unroll
+    for (int i = 0; i < kSlotLoads; ++i)
+      if (i * 512 + t < kSlotPieces) *reinterpret_cast<u32x4_t*>(lds + L::kSlot + (i * 512 + t) * 16) = next.s[i];
+  };
+  // K^T, a quarter of its rows and a step of 32 tokens a wave, transposed within the lane
+  auto turn_keys = [&] {
+    const int q = w % 4, s = w / 4;
+    uint32_t z[8];
+#pragma unroll
+    for (int j = 0; j < 8; ++j) {
+      const uint8_t* from = lds + L::kKeys + (32 * s + (j / 4) * 16 + 4 * g + j % 4) * L::kRow + (q * (DK / 4) + n * TW) * 2;
+      if constexpr (TW == 2)
+        z[j] = *reinterpret_cast<const uint32_t*>(from);
+      else
+        z[j] = *reinterpret_cast<const uint16_t*>(from);
+    }
+#pragma unroll
+    for (int i = 0; i < TW; ++i) {
+      uint32_t e[4];
+#pragma unroll
+      for (int j = 0; j < 4; ++j) e[j] = i ? high_halves(z[2 * j], z[2 * j + 1]) : low_halves(z[2 * j], z[2 * j + 1]);
+      *reinterpret_cast<uint4*>(lds + L::kTurned + (s * (DK / 16) + q * TW + i) * 1024 + lane * 16) =
+          make_uint4(e[0], e[1], e[2], e[3]);
+    }
+  };
+  // step s of row tile i of the keys or queries, in the order of the state's planes
+  auto rows_at = [&](int area, int i, int s) {
+    const uint8_t* row = lds + area + (16 * i + n) * L::kRow + 64 * s;
+    if constexpr (TW == 2) return *reinterpret_cast<const uint4*>(row + 16 * g);
+    const uint2 x = *reinterpret_cast<const uint2*>(row + 8 * g), y = *reinterpret_cast<const uint2*>(row + 32 + 8 * g);
+    return make_uint4(x.x, x.y, y.x, y.y);
+  };
+  auto block = [&](int at, int p, int i, int s) {
+    return *reinterpret_cast<const uint4*>(lds + L::kSlot + at + (p * kBlocks + block_of(i, s)) * kBlockBytes + lane * 16);
+  };
+  auto decays = [&](int at, int i) { return *reinterpret_cast<const float4_t*>(lds + L::kSlot + at + (16 * i + 4 * g) * 4); };
+  // rows of tiles 2 s and 2 s + 1 as planes of a right operand
+  auto planes_of = [&](const float4_t& x, const float4_t& y, auto& out) {
+    constexpr int N = sizeof(out) / sizeof(out[0]);
+    uint32_t z[4][N];
+    split_pair(x[0], x[1], z[0]);
+    split_pair(x[2], x[3], z[1]);
+    split_pair(y[0], y[1], z[2]);
+    split_pair(y[2], y[3], z[3]);
+#pragma unroll
+    for (int p = 0; p < N; ++p) out[p] = make_uint4(z[0][p], z[1][p], z[2][p], z[3][p]);
+  };
+
+  if (chunks > 0) fetch(0);
+  for (int ch = 0; ch < chunks; ++ch) {
+    put();
+    __syncthreads();
+    turn_keys();
+    if (ch + 1 < chunks) fetch(ch + 1);
+    float4_t o[4], N[4];
+    {
+      uint4 z[KS][P];
+#pragma unroll
+      for (int s = 0; s < KS; ++s) {
+        if constexpr (TW == 2) {
+          const float4_t x = {S[2 * s][0], S[2 * s + 1][0], S[2 * s][1], S[2 * s + 1][1]};
+          const float4_t y = {S[2 * s][2], S[2 * s + 1][2], S[2 * s][3], S[2 * s + 1][3]};
+          planes_of(x, y, z[s]);
+        } else {
+          planes_of(S[2 * s], S[2 * s + 1], z[s]);
+        }
+      }
+      float4_t ks[4];
+#pragma unroll
+      for (int i = 0; i < 4; ++i) o[i] = ks[i] = {0, 0, 0, 0};
+#pragma unroll
+      for (int s = 0; s < KS; ++s) {
+        uint4 x[4];
+        if (DELTA) {
+#pragma unroll
+          for (int i = 0; i < 4; ++i) x[i] = rows_at(L::kKeys, i, s);
+#pragma unroll
+          for (int p = P - 1; p >= 0; --p)
+#pragma unroll
+            for (int i = 0; i < 4; ++i) ks[i] = mfma_bf16(x[i], z[s][p], ks[i]);
+        }
+#pragma unroll
+        for (int i = 0; i < 4; ++i) x[i] = rows_at(L::kQueries, i, s);
+#pragma unroll
+        for (int p = 1; p >= 0; --p)
+#pragma unroll
+          for (int i = 0; i < 4; ++i) o[i] = mfma_bf16(x[i], z[s][p], o[i]);
+      }
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        const float4_t decay = decays(Slot::kDecay, i);
+        o[i] *= decay * a.scale;
+#pragma unroll
+        for (int r = 0; r < 4; ++r)
+          N[i][r] = __uint_as_float((uint32_t) * reinterpret_cast<const uint16_t*>(
+                        lds + L::kValues + (16 * i + 4 * g + r) * L::kValueRow + (16 * w + n) * 2) << 16);
+        if (DELTA) N[i] -= decay * ks[i];
+      }
+    }
+    if (DELTA) {  // N = T R
+      uint4 r[2][3];
+      planes_of(N[0], N[1], r[0]);
+      planes_of(N[2], N[3], r[1]);
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        float4_t acc[3] = {{0, 0, 0, 0}, {0, 0, 0, 0}, {0, 0, 0, 0}};
+#pragma unroll
+        for (int s = 0; s <= i / 2; ++s) {
+          const uint4 t0 = block(Slot::kT, 0, i, s), t1 = block(Slot::kT, 1, i, s), t2 = block(Slot::kT, 2, i, s);
+          acc[0] = mfma_bf16(t0, r[s][0], acc[0]);
+          acc[1] = mfma_bf16(t1, r[s][0], acc[1]);
+          acc[2] = mfma_bf16(t2, r[s][0], acc[2]);
+          acc[1] = mfma_bf16(t0, r[s][1], acc[1]);
+          acc[2] = mfma_bf16(t1, r[s][1], acc[2]);
+          acc[2] = mfma_bf16(t0, r[s][2], acc[2]);
+        }
+        N[i] = (acc[2] + acc[1]) + acc[0];
+      }
+    }
+    {
+      constexpr int PN = DELTA ? 2 : 1;  // without beta N is V, one plane
+      uint4 x[2][PN];
+      planes_of(N[0], N[1], x[0]);
+      planes_of(N[2], N[3], x[1]);
+#pragma unroll
+      for (int i = 0; i < 4; ++i)
+#pragma unroll
+        for (int s = 0; s <= i / 2; ++s) {
+          const uint4 p0 = block(Slot::kP, 0, i, s);
+          o[i] = mfma_bf16(block(Slot::kP, 1, i, s), x[s][0], o[i]);
+          if constexpr (DELTA) o[i] = mfma_bf16(p0, x[s][1], o[i]);
+          o[i] = mfma_bf16(p0, x[s][0], o[i]);
+        }
+    }
+    wave_lds_fence();  // the results go where this wave's values were
+#pragma unroll
+    for (int i = 0; i < 4; ++i)
+#pragma unroll
+      for (int r = 0; r < 4; ++r)
+        *reinterpret_cast<uint16_t*>(lds + L::kValues + (16 * i + 4 * g + r) * L::kValueRow + (16 * w + n) * 2) =
+            __builtin_bit_cast(uint16_t, (__bf16)o[i][r]);
+    uint4 u[2][3];
+#pragma unroll
+    for (int s = 0; s < 2; ++s)
+      planes_of(N[2 * s] * decays(Slot::kLeft, 2 * s), N[2 * s + 1] * decays(Slot::kLeft, 2 * s + 1), u[s]);
+    const float whole = reinterpret_cast<const float*>(lds + L::kSlot + Slot::kDecay)[63];
+    __syncthreads();
+    // S' = e^G S + K^T (e^(G_64 - G) N)
+#pragma unroll
+    for (int x = 0; x < DK / 16; ++x) S[x] *= whole;
+#pragma unroll
+    for (int s = 0; s < 2; ++s) {
+      uint4 k[DK / 16];
+#pragma unroll
+      for (int x = 0; x < DK / 16; ++x)
+        k[x] = *reinterpret_cast<const uint4*>(lds + L::kTurned + (s * (DK / 16) + x) * 1024 + lane * 16);
+#pragma unroll
+      for (int p = 2; p >= 0; --p)
+#pragma unroll
+        for (int x = 0; x < DK / 16; ++x) S[x] = mfma_bf16(k[x], u[s][p], S[x]);
+    }
+#pragma unroll
+    for (int i = 0; i < 2; ++i) {
+      const int r = i * 32 + t / 16;
+      if (r < rows.count - ch * kChunk)
+        *reinterpret_cast<u32x4_t*>(a.out + (rows.first + (int64_t)ch * kChunk + r) * a.ldo + col + t % 16 * 8) =
+            *reinterpret_cast<const u32x4_t*>(lds + L::kValues + r * L::kValueRow + t % 16 * 16);
+    }
+    __syncthreads();
+  }
+#pragma unroll
+  for (int x = 0; x < DK / 16; ++x)
+#pragma unroll
+    for (int r = 0; r < 4; ++r) *state_at(x, r) = S[x][r];
+}
+
 size_t gdn_prefill_workspace(int64_t T, int64_t B, int, int v_heads, int, int) {
   return T == 0 ? 0 : (size_t)chunk_slots(T, B) * v_heads * Slot::kBytesDelta;
 }
@@ -850,22 +1134,41 @@ static hipError_t launch_prefill(const GdnArgs& a, hipStream_t stream) {
     const hipError_t e = hipGetLastError();
     if (e != hipSuccess) return e;
   }
+  const int64_t pairs = (a.B * a.v_heads + 7) / 8 * 8;
+  // Whole heads where they fill the GPU, a workgroup on each CU: 5.6 us a chunk for 128
+  // columns against four times 2.2 us for 32.  32 heads of 128: 24 prompts of up to 1000
+  // tokens take 331 us (456 column by column), 12 of 100 55 us (70), 8 of 2048 319 us (426),
+  // 24 of 1000 without beta 294 us (372); 6 of up to 8192, 192 heads, 893 us (699).  A
+  // sequence that alone would outlast the rest goes column by column all the same -- only
+  // the device knows which, and there can be no more than `most` -- in a launch of its own
+  // before: one of 8192 beside eleven of 100 takes 379 us (349), without beta 237 (330).
+  const int64_t heads = (int64_t)a.v_heads * (a.v_dim / 128);
+  if (a.v_dim % 128 == 0 && a.B * heads >= kCUs) {
+    const int64_t most = std::min(a.B, 2 * kCUs / (3 * heads));
+    if (most > 0) {
+      const int64_t some = (most * a.v_heads + 7) / 8 * 8;
+      gdn_state_kernel<DK, 2, DELTA><<<(unsigned)(some * (a.v_dim / 32)), 768, 0, stream>>>(a, true);
+      const hipError_t e = hipGetLastError();
+      if (e != hipSuccess) return e;
+    }
+    gdn_head_kernel<DK, DELTA><<<(unsigned)(pairs * (a.v_dim / 128)), 512, 0, stream>>>(a);
+    return hipGetLastError();
+  }
   // A workgroup fills a CU's LDS or its waves, so the launch runs in rounds of one for
   // each CU; one of 32 columns takes about 1.4 times as long as one of 16, and without
   // beta one of 64 about 1.6 times as long as one of 32.  16 columns where they fit in one
   // round (32 heads of 128, 2 x 4096 tokens: 182 us against 191 with 32), else 32 (3 x
   // 4096: 318 against 345 with 16; 4 x 4096: 297 against 364), or 64 without beta where
   // 32 would not fit in one (6 x 8192: 428 us against 467 with 32).
-  const int64_t pairs = (a.B * a.v_heads + 7) / 8 * 8;
   const bool one_round = pairs * (a.v_dim / 16) <= kCUs;
   const bool wide = !DELTA && a.v_dim % 64 == 0 && pairs * (a.v_dim / 32) > kCUs;
   const unsigned grid = (unsigned)(pairs * (a.v_dim / (wide ? 64 : (one_round ? 16 : 32))));
   if (one_round)
-    gdn_state_kernel<DK, 1, DELTA><<<grid, 768, 0, stream>>>(a);
+    gdn_state_kernel<DK, 1, DELTA><<<grid, 768, 0, stream>>>(a, false);
   else if (!wide)
-    gdn_state_kernel<DK, 2, DELTA><<<grid, 768, 0, stream>>>(a);
+    gdn_state_kernel<DK, 2, DELTA><<<grid, 768, 0, stream>>>(a, false);
   else if constexpr (!DELTA)
-    gdn_state_kernel<DK, 4, DELTA><<<grid, 768, 0, stream>>>(a);
+    gdn_state_kernel<DK, 4, DELTA><<<grid, 768, 0, stream>>>(a, false);
   return hipGetLastError();
 }
 

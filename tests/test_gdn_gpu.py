@@ -175,6 +175,30 @@ def test_prompts_of_many_heads(B, Hk, Hv, Dk, Dv, delta):
     assert (out[ends[-1]:] == 77).all() and (out[ends[1]:ends[2]] == 77).all()
 
 
+# Heads enough for a workgroup each: some sequences long beside the others (those go another
+# way), none, all empty but one, more than 64, two slabs of 128 columns, the last rows partial.
+@pytest.mark.parametrize("delta", [True, False])
+@pytest.mark.parametrize("Hk,Hv,Dk,Dv,lens", [
+    (2, 16, 128, 128, [64] * 9 + [65] * 9), (4, 16, 64, 128, [1, 63, 128, 0, 200, 7] * 3), (2, 16, 128, 256, [70] * 8 + [0]),
+    (1, 4, 64, 128, [3] * 66 + [0, 1, 250, 2]), (1, 32, 64, 128, [0] * 7 + [140]), (2, 4, 128, 128, [300] + [5] * 68 + [66])])
+def test_prompts_by_whole_heads(Hk, Hv, Dk, Dv, lens, delta):
+    say(f"[gdn] whole heads {Hk}/{Hv} {Dk}x{Dv} lens={lens[:4]}.. delta={delta}")
+    B, T = len(lens), sum(lens) + 1
+    assert B * Hv * (Dv // 128) >= 256
+    ends = np.concatenate([[0], np.cumsum(lens)])
+    rng = np.random.default_rng(T)
+    c = Case(T, Hk, Hv, Dk, Dv, delta, B + 1, seed=T, wide=True)
+    index, has = rng.permutation(B + 1)[:B].astype(np.int32), rng.integers(0, 2, B).astype(np.int32)
+    index[2] = B + 1                                       # a padded row
+    q, k, v, g, b, state = c.dev()
+    out = torch.full(v.shape, 77.0, dtype=torch.bfloat16, device=DEV)
+    to = lambda a: torch.from_numpy(np.asarray(a, np.int32)).to(DEV)  # noqa: E731
+    nv.gdn_prefill(q, k, v, g, b, state, to(ends), has_state=to(has), state_index=to(index), out=out)
+    torch.cuda.synchronize()
+    c.check(out, state, index, ends, has, Dk ** -0.5)
+    assert (out[ends[-1]:] == 77).all() and (out[ends[2]:ends[3]] == 77).all()
+
+
 def test_one_state_twice_disturbs_no_other():
     """Two sequences of one state: its contents are unspecified, every other state and output is right."""
     c = Case(90, 2, 4, 64, 32, True, 4, seed=14)
