@@ -603,7 +603,9 @@ class PagedKVCache:
     """A paged key-value cache over two tensors [pages, page_size, kv_heads, head_dim] of the
     same strides (any layout whose rows are contiguous, e.g. views of [pages, 2, page_size,
     ...] or permuted [pages, kv_heads, page_size, ...]): bf16, or uint8 E4M3 codes with the
-    calibrated maxima k_amax and v_amax (fp32 [1] on the GPU)."""
+    calibrated maxima k_amax and v_amax (fp32 [1] on the GPU).  It holds these tensors, whose
+    addresses every call takes from ``desc``: write into them at will; for others (or after
+    one's storage was moved) make a new cache."""
 
     def __init__(self, k, v, k_amax=None, v_amax=None):
         assert k.dim() == 4 and k.dtype in (torch.bfloat16, torch.uint8) and k.is_cuda, "k: a 4-d bf16 or uint8 cuda tensor"
@@ -613,12 +615,18 @@ class PagedKVCache:
         for a in (k_amax, v_amax):
             assert (a is None) == (k.dtype == torch.bfloat16), "k_amax and v_amax belong to E4M3 codes, and only to them"
             assert a is None or (a.dtype == torch.float32 and a.numel() == 1 and a.device == k.device), "amax: fp32 [1]"
-        self.k, self.v, self.k_amax, self.v_amax = k, v, k_amax, v_amax
+        self._tensors = k, v, k_amax, v_amax
         self.device_index = k.get_device()
         self.num_pages, self.page_size, self.kv_heads, self.head_dim = k.shape
         s = k.stride()
         self.desc = KVCacheDesc(k.data_ptr(), v.data_ptr(), _ptr(k_amax), _ptr(v_amax), self.num_pages, s[0], s[1],
                                 s[2], self.page_size, self.kv_heads, self.head_dim, DTYPE[k.dtype])
+
+    # read-only: another tensor in their place would leave desc with the address of freed memory
+    k = property(lambda self: self._tensors[0])
+    v = property(lambda self: self._tensors[1])
+    k_amax = property(lambda self: self._tensors[2])
+    v_amax = property(lambda self: self._tensors[3])
 
     @classmethod
     def empty(cls, num_pages, page_size, kv_heads, head_dim, device, k_amax=None, v_amax=None):
