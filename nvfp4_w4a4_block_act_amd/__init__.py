@@ -349,17 +349,25 @@ class Workspace:
 
     The kernels write into it, so calls that share one Workspace must be ordered
     (issued on one stream, or synchronized between streams).  Growing it frees the
-    old buffer through torch's stream-ordered allocator."""
+    old buffer through torch's stream-ordered allocator, unless a captured call has it:
+    a graph may be replayed at any time, so its buffer lives as long as the Workspace."""
 
     def __init__(self, device):
         self.device = device
         self.buf = None
+        self._captured = False       # whether a captured call has the buffer
+        self._kept = []              # earlier buffers that one has
 
     def get(self, nbytes):
         if nbytes == 0:
             return None, 0
         if self.buf is None or self.buf.numel() < nbytes:
+            if self._captured:
+                self._kept.append(self.buf)
+                self._captured = False
             self.buf = torch.empty(nbytes, dtype=torch.uint8, device=self.device)
+        if not self._captured and torch.cuda.is_current_stream_capturing():
+            self._captured = True
         return self.buf, self.buf.numel()
 
 

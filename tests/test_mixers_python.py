@@ -1,5 +1,7 @@
 """The mixers' Python layer on the CPU: what a caller may rely on before a call reaches the
 library (which needs a GPU)."""
+import weakref
+
 import pytest
 import torch
 
@@ -12,3 +14,25 @@ def test_a_caches_tensors_cannot_be_replaced(name):
     cache = nv.PagedKVCache.__new__(nv.PagedKVCache)       # (its constructor wants cuda tensors)
     with pytest.raises(AttributeError):
         setattr(cache, name, torch.zeros(1))
+
+
+def test_a_captured_calls_scratch_outlives_growth(monkeypatch):
+    """A graph that was captured with a small Workspace writes into that buffer at every replay:
+    a larger call after it must not give the buffer back to the allocator."""
+    capturing = [False]
+    monkeypatch.setattr(torch.cuda, "is_current_stream_capturing", lambda: capturing[0])
+    ws = nv.Workspace("cpu")
+    eager = weakref.ref(ws.get(64)[0])
+    assert ws.get(128)[1] == 128 and eager() is None        # nobody has it: freed
+    capturing[0] = True
+    first = weakref.ref(ws.get(100)[0])
+    capturing[0] = False
+    assert ws.get(100)[0] is first() and ws.get(0) == (None, 0)
+    assert ws.get(4096)[1] == 4096
+    assert first() is not None
+    second = weakref.ref(ws.get(4096)[0])
+    ws.get(8192)
+    assert second() is None
+    kept = first().data_ptr()
+    del ws
+    assert kept and first() is None
