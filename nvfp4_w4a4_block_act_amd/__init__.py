@@ -365,6 +365,10 @@ class Workspace:
             if self._captured:
                 self._kept.append(self.buf)
                 self._captured = False
+            elif self.buf is not None and self.buf.is_cuda:
+                # earlier calls may have used it on other streams than the one it was allocated on;
+                # they are all ordered before this call, so this call's stream is the one to wait for
+                self.buf.record_stream(torch.cuda.current_stream(self.buf.device))
             self.buf = torch.empty(nbytes, dtype=torch.uint8, device=self.device)
         if not self._captured and torch.cuda.is_current_stream_capturing():
             self._captured = True

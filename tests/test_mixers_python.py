@@ -36,3 +36,24 @@ def test_a_captured_calls_scratch_outlives_growth(monkeypatch):
     kept = first().data_ptr()
     del ws
     assert kept and first() is None
+
+
+def test_growth_on_another_stream_waits_for_it(monkeypatch):
+    """A buffer allocated on one stream and last used on another goes back to the allocator
+    together with the stream of the call that grows the Workspace."""
+    class Buffer:
+        is_cuda, device, streams = True, "cuda:0", []
+
+        def numel(self):
+            return 64
+
+        def record_stream(self, stream):
+            self.streams.append(stream)
+
+    monkeypatch.setattr(torch.cuda, "is_current_stream_capturing", lambda: False)
+    monkeypatch.setattr(torch.cuda, "current_stream", lambda device=None: ("stream of", device))
+    ws = nv.Workspace("cpu")
+    ws.buf = old = Buffer()
+    assert ws.get(64) == (old, 64) and old.streams == []
+    ws.get(65)
+    assert old.streams == [("stream of", "cuda:0")]
