@@ -15,6 +15,7 @@ current stream); the ``nvfp4_*`` wrappers take a raw hipStream_t handle.
 """
 import ctypes
 import functools
+import inspect
 import os
 from dataclasses import dataclass
 
@@ -568,11 +569,16 @@ def _on_device(fn):
     """For the mixers: runs a function with its first tensor's GPU current, on that
     GPU's current stream or on ``stream`` (keyword-only, a torch.cuda.Stream of it), and
     allocates there (see _on_stream)."""
+    name = next(iter(inspect.signature(fn).parameters))
+
     @functools.wraps(fn)
-    def wrapper(first, *args, stream=None, **kw):
+    def wrapper(*args, stream=None, **kw):
+        first = args[0] if args else kw.get(name)
+        if not isinstance(first, torch.Tensor):
+            raise TypeError(f"{fn.__name__}: {name}: a tensor is needed")
         dev = first.get_device()
-        if stream is None and dev == torch.cuda.current_device():
-            return fn(first, *args, stream=_current_stream(dev), **kw)
+        if stream is None and dev >= 0 and dev == torch.cuda.current_device():
+            return fn(*args, stream=_current_stream(dev), **kw)
         if stream is not None and not isinstance(stream, torch.cuda.Stream):
             raise TypeError(f"{fn.__name__}: stream must be a torch.cuda.Stream "
                             "(the nvfp4_* wrappers take raw handles)")
@@ -580,9 +586,9 @@ def _on_device(fn):
         assert stream is None or stream.device == first.device, f"{fn.__name__}: the stream is another GPU's"
         with torch.cuda.device(first.device):
             if stream is None:
-                return fn(first, *args, stream=_current_stream(dev), **kw)
+                return fn(*args, stream=_current_stream(dev), **kw)
             with torch.cuda.stream(stream):
-                return fn(first, *args, stream=stream.cuda_stream, **kw)
+                return fn(*args, stream=stream.cuda_stream, **kw)
     return wrapper
 
 

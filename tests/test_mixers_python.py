@@ -1,5 +1,6 @@
 """The mixers' Python layer on the CPU: what a caller may rely on before a call reaches the
 library (which needs a GPU)."""
+import inspect
 import weakref
 
 import pytest
@@ -57,3 +58,19 @@ def test_growth_on_another_stream_waits_for_it(monkeypatch):
     assert ws.get(64) == (old, 64) and old.streams == []
     ws.get(65)
     assert old.streams == [("stream of", "cuda:0")]
+
+
+@pytest.mark.parametrize("fn", [nv.kv_append, nv.attn_decode, nv.gdn_step, nv.gdn_prefill])
+def test_every_argument_can_be_given_by_name(fn):
+    """By the names that the signature shows, the first tensor's too: with tensors on the CPU the
+    call gets as far as the check that refuses them."""
+    names = [p.name for p in inspect.signature(fn).parameters.values() if p.default is p.empty]
+    x = torch.zeros(2, 4, 64, dtype=torch.bfloat16)
+    with pytest.raises(AssertionError, match="cuda tensor"):
+        fn(**{n: x for n in names})
+    with pytest.raises(AssertionError, match="cuda tensor"):
+        fn(x, **{n: x for n in names[1:]})
+    with pytest.raises(TypeError, match=names[0]):
+        fn(**{n: x for n in names[1:]})
+    with pytest.raises(TypeError, match=names[0]):
+        fn(None, **{n: x for n in names[1:]})
