@@ -50,7 +50,8 @@ extern "C" {
 #endif
 
 /* 2: nvfp4_gemm_form may return 2 (the MFMA GEMM with 256 x 128 tiles). */
-/* 3: nvfp4_read_probe. */
+/* 3: nvfp4_read_probe; later also the token mixers (nvfp4_kv_append to nvfp4_gdn_prefill),
+ *    which a library of version 3 may still lack: look the symbol up. */
 #define NVFP4_ABI_VERSION 3
 #define NVFP4_MAX_SEGMENTS 16
 

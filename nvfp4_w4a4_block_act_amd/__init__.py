@@ -56,79 +56,88 @@ _i64, _vp, _sz = ctypes.c_int64, ctypes.c_void_p, ctypes.c_size_t
 _i32, _f32 = ctypes.c_int32, ctypes.c_float
 
 
+def _declare(lib):
+    """Result and argument types of every function of the C ABI."""
+    lib.nvfp4_abi_version.restype = ctypes.c_int
+    lib.nvfp4_status_str.restype = ctypes.c_char_p
+    lib.nvfp4_status_str.argtypes = [ctypes.c_int]
+    lib.nvfp4_quantize_act_workspace_bytes.restype = _sz
+    lib.nvfp4_quantize_act_workspace_bytes.argtypes = [_i64, _i64]
+    lib.nvfp4_quantize_act.restype = ctypes.c_int
+    lib.nvfp4_quantize_act.argtypes = [_vp, _i64, _i64, _i64, _vp, _vp, _vp, _vp, _vp, _sz, _vp]
+    lib.nvfp4_packed_weight_bytes.restype = ctypes.c_int
+    lib.nvfp4_packed_weight_bytes.argtypes = [_i64, _i64, ctypes.POINTER(_sz), ctypes.POINTER(_sz)]
+    lib.nvfp4_pack_weight_workspace_bytes.restype = _sz
+    lib.nvfp4_pack_weight_workspace_bytes.argtypes = [_i64, _i64, ctypes.c_int32]
+    lib.nvfp4_pack_weight.restype = ctypes.c_int
+    lib.nvfp4_pack_weight.argtypes = [_vp, _i64, _i64, _i64, ctypes.POINTER(Segment), ctypes.c_int32,
+                                      _vp, _vp, _vp, _vp, _sz, _vp]
+    lib.nvfp4_weight_to_canonical.restype = ctypes.c_int
+    lib.nvfp4_weight_to_canonical.argtypes = [_vp, _vp, _i64, _i64, _vp, _vp, _vp]
+    lib.nvfp4_gemm.restype = ctypes.c_int
+    lib.nvfp4_gemm.argtypes = [_vp, _vp, _vp, _i64, _i64, _vp, _vp, _i64, ctypes.POINTER(Segment), _vp,
+                               ctypes.c_int32, _vp, _i64, _vp]
+    lib.nvfp4_gemm_form.restype = ctypes.c_int
+    lib.nvfp4_gemm_form.argtypes = [_i64, _i64, _i64]
+    lib.nvfp4_linear_workspace_bytes.restype = _sz
+    lib.nvfp4_linear_workspace_bytes.argtypes = [_i64, _i64]
+    lib.nvfp4_linear.restype = ctypes.c_int
+    lib.nvfp4_linear.argtypes = [_vp, _i64, _i64, _i64, _vp, _vp, _vp, _vp, _vp, _vp, _i64,
+                                 ctypes.POINTER(Segment), _vp, ctypes.c_int32, _vp, _i64, _vp, _sz, _vp]
+    lib.nvfp4_linear_noalloc.restype = ctypes.c_int
+    lib.nvfp4_linear_noalloc.argtypes = [_vp, _i64, _i64, _i64, _vp, _vp, _vp, _vp, _vp, _vp, _i64,
+                                         ctypes.POINTER(Segment), _vp, ctypes.c_int32, _vp, _i64, _vp]
+    lib.nvfp4_pack_weight_gate_up.restype = ctypes.c_int
+    lib.nvfp4_pack_weight_gate_up.argtypes = [_vp, _i64, _i64, _i64, _vp, _vp, _vp, _vp, _sz, _vp]
+    lib.nvfp4_gemm_swiglu_quantize.restype = ctypes.c_int
+    lib.nvfp4_gemm_swiglu_quantize.argtypes = [_vp, _vp, _vp, _i64, _i64, _vp, _vp, _i64, _vp, _vp, _vp, _vp,
+                                               _vp, _vp]
+    lib.nvfp4_amax_observe_workspace_bytes.restype = _sz
+    lib.nvfp4_amax_observe_workspace_bytes.argtypes = [_i64, _i64]
+    lib.nvfp4_amax_observe.restype = ctypes.c_int
+    lib.nvfp4_amax_observe.argtypes = [_vp, _i64, _i64, _i64, _vp, _vp, _sz, _vp]
+    lib.nvfp4_quantize_stats.restype = ctypes.c_int
+    lib.nvfp4_quantize_stats.argtypes = [_vp, _i64, _i64, _i64, _vp, _vp, _vp]
+    lib.nvfp4_kv_fp8_encode.restype = ctypes.c_int
+    lib.nvfp4_kv_fp8_encode.argtypes = [_vp, _i64, _vp, _vp, _vp]
+    lib.nvfp4_kv_fp8_decode.restype = ctypes.c_int
+    lib.nvfp4_kv_fp8_decode.argtypes = [_vp, _i64, _vp, _vp, _vp]
+    lib.nvfp4_swiglu.restype = ctypes.c_int
+    lib.nvfp4_swiglu.argtypes = [_vp, _i64, _i64, _i64, _vp, _i64, _vp]
+    lib.nvfp4_convert_sweep.restype = ctypes.c_int
+    lib.nvfp4_convert_sweep.argtypes = [ctypes.c_int32, ctypes.c_uint32, _i64, _vp, _vp]
+    lib.nvfp4_read_probe.restype = ctypes.c_int
+    lib.nvfp4_read_probe.argtypes = [_vp, _i64, ctypes.c_int32, _vp, _vp]
+    cache_p = ctypes.POINTER(KVCacheDesc)
+    lib.nvfp4_kv_append.restype = ctypes.c_int
+    lib.nvfp4_kv_append.argtypes = [_vp, _vp, _vp, _i32, _i64, _i32, _i64, _i64, _i64, _vp, _i32, _i64, _i32, _vp,
+                                    _vp, cache_p, _vp, _i64, _vp]
+    lib.nvfp4_attn_decode_workspace_bytes.restype = _sz
+    lib.nvfp4_attn_decode_workspace_bytes.argtypes = [_i64, _i32, _i32, _i32, _i64, _i64]
+    lib.nvfp4_attn_decode.restype = ctypes.c_int
+    lib.nvfp4_attn_decode.argtypes = [_vp, _i64, _i32, _i64, cache_p, _vp, _i64, _vp, _i64, _f32, _i64, _vp, _i64,
+                                      _vp, _vp, _sz, _vp]
+    gdn = [_vp, _i64, _vp, _i64, _vp, _i64, _vp, _i64, _vp, _i64]
+    lib.nvfp4_gdn_step.restype = ctypes.c_int
+    lib.nvfp4_gdn_step.argtypes = gdn + [_i64, _i32, _i32, _i32, _i32, _vp, _i64, _vp, _f32, _vp, _i64, _vp]
+    lib.nvfp4_gdn_prefill_workspace_bytes.restype = _sz
+    lib.nvfp4_gdn_prefill_workspace_bytes.argtypes = [_i64, _i64, _i32, _i32, _i32, _i32]
+    lib.nvfp4_gdn_prefill.restype = ctypes.c_int
+    lib.nvfp4_gdn_prefill.argtypes = gdn + [_i64, _i64, _vp, _i32, _i32, _i32, _i32, _vp, _i64, _vp, _vp, _f32,
+                                            _vp, _i64, _vp, _sz, _vp]
+
+
 def _lib():
     global _LIB
     if _LIB is None:
         if not os.path.exists(LIB_PATH):
             raise ImportError(f"{LIB_PATH} is not built; run python -m nvfp4_w4a4_block_act_amd.build")
         lib = ctypes.CDLL(LIB_PATH)
-        lib.nvfp4_abi_version.restype = ctypes.c_int
-        lib.nvfp4_status_str.restype = ctypes.c_char_p
-        lib.nvfp4_status_str.argtypes = [ctypes.c_int]
-        lib.nvfp4_quantize_act_workspace_bytes.restype = _sz
-        lib.nvfp4_quantize_act_workspace_bytes.argtypes = [_i64, _i64]
-        lib.nvfp4_quantize_act.restype = ctypes.c_int
-        lib.nvfp4_quantize_act.argtypes = [_vp, _i64, _i64, _i64, _vp, _vp, _vp, _vp, _vp, _sz, _vp]
-        lib.nvfp4_packed_weight_bytes.restype = ctypes.c_int
-        lib.nvfp4_packed_weight_bytes.argtypes = [_i64, _i64, ctypes.POINTER(_sz), ctypes.POINTER(_sz)]
-        lib.nvfp4_pack_weight_workspace_bytes.restype = _sz
-        lib.nvfp4_pack_weight_workspace_bytes.argtypes = [_i64, _i64, ctypes.c_int32]
-        lib.nvfp4_pack_weight.restype = ctypes.c_int
-        lib.nvfp4_pack_weight.argtypes = [_vp, _i64, _i64, _i64, ctypes.POINTER(Segment), ctypes.c_int32,
-                                          _vp, _vp, _vp, _vp, _sz, _vp]
-        lib.nvfp4_weight_to_canonical.restype = ctypes.c_int
-        lib.nvfp4_weight_to_canonical.argtypes = [_vp, _vp, _i64, _i64, _vp, _vp, _vp]
-        lib.nvfp4_gemm.restype = ctypes.c_int
-        lib.nvfp4_gemm.argtypes = [_vp, _vp, _vp, _i64, _i64, _vp, _vp, _i64, ctypes.POINTER(Segment), _vp,
-                                   ctypes.c_int32, _vp, _i64, _vp]
-        lib.nvfp4_gemm_form.restype = ctypes.c_int
-        lib.nvfp4_gemm_form.argtypes = [_i64, _i64, _i64]
-        lib.nvfp4_linear_workspace_bytes.restype = _sz
-        lib.nvfp4_linear_workspace_bytes.argtypes = [_i64, _i64]
-        lib.nvfp4_linear.restype = ctypes.c_int
-        lib.nvfp4_linear.argtypes = [_vp, _i64, _i64, _i64, _vp, _vp, _vp, _vp, _vp, _vp, _i64,
-                                     ctypes.POINTER(Segment), _vp, ctypes.c_int32, _vp, _i64, _vp, _sz, _vp]
-        lib.nvfp4_linear_noalloc.restype = ctypes.c_int
-        lib.nvfp4_linear_noalloc.argtypes = [_vp, _i64, _i64, _i64, _vp, _vp, _vp, _vp, _vp, _vp, _i64,
-                                             ctypes.POINTER(Segment), _vp, ctypes.c_int32, _vp, _i64, _vp]
-        lib.nvfp4_pack_weight_gate_up.restype = ctypes.c_int
-        lib.nvfp4_pack_weight_gate_up.argtypes = [_vp, _i64, _i64, _i64, _vp, _vp, _vp, _vp, _sz, _vp]
-        lib.nvfp4_gemm_swiglu_quantize.restype = ctypes.c_int
-        lib.nvfp4_gemm_swiglu_quantize.argtypes = [_vp, _vp, _vp, _i64, _i64, _vp, _vp, _i64, _vp, _vp, _vp, _vp,
-                                                   _vp, _vp]
-        lib.nvfp4_amax_observe_workspace_bytes.restype = _sz
-        lib.nvfp4_amax_observe_workspace_bytes.argtypes = [_i64, _i64]
-        lib.nvfp4_amax_observe.restype = ctypes.c_int
-        lib.nvfp4_amax_observe.argtypes = [_vp, _i64, _i64, _i64, _vp, _vp, _sz, _vp]
-        lib.nvfp4_quantize_stats.restype = ctypes.c_int
-        lib.nvfp4_quantize_stats.argtypes = [_vp, _i64, _i64, _i64, _vp, _vp, _vp]
-        lib.nvfp4_kv_fp8_encode.restype = ctypes.c_int
-        lib.nvfp4_kv_fp8_encode.argtypes = [_vp, _i64, _vp, _vp, _vp]
-        lib.nvfp4_kv_fp8_decode.restype = ctypes.c_int
-        lib.nvfp4_kv_fp8_decode.argtypes = [_vp, _i64, _vp, _vp, _vp]
-        lib.nvfp4_swiglu.restype = ctypes.c_int
-        lib.nvfp4_swiglu.argtypes = [_vp, _i64, _i64, _i64, _vp, _i64, _vp]
-        lib.nvfp4_convert_sweep.restype = ctypes.c_int
-        lib.nvfp4_convert_sweep.argtypes = [ctypes.c_int32, ctypes.c_uint32, _i64, _vp, _vp]
-        lib.nvfp4_read_probe.restype = ctypes.c_int
-        lib.nvfp4_read_probe.argtypes = [_vp, _i64, ctypes.c_int32, _vp, _vp]
-        cache_p = ctypes.POINTER(KVCacheDesc)
-        lib.nvfp4_kv_append.restype = ctypes.c_int
-        lib.nvfp4_kv_append.argtypes = [_vp, _vp, _vp, _i32, _i64, _i32, _i64, _i64, _i64, _vp, _i32, _i64, _i32, _vp,
-                                        _vp, cache_p, _vp, _i64, _vp]
-        lib.nvfp4_attn_decode_workspace_bytes.restype = _sz
-        lib.nvfp4_attn_decode_workspace_bytes.argtypes = [_i64, _i32, _i32, _i32, _i64, _i64]
-        lib.nvfp4_attn_decode.restype = ctypes.c_int
-        lib.nvfp4_attn_decode.argtypes = [_vp, _i64, _i32, _i64, cache_p, _vp, _i64, _vp, _i64, _f32, _i64, _vp, _i64,
-                                          _vp, _vp, _sz, _vp]
-        gdn = [_vp, _i64, _vp, _i64, _vp, _i64, _vp, _i64, _vp, _i64]
-        lib.nvfp4_gdn_step.restype = ctypes.c_int
-        lib.nvfp4_gdn_step.argtypes = gdn + [_i64, _i32, _i32, _i32, _i32, _vp, _i64, _vp, _f32, _vp, _i64, _vp]
-        lib.nvfp4_gdn_prefill_workspace_bytes.restype = _sz
-        lib.nvfp4_gdn_prefill_workspace_bytes.argtypes = [_i64, _i64, _i32, _i32, _i32, _i32]
-        lib.nvfp4_gdn_prefill.restype = ctypes.c_int
-        lib.nvfp4_gdn_prefill.argtypes = gdn + [_i64, _i64, _vp, _i32, _i32, _i32, _i32, _vp, _i64, _vp, _vp, _f32,
-                                                _vp, _i64, _vp, _sz, _vp]
+        try:
+            _declare(lib)
+        except AttributeError as e:      # functions were added without a new NVFP4_ABI_VERSION
+            raise ImportError(f"{LIB_PATH} is of an earlier build ({e}); run python -m "
+                              "nvfp4_w4a4_block_act_amd.build") from None
         _LIB = lib
     return _LIB
 

@@ -74,3 +74,21 @@ def test_every_argument_can_be_given_by_name(fn):
         fn(**{n: x for n in names[1:]})
     with pytest.raises(TypeError, match=names[0]):
         fn(None, **{n: x for n in names[1:]})
+
+
+def test_a_library_of_an_earlier_build_is_named(monkeypatch):
+    """A library without the mixers has the same version number: loading it says what is wrong."""
+    class Function:
+        pass
+
+    class Earlier:
+        def __getattr__(self, name):
+            if name.startswith(("nvfp4_gdn", "nvfp4_attn", "nvfp4_kv_append")):
+                raise AttributeError(f"undefined symbol: {name}")
+            return Function()
+
+    nv.lib()
+    monkeypatch.setattr(nv, "_LIB", None)
+    monkeypatch.setattr(nv.ctypes, "CDLL", lambda path: Earlier())
+    with pytest.raises(ImportError, match="earlier build.*nvfp4_kv_append"):
+        nv.lib()
