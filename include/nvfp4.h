@@ -342,9 +342,10 @@ typedef enum {
 
 /* A paged key-value cache (a HOST struct of device pointers).  Row (page, token,
  * head) of k and of v holds head_dim contiguous elements at element offset
- * page * page_stride + token * token_stride + head * head_stride; the rows of one
- * tensor must not overlap, and every row must be 16-byte aligned.  k and v have
- * the same strides and may lie interleaved in one allocation.
+ * page * page_stride + token * token_stride + head * head_stride; every row must be
+ * 16-byte aligned, and no two rows may overlap, neither of one tensor (NVFP4_ESHAPE)
+ * nor of both (NVFP4_EINVAL).  k and v have the same strides and may lie interleaved
+ * in one allocation.
  * head_dim is 64, 128 or 256, page_size a positive multiple of 16, token_stride
  * below 2^26.  dtype is
  * NVFP4_BF16, or NVFP4_E4M3 with device pointers to the calibrated maxima of |k|

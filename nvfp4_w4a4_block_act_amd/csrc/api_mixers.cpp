@@ -5,6 +5,8 @@
 #include <math.h>
 #include <stdint.h>
 
+#include <utility>
+
 #include "api_checks.hpp"
 #include "launch.hpp"
 #include "mixers.hpp"
@@ -27,25 +29,52 @@ int64_t cache_span(const nvfp4_kv_cache& c) {
                                 (int64_t)(c.kv_heads - 1) * c.head_stride + c.head_dim;
 }
 
-// Rows do not overlap: taken by growing stride, each of the three axes steps over
-// what the smaller ones span (an axis of one element has no stride).
-bool rows_disjoint(const nvfp4_kv_cache& c) {
-  int64_t stride[3] = {c.head_stride, c.token_stride, c.page_stride};
-  int64_t count[3] = {c.kv_heads, c.page_size, c.num_pages};
+// The three axes that a row's place in a cache tensor has, by growing stride.
+struct Axes {
+  int64_t stride[3], count[3];
+};
+Axes axes_of(const nvfp4_kv_cache& c) {
+  Axes a = {{c.head_stride, c.token_stride, c.page_stride}, {c.kv_heads, c.page_size, c.num_pages}};
   for (int i = 0; i < 3; ++i)
     for (int j = i + 1; j < 3; ++j)
-      if (stride[j] < stride[i]) {
-        const int64_t s = stride[i], n = count[i];
-        stride[i] = stride[j], count[i] = count[j];
-        stride[j] = s, count[j] = n;
+      if (a.stride[j] < a.stride[i]) {
+        std::swap(a.stride[i], a.stride[j]);
+        std::swap(a.count[i], a.count[j]);
       }
-  int64_t span = c.head_dim;
+  return a;
+}
+
+// Rows of one tensor do not overlap: each axis steps over what the smaller ones span (an
+// axis of one element has no stride).
+bool rows_disjoint(const Axes& a, int64_t dim) {
+  int64_t span = dim;
   for (int i = 0; i < 3; ++i) {
-    if (count[i] <= 1) continue;
-    if (stride[i] < span) return false;
-    span += (count[i] - 1) * stride[i];
+    if (a.count[i] <= 1) continue;
+    if (a.stride[i] < span) return false;
+    span += (a.count[i] - 1) * a.stride[i];
   }
   return true;
+}
+
+// Whether two rows of tensors `rest` elements apart, which differ by any steps along the
+// axes up to `axis`, have an element in common.  Since an axis steps over what the smaller
+// ones span, only the two steps on either side of `rest` come near enough.
+bool rows_meet(const Axes& a, int64_t dim, int64_t rest, int axis) {
+  if (axis < 0) return rest > -dim && rest < dim;
+  if (a.count[axis] <= 1) return rows_meet(a, dim, rest, axis - 1);
+  const int64_t most = a.count[axis] - 1, stride = a.stride[axis];
+  const int64_t below = rest / stride - (rest % stride < 0 ? 1 : 0);
+  for (const int64_t n : {below, below + 1})
+    if (n >= -most && n <= most && rows_meet(a, dim, rest - n * stride, axis - 1)) return true;
+  return false;
+}
+
+// No row of k overlaps one of v (rows_disjoint holds): they may lie interleaved.
+bool tensors_disjoint(const nvfp4_kv_cache& c, const Axes& a) {
+  if (c.num_pages == 0) return true;
+  const uintptr_t k = reinterpret_cast<uintptr_t>(c.k), v = reinterpret_cast<uintptr_t>(c.v);
+  const uintptr_t apart = (k < v ? v - k : k - v) / cache_elem(c);  // whole elements: both are aligned
+  return apart >= (uintptr_t)1 << 60 || !rows_meet(a, c.head_dim, (int64_t)apart, 2);  // spans are below 2^58
 }
 
 nvfp4_status check_cache(const nvfp4_kv_cache* c) {
@@ -60,13 +89,14 @@ nvfp4_status check_cache(const nvfp4_kv_cache* c) {
   if (c->token_stride >= (1 << 26)) return NVFP4_ESHAPE;  // 16 rows within 32-bit byte offsets
   // (num_pages - 1) * page_stride must stay far inside int64
   if (c->num_pages > 1 && c->page_stride > ((int64_t)1 << 56) / c->num_pages) return NVFP4_ESHAPE;
-  if (!rows_disjoint(*c)) return NVFP4_ESHAPE;
+  const Axes axes = axes_of(*c);
+  if (!rows_disjoint(axes, c->head_dim)) return NVFP4_ESHAPE;
   if (c->num_pages > 0 && (!c->k || !c->v || c->k == c->v)) return NVFP4_EINVAL;
   if (c->dtype == NVFP4_E4M3 && (!c->k_amax || !c->v_amax)) return NVFP4_EINVAL;
   if (!all_aligned({c->k, c->v, c->k_amax, c->v_amax})) return NVFP4_EALIGN;
   const int64_t unit = 16 / (int64_t)cache_elem(*c);
   if (c->page_stride % unit || c->token_stride % unit || c->head_stride % unit) return NVFP4_EALIGN;
-  return NVFP4_OK;
+  return tensors_disjoint(*c, axes) ? NVFP4_OK : NVFP4_EINVAL;
 }
 
 nvfp4_status check_append(const nvfp4::AppendArgs& a, int32_t src_dtype, const nvfp4_kv_cache* cache) {
@@ -93,7 +123,7 @@ nvfp4_status check_append(const nvfp4::AppendArgs& a, int32_t src_dtype, const n
                      {a.slots, (size_t)a.T * 8},
                      {cache->k_amax, cache->dtype == NVFP4_E4M3 ? 4u : 0u},
                      {cache->v_amax, cache->dtype == NVFP4_E4M3 ? 4u : 0u}};
-  // k and v of the cache may lie interleaved, so they are not held against each other
+  // k and v of the cache may lie interleaved: check_cache holds their rows against each other
   const Buf k_outs[] = {{cache->k, span}, {a.q_out, extent(a.T, qw, a.ldqo, 2)}};
   const Buf v_outs[] = {{cache->v, span}, {a.q_out, extent(a.T, qw, a.ldqo, 2)}};
   return disjoint(k_outs, ins) && disjoint(v_outs, ins) ? NVFP4_OK : NVFP4_EINVAL;
