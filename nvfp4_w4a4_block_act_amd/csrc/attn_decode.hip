@@ -413,12 +413,17 @@ template <int DIM, bool FP8, int kWaves>
 static hipError_t launch_waves(const AttnArgs& a, const Splits& s, hipStream_t stream) {
   const int group = a.q_heads / a.cache.kv_heads;
   const dim3 grid((unsigned)(a.cache.kv_heads * ((group + 15) / 16) * ((a.B * s.count + 7) / 8 * 8)));
-  const size_t lds = std::max<size_t>((size_t)kWaves * std::min(group, 16) * (DIM + 4) * sizeof(float),
-                                      (size_t)kWaves * Tile<DIM, FP8>::kLdsBytes);
+  auto bytes = [](int heads) {
+    return std::max<size_t>((size_t)kWaves * heads * (DIM + 4) * sizeof(float), (size_t)kWaves * Tile<DIM, FP8>::kLdsBytes);
+  };
+  const size_t lds = bytes(std::min(group, 16));
   hipError_t e = hipSuccess;
-  if (lds > 48 * 1024)  // above the default bound of dynamic LDS: many heads of 256
+  // Above the default bound of dynamic LDS (many heads of 128 or 256).  The bound is the
+  // kernel's, for all threads of the process: always that of 16 heads, so that no other call
+  // can set it lower between here and the launch.
+  if (lds > 48 * 1024)
     e = hipFuncSetAttribute(reinterpret_cast<const void*>(&attn_decode_kernel<DIM, FP8, kWaves>),
-                            hipFuncAttributeMaxDynamicSharedMemorySize, (int)lds);
+                            hipFuncAttributeMaxDynamicSharedMemorySize, (int)bytes(16));
   if (e != hipSuccess) return e;
   attn_decode_kernel<DIM, FP8, kWaves><<<grid, kWaves * 64, lds, stream>>>(a, s.count, s.tokens);
   return hipGetLastError();
