@@ -35,6 +35,7 @@
 // account for most of the rest, and more tiles or waves in flight made it slower.
 #include <algorithm>
 
+#include "attn_splits.hpp"
 #include "common.hpp"
 #include "mixers.hpp"
 #include "mixers_device.hpp"
@@ -45,26 +46,18 @@ constexpr float kNone = -3.402823466e38f;  // reference before any token: finite
 constexpr float kSlack = 8.0f;
 constexpr float kLog2e = 1.44269504088896340736f, kLn2 = 0.69314718055994530942f;
 
-// Splits of a sequence, from sizes the host knows: about twelve workgroups for each CU
-// (uneven lengths even out over them), none with fewer than 512 tokens -- or 256 where
-// there would be less than two workgroups for each CU, but no split, and no second
-// kernel, for less than 1024.  8 heads of 128, E4M3: 67 sequences of up to 4099 take 73 us
-// (eight for each CU 80, sixteen 75), 128 of up to 4096 129 us (132, 125), 160 of up to
-// 1024 49 us (48, 49); 24 of up to 2000, 4 heads of 256 in bf16, 30 us (39 with splits of
-// 512), one of 32768 20 us (23 with splits of 256).  Equal shares of all sequences' tiles,
-// as many as the GPU holds at once, taken from the lengths on the device, were no faster
-// and slower for few sequences (one of 32768: 27 us against 22).
-struct Splits {
-  int count, tokens;  // tokens of one split: a multiple of 16
+// How a launch splits its sequences, as the kernels get it (attn_splits.hpp).
+struct Plan {
+  int rows, splits, tokens, bound;
+  // a sequence's own tokens of a split; a single one covers whatever there is
+  __device__ __forceinline__ int tokens_of(int len, int window) const {
+    return splits == 1 ? tokens : attn_split_tokens(rows, tokens, bound, (int)attn_span(len, window));
+  }
 };
-static Splits attn_splits(int64_t B, int q_heads, int kv_heads, int64_t max_len, int64_t window) {
-  const int64_t span = window > 0 && window < max_len ? window + 15 : max_len;
+static Plan attn_plan(int64_t B, int q_heads, int kv_heads, int64_t max_len, int64_t window) {
   const int64_t rows = B * kv_heads * ((q_heads / kv_heads + 15) / 16);
-  const int64_t want = std::max<int64_t>(1, (int64_t)kCUs * 12 / rows);
-  int64_t n = std::min(want, std::max<int64_t>(1, span / 512));
-  if (n > 1 && rows * n < 2 * kCUs) n = std::min((2 * kCUs + rows - 1) / rows, span / 256);
-  const int64_t tokens = std::max<int64_t>(16, (span + n - 1) / n + 15) / 16 * 16;
-  return {(int)std::max<int64_t>(1, (span + tokens - 1) / tokens), (int)tokens};
+  const Splits s = attn_splits(rows, max_len, window);
+  return {(int)rows, s.count, s.tokens, (int)attn_span(max_len, window)};
 }
 
 // 16 tokens' keys and values on their way: rows in pieces of 16 bytes, lanes side by side
@@ -236,8 +229,9 @@ __device__ __forceinline__ int64_t part_row(const AttnArgs& a, int b, int head, 
 }
 
 template <int DIM, bool FP8, int kWaves>
-__global__ __launch_bounds__(kWaves * 64, 2) void attn_decode_kernel(AttnArgs a, int splits, int split_tokens) {
+__global__ __launch_bounds__(kWaves * 64, 2) void attn_decode_kernel(AttnArgs a, Plan plan) {
   constexpr int ES = FP8 ? 1 : 2, PAD = DIM + 4;
+  const int splits = plan.splits;
   const int group = a.q_heads / a.cache.kv_heads, per = (group + 15) / 16;
   const int gx = a.cache.kv_heads * per;
   const uint32_t xcd_turn = blockIdx.x / 8, which = xcd_turn % gx, item = (xcd_turn / gx) * 8 + blockIdx.x % 8;
@@ -254,7 +248,7 @@ __global__ __launch_bounds__(kWaves * 64, 2) void attn_decode_kernel(AttnArgs a,
 
   const int len = min(max(a.lens[b], 0), a.max_len);
   const int begin = a.window > 0 ? max(0, len - a.window) : 0;
-  const int first_tile = begin / 16;
+  const int first_tile = begin / 16, split_tokens = plan.tokens_of(len, a.window);
   // this split's tokens, from the tile that `begin` lies in
   const int from = first_tile * 16 + split * split_tokens;
   const int to = min(len, from + split_tokens);
@@ -362,12 +356,13 @@ __global__ __launch_bounds__(kWaves * 64, 2) void attn_decode_kernel(AttnArgs a,
 // Joins the splits of one query head: each counts 2^(its m - the largest m).  Groups of
 // DIM / 4 threads take the splits in turn, then one group their sums.
 template <int DIM, bool FP8, int kGroups>
-__global__ __launch_bounds__(DIM / 4 * kGroups) void attn_join_kernel(AttnArgs a, int splits, int split_tokens) {
+__global__ __launch_bounds__(DIM / 4 * kGroups) void attn_join_kernel(AttnArgs a, Plan plan) {
   constexpr int kLanes = DIM / 4;
+  const int splits = plan.splits;
   const int h = blockIdx.x, b = blockIdx.y, d = threadIdx.x % kLanes, grp = threadIdx.x / kLanes;
   const int len = min(max(a.lens[b], 0), a.max_len);
   const int start = a.window > 0 ? max(0, len - a.window) / 16 * 16 : 0;
-  const int used = (len - start + split_tokens - 1) / split_tokens;
+  const int split_tokens = plan.tokens_of(len, a.window), used = (len - start + split_tokens - 1) / split_tokens;
   if (used <= 1) return;
   const float* parts = static_cast<const float*>(a.workspace);
   const float2* ml = reinterpret_cast<const float2*>(parts + part_row(a, (int)gridDim.y, 0, splits, 0) * DIM) +
@@ -405,14 +400,14 @@ __global__ __launch_bounds__(DIM / 4 * kGroups) void attn_join_kernel(AttnArgs a
 }
 
 size_t attn_decode_workspace(int64_t B, int q_heads, int kv_heads, int head_dim, int64_t max_len, int64_t window) {
-  const Splits s = attn_splits(B, q_heads, kv_heads, max_len, window);
-  return s.count > 1 ? (size_t)B * q_heads * s.count * (head_dim + 2) * sizeof(float) : 0;
+  const int splits = attn_plan(B, q_heads, kv_heads, max_len, window).splits;
+  return splits > 1 ? (size_t)B * q_heads * splits * (head_dim + 2) * sizeof(float) : 0;
 }
 
 template <int DIM, bool FP8, int kWaves>
-static hipError_t launch_waves(const AttnArgs& a, const Splits& s, hipStream_t stream) {
+static hipError_t launch_waves(const AttnArgs& a, const Plan& plan, hipStream_t stream) {
   const int group = a.q_heads / a.cache.kv_heads;
-  const dim3 grid((unsigned)(a.cache.kv_heads * ((group + 15) / 16) * ((a.B * s.count + 7) / 8 * 8)));
+  const dim3 grid((unsigned)(a.cache.kv_heads * ((group + 15) / 16) * ((a.B * plan.splits + 7) / 8 * 8)));
   auto bytes = [](int heads) {
     return std::max<size_t>((size_t)kWaves * heads * (DIM + 4) * sizeof(float), (size_t)kWaves * Tile<DIM, FP8>::kLdsBytes);
   };
@@ -425,22 +420,22 @@ static hipError_t launch_waves(const AttnArgs& a, const Splits& s, hipStream_t s
     e = hipFuncSetAttribute(reinterpret_cast<const void*>(&attn_decode_kernel<DIM, FP8, kWaves>),
                             hipFuncAttributeMaxDynamicSharedMemorySize, (int)bytes(16));
   if (e != hipSuccess) return e;
-  attn_decode_kernel<DIM, FP8, kWaves><<<grid, kWaves * 64, lds, stream>>>(a, s.count, s.tokens);
+  attn_decode_kernel<DIM, FP8, kWaves><<<grid, kWaves * 64, lds, stream>>>(a, plan);
   return hipGetLastError();
 }
 
 template <int DIM, bool FP8>
 static hipError_t launch_dim(const AttnArgs& a, hipStream_t stream) {
-  const Splits s = attn_splits(a.B, a.q_heads, a.cache.kv_heads, a.max_len, a.window);
+  const Plan plan = attn_plan(a.B, a.q_heads, a.cache.kv_heads, a.max_len, a.window);
   // few short sequences: eight waves to a workgroup, so that each has fewer tiles to go through
-  const bool few = s.count == 1 && a.B * a.q_heads <= 2 * kCUs;
-  hipError_t e = few ? launch_waves<DIM, FP8, 8>(a, s, stream) : launch_waves<DIM, FP8, 4>(a, s, stream);
-  if (e != hipSuccess || s.count == 1) return e;
+  const bool few = plan.splits == 1 && a.B * a.q_heads <= 2 * kCUs;
+  hipError_t e = few ? launch_waves<DIM, FP8, 8>(a, plan, stream) : launch_waves<DIM, FP8, 4>(a, plan, stream);
+  if (e != hipSuccess || plan.splits == 1) return e;
   const dim3 rows(a.q_heads, (unsigned)a.B);
-  if (s.count <= 16)
-    attn_join_kernel<DIM, FP8, 4><<<rows, DIM, 0, stream>>>(a, s.count, s.tokens);
+  if (plan.splits <= 16)
+    attn_join_kernel<DIM, FP8, 4><<<rows, DIM, 0, stream>>>(a, plan);
   else
-    attn_join_kernel<DIM, FP8, 16><<<rows, DIM * 4, 0, stream>>>(a, s.count, s.tokens);
+    attn_join_kernel<DIM, FP8, 16><<<rows, DIM * 4, 0, stream>>>(a, plan);
   return hipGetLastError();
 }
 

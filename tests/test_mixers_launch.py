@@ -41,3 +41,7 @@ def recorded(tmp_path, checker, *sources):
 
 def test_attention_launches(tmp_path):
     recorded(tmp_path, "check_attn_launch.cpp", "attn_decode.hip")
+
+
+def test_attention_splits(tmp_path):
+    recorded(tmp_path, "check_attn_splits.cpp")
