@@ -408,8 +408,8 @@ nvfp4_status nvfp4_kv_append(const void* q, const void* k, const void* v, int32_
  *   block_table int32 [B][ldt], ldt >= ceil(max_len / page_size).
  *   max_len    upper bound of the lengths, known on the host; at most 2^30.  The
  *              work is split by the lengths themselves: a bound 2 to 256 times the
- *              longest cost 0 to 8 % for sequences of 4096 and more, and 4 us, a
- *              second kernel, for shorter ones.
+ *              longest cost 0 to 8 % for sequences of 4096 and more, and 2 to 9 us,
+ *              for a second kernel, for shorter ones.
  *   out        bf16, row stride ldo (multiple of 8); lse fp32 [B][q_heads] or NULL.
  *   workspace  device scratch of nvfp4_attn_decode_workspace_bytes (contents need
  *              no setup; NULL allowed when that is 0): the partial results of long
