@@ -362,7 +362,7 @@ struct StateLds {
 template <int DK, int NT, bool DELTA>
 struct StateWave {
   using L = StateLds<DK, NT, DELTA>;
-  static constexpr int TW = DK / 64, KS = DK / 32;
+  static constexpr int TW = DK / 64;
   const GdnArgs& a;
   uint8_t* lds;
   int64_t first;     // row of the sequence's first token
@@ -400,15 +400,11 @@ struct StateWave {
   }
 };
 
-// Rows of a tensor that a lane reads in chunk after chunk: N pointers, moved on by a
-// chunk's rows; the sequence's last chunk, when partial, clamps to its last row.
+// Rows of a tensor that a lane reads or writes in chunk after chunk: N pointers, moved on by
+// a chunk's rows.
 template <int N, typename T>
 struct RowPointers {
   T* p[N];
-  __device__ __forceinline__ void at(T* base, int64_t row0, int64_t ld, int first, int last) {
-#pragma unroll
-    for (int j = 0; j < N; ++j) p[j] = base + (row0 + min(first + j, last)) * ld;
-  }
   __device__ __forceinline__ void on(int64_t step) {
 #pragma unroll
     for (int j = 0; j < N; ++j) p[j] += step;
