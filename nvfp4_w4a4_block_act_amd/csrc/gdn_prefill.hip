@@ -131,8 +131,9 @@ __device__ __forceinline__ int long_sequence(const GdnArgs& a, int r) {
 constexpr int kLd = 68;  // row stride of the 64 x 64 matrices in LDS
 constexpr float kLog2e = 1.44269504088896340736f;
 
-// e^x of a sum of log decays.  x log2(e) is rounded, |x| 2^-24 relative; x e^x is at most
-// 0.37, so the factor is off by 2^-25 of its largest value.
+// e^x of a sum of log decays (x <= 0).  The cast, the constant and the product are off by 1, 0.23
+// and 1 times 2^-24 relative, so the exponent by 2.23 2^-24 |x|; |x| e^x is at most 0.37, so
+// the factor by 0.83 2^-24 of its largest value, 1, and by the exponential's own 2^-23 of itself.
 __device__ __forceinline__ float fade_of(double x) { return __builtin_amdgcn_exp2f((float)x * kLog2e); }
 
 // Four rows' columns 32 s + 4 g + 0 .. 3 and 32 s + 16 + 4 g + 0 .. 3 as operand planes at `to`.
