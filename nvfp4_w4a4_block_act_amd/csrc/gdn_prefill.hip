@@ -1151,12 +1151,17 @@ static hipError_t launch_prefill(const GdnArgs& a, hipStream_t stream) {
     gdn_head_kernel<DK, DELTA><<<(unsigned)(pairs * (a.v_dim / 128)), 512, 0, stream>>>(a);
     return hipGetLastError();
   }
-  // A workgroup fills a CU's LDS or its waves, so the launch runs in rounds of one for
-  // each CU; one of 32 columns takes about 1.4 times as long as one of 16, and without
-  // beta one of 64 about 1.6 times as long as one of 32.  16 columns where they fit in one
-  // round (32 heads of 128, 2 x 4096 tokens: 182 us against 191 with 32), else 32 (3 x
-  // 4096: 318 against 345 with 16; 4 x 4096: 297 against 364), or 64 without beta where
-  // 32 would not fit in one (6 x 8192: 428 us against 467 with 32).
+  // The launch runs in rounds.  With keys of 128 a workgroup fills a CU's LDS or its waves, so a
+  // round is one for each CU; one of 32 columns takes about 1.4 times as long as one of 16, and
+  // without beta one of 64 about 1.6 times as long as one of 32.  So 16 columns where they fit in
+  // one round (32 heads of 128, 8192 tokens: 238 us against 334 with 32), else 32 (2 x 4096
+  // tokens: 205 against 241 with 16; 3 x 4096: 365 against 390; 4 x 4096: 408 against 520), or 64
+  // without beta where 32 would not fit in one (4 x 4096: 222 us against 268 with 32; 6 of up to
+  // 8192: 428 against 467).  Where one sequence is far longer than the rest the smaller width can
+  // be the faster (4096 and 1500 tokens: 163 us with 16 columns, 179 with 32), which the host
+  // cannot know.  With keys of 64 two workgroups of 16 columns share a CU, so that up to two
+  // rounds' worth of them would be as fast or faster (3 x 4096: 305 us against 331 with 32, 5 x
+  // 300: 50 against 56; 2 x 4096: 187 against 180); the rule does not tell them apart.
   const bool one_round = pairs * (a.v_dim / 16) <= kCUs;
   const bool wide = !DELTA && a.v_dim % 64 == 0 && pairs * (a.v_dim / 32) > kCUs;
   const unsigned grid = (unsigned)(pairs * (a.v_dim / (wide ? 64 : (one_round ? 16 : 32))));
