@@ -27,9 +27,11 @@
  *    status except NVFP4_EHIP means nothing was enqueued.  NVFP4_EHIP means the
  *    HIP runtime rejected a launch (hipGetLastError); a call that enqueues
  *    several kernels (the two-pass quantizer, nvfp4_linear outside its
- *    one-launch range, some GEMMs with a ragged last tile column) may already have
- *    enqueued the kernels before the rejected one, and all of its outputs are
- *    then unspecified.  The library never prints and never aborts.
+ *    one-launch range, some GEMMs with a ragged last tile column, nvfp4_attn_decode
+ *    over split sequences, nvfp4_gdn_prefill) may already have enqueued the kernels
+ *    before the rejected one, and all of its outputs are then unspecified -- of
+ *    nvfp4_gdn_prefill the states too, which it updates in place: restore them before
+ *    calling again.  The library never prints and never aborts.
  *  - Element codes are packed two per byte, the even k in the low nibble:
  *    byte j of a row = code[2j] | code[2j+1] << 4; code = sign << 3 | mag,
  *    mag 0..7 = 0, 0.5, 1, 1.5, 2, 3, 4, 6.  Scales are E4M3FN bytes

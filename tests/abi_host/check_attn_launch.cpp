@@ -44,7 +44,16 @@ int main() {
                 printf("%s: %zu bytes of LDS under a bound of %zu\n", l.kernel.c_str(), l.lds, l.lds_bound);
                 ++bad;
               }
-            if (launches.empty()) ++bad;
+            const size_t all = launches.size();
+            if (all == 0) ++bad;
+            for (size_t i = 0; i < all; ++i) {  // whichever launch is rejected, the call says so and launches no more
+              launches.clear();
+              fail_launch = (int)i;
+              if (nvfp4::launch_attn_decode(args(B, 2, group, dim, fp8, max_len, 0), nullptr) == hipSuccess ||
+                  launches.size() != i)
+                printf("launch %zu of %zu rejected, but the call goes on\n", i, all), ++bad;
+            }
+            fail_launch = -1;
             ++n;
           }
   if (bound.empty()) printf("no bound was set\n"), ++bad;

@@ -45,3 +45,7 @@ def test_attention_launches(tmp_path):
 
 def test_attention_splits(tmp_path):
     recorded(tmp_path, "check_attn_splits.cpp")
+
+
+def test_prefill_launches(tmp_path):
+    recorded(tmp_path, "check_prefill_launch.cpp", "gdn_prefill.hip")
