@@ -454,9 +454,15 @@ nvfp4_status nvfp4_gdn_step(const void* q, int64_t ldq, const void* k, int64_t l
 /* nvfp4_gdn_prefill: the tokens [cu_seqlens[b], cu_seqlens[b + 1]) of each of B
  * sequences, T rows in all (device int32 [B + 1], non-decreasing, clamped to
  * [0, T]; rows of no sequence are left as they were; an empty sequence only
- * carries its state on).  Sequence b starts from its state if has_state (device
- * int32 [B]) is given and has_state[b] != 0, else from zero; its last state is
- * stored.  Workspace: nvfp4_gdn_prefill_workspace_bytes. */
+ * carries its state on).  Bounds that fall somewhere are not followed outside the
+ * buffers, but every output and state of such a call is unspecified.
+ * Sequence b starts from its state if has_state (device int32 [B]) is given and
+ * has_state[b] != 0, else from zero; its last state is stored.
+ * States, and what is read from them to write them, keep 24 significant bits
+ * throughout; where the state, the written values and the scores of a chunk enter
+ * its bf16 outputs they do so to 16 (nvfp4_gdn_step: 24 throughout).
+ * Workspace: nvfp4_gdn_prefill_workspace_bytes, which is enough with beta and without
+ * (a call without uses 13 KB of 31 for a chunk of 64 tokens and value head). */
 size_t nvfp4_gdn_prefill_workspace_bytes(int64_t T, int64_t B, int32_t k_heads, int32_t v_heads, int32_t k_dim,
                                          int32_t v_dim);
 
