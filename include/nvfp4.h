@@ -382,8 +382,8 @@ typedef struct {
  *   positions int64 [T]; slots int64 [T]: the token's cache row, page * page_size
  *             + offset.  A token whose slot is negative or not below num_pages *
  *             page_size, or whose position is outside [0, max_pos), is a padded
- *             row: nothing of it is written.  Slots of one call must differ: of
- *             tokens that share one, which is kept is unspecified.
+ *             row: nothing of it is written.  Slots of one call must differ: the
+ *             contents of a cache row that two tokens share are unspecified.
  *   q_out     bf16 [T], token stride ldqo: the rotated queries (RNE).
  * k (rotated) and v are rounded to bf16 (RNE) and stored as that, or as the codes
  * that nvfp4_kv_fp8_encode gives for it: results are bit-exact to that definition.
