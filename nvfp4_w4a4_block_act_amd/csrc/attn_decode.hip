@@ -9,7 +9,7 @@
 // Layout.  A wave takes tiles of 16 tokens (a page holds whole tiles) for up to 16
 // query heads that share a key-value head.  Lanes load whole rows side by side, 16
 // bytes each -- a load in operand order, 16 rows side by side, costs the vector cache
-// one access a lane, four times as many (67 sequences of up to 4099: 89 us against 78,
+// one access a lane, four times as many (67 sequences of up to 4099: 14 % more time,
 // hints below included) -- and the tile passes through a corner of LDS that only its wave uses:
 //  * scores: S^T = K Q^T (16 x 16 x 32, bf16): lane (r, g) = (lane % 16, lane / 16)
 //    takes 16-byte pieces of token r's key row; which elements of the row a step
@@ -30,9 +30,13 @@
 //
 // Bound by memory: each key and value once.  67 sequences of up to 4099 (350 MB of E4M3,
 // 8 heads of 128) take 71 us, 4.9 TB/s; 6 of up to 32768 (541 MB of bf16, 4 heads of 256)
-// 100 us, 5.4 TB/s; one of 517 tokens 10 us, which is the call.  Bare reads of as many
-// bytes take 51 to 56 and 78 us; rows in scattered places, two streams a workgroup,
-// account for most of the rest, and more tiles or waves in flight made it slower.
+// 100 us, 5.4 TB/s; one of 517 tokens 8.8 us, of which the kernel is 7.3: five tiles one
+// after the other in each of eight waves.  Bare reads of as many bytes take 51 to 56 and
+// 78 us; rows in scattered places, two streams a workgroup, account for most of the rest,
+// and more tiles or waves in flight made it slower.  More than 16 query heads of a key-value
+// head read its tiles once for each 16: 64 of up to 4096 with 24 heads on each of two (82 MB)
+// fetch 99 MB, the second reading mostly from the caches, and take 35 us, 2.3 TB/s, bound by
+// the work on the tiles.  Rows of 64 bytes (16 heads of 64, E4M3, 322 MB): 76 us, 4.2 TB/s.
 #include <algorithm>
 
 #include "attn_splits.hpp"
@@ -72,9 +76,9 @@ struct Tile {
   u32x4_t k[kLoads], v[kLoads];
 };
 
-// A row of whole cache lines is read once and hinted so (67 x 4099 of 128 bytes: 77 us
-// against 84; 6 x 32768 of 512: 111 against 116); rows of 64 bytes share lines with the
-// next head's, which the hint would drop (95 us against 83).
+// A row of whole cache lines is read once and hinted so (67 x 4099 of 128 bytes take 8 % more
+// without, 6 x 32768 of 512 4 %); rows of 64 bytes share lines with the next head's, which the
+// hint would drop (14 % more with it).
 template <int ROW>
 __device__ __forceinline__ u32x4_t load_piece(const uint8_t* p) {
   if constexpr (ROW >= 128) return __builtin_nontemporal_load(reinterpret_cast<const u32x4_t*>(p));
@@ -239,7 +243,7 @@ __global__ __launch_bounds__(kWaves * 64, 2) void attn_decode_kernel(AttnArgs a,
   const int heads = min(16, (kvh + 1) * group - head0);
   // The later splits of shorter sequences are empty, so each XCD has to get all of them
   // alike: where their number and eight have a factor in common, they move on by one each
-  // time the pattern would repeat (16 sequences of up to 8192 in bf16: 67 us against 74).
+  // time the pattern would repeat (16 sequences of up to 8192 in bf16: 10 % more time without).
   const int b = item / splits, split = (item % splits + b / (8 / min(8, splits & -splits))) % splits;
   if (b >= a.B) return;
   const int lane = threadIdx.x % 64, r = lane % 16, g = lane / 16;

@@ -14,12 +14,12 @@ namespace nvfp4 {
 // Splits of a sequence, from sizes the host knows: about twelve workgroups for each CU
 // (uneven lengths even out over them), none with fewer than 512 tokens -- or 256 where
 // there would be less than two workgroups for each CU, but no split, and no second
-// kernel, for less than 1024.  8 heads of 128, E4M3: 67 sequences of up to 4099 take 73 us
-// (eight for each CU 80, sixteen 75), 128 of up to 4096 129 us (132, 125), 160 of up to
-// 1024 49 us (48, 49); 24 of up to 2000, 4 heads of 256 in bf16, 30 us (39 with splits of
-// 512), one of 32768 20 us (23 with splits of 256).  Equal shares of all sequences' tiles,
-// as many as the GPU holds at once, taken from the lengths on the device, were no faster
-// and slower for few sequences (one of 32768: 27 us against 22).
+// kernel, for less than 1024.  8 heads of 128, E4M3, against eight and sixteen for each CU: 67
+// sequences of up to 4099 take 9 % and 3 % less time, 128 of up to 4096 2 % less and 3 % more,
+// 160 of up to 1024 2 % more and as much.  24 of up to 2000, 4 heads of 256 in bf16, take 30 %
+// more with splits of 512, one of 32768 15 % more with splits of 256.  Equal shares of all
+// sequences' tiles, as many as the GPU holds at once, taken from the lengths on the device,
+// were no faster, and a fifth slower for one of 32768.
 struct Splits {
   int count, tokens;  // tokens of one split: a multiple of 16
 };

@@ -10,8 +10,10 @@
 // carries the state from chunk to chunk, a workgroup for 16, 32 or 64 of its columns, or
 // for 128 where there are heads enough; columns touch no other column.  Bound by the latency of that chain: 8192 tokens of 32
 // heads of 128 x 128 take 244 us, of which the first kernel is 48 and 128 chunks one
-// after the other, at 1.5 us (three exchanges through LDS and their barriers), the rest;
-// 6 of up to 8192 without beta 416 us, 86 of them the first kernel.  Memory's part of the former is 40 us.
+// after the other, at 1.5 us (three exchanges through LDS and their barriers), the rest.
+// Without beta also by memory: 6 of up to 8192 take 411 us, 88 of them the first kernel, and
+// move 1434 MB for a call of 663 (P out and in, keys and queries for each kernel and each slab
+// of columns), 280 us at a copy's rate.
 //
 // Precision.  The state is binary32 and its path keeps binary32's accuracy on the
 // bf16 matrix cores (fp32 matrix products run at 1/16 of their rate): q, k and v are
