@@ -36,7 +36,7 @@
 // and more tiles or waves in flight made it slower.  More than 16 query heads of a key-value
 // head read its tiles once for each 16: 64 of up to 4096 with 24 heads on each of two (82 MB)
 // fetch 99 MB, the second reading mostly from the caches, and take 35 us, 2.3 TB/s, bound by
-// the work on the tiles.  Rows of 64 bytes (16 heads of 64, E4M3, 322 MB): 76 us, 4.2 TB/s.
+// the work on the tiles.  Rows of 64 bytes (16 heads of 64, E4M3, 322 MB): 77 us, 4.2 TB/s.
 #include <algorithm>
 
 #include "attn_splits.hpp"
