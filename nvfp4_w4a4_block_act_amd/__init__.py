@@ -626,6 +626,13 @@ def _table(x, dev, dtype, n, what):
     return x
 
 
+def _scratch(workspace, x, nbytes):
+    """A caller's Workspace, or a new one, of x's GPU: its buffer and size."""
+    buf, nbytes = (Workspace(x.device) if workspace is None else workspace).get(nbytes)
+    assert buf is None or buf.get_device() == x.get_device(), "workspace: another device's"
+    return buf, nbytes
+
+
 class PagedKVCache:
     """A paged key-value cache over two tensors [pages, page_size, kv_heads, head_dim] of the
     same strides (any layout whose rows are contiguous, e.g. views of [pages, 2, page_size,
@@ -724,8 +731,7 @@ def attn_decode(q, cache, block_table, seq_lens, max_len=None, scale=None, windo
         lse = torch.empty((B, H), dtype=torch.float32, device=q.device)
     assert lse.dtype == torch.float32 and lse.shape == (B, H) and lse.is_contiguous() and lse.get_device() == dev, "lse"
     ldo = _rows3(out, dev, torch.bfloat16, B, H, D, "out")
-    ws = workspace if workspace is not None else Workspace(q.device)
-    buf, nbytes = ws.get(nvfp4_attn_decode_workspace_bytes(B, H, cache.kv_heads, D, max_len, window))
+    buf, nbytes = _scratch(workspace, q, nvfp4_attn_decode_workspace_bytes(B, H, cache.kv_heads, D, max_len, window))
     nvfp4_attn_decode(q, B, H, ldq, cache.desc, block_table, block_table.stride(0) if B > 1 else pages, seq_lens, max_len,
                       D ** -0.5 if scale is None else scale, window, out, ldo, lse, buf, nbytes, stream)
     return out, lse
@@ -773,8 +779,7 @@ def gdn_prefill(q, k, v, g, beta, state, cu_seqlens, has_state=None, state_index
     first, dims, scale, out, ldo = _gdn_args(q, k, v, g, beta, state, state_index, B, scale, out)
     _table(cu_seqlens, q.get_device(), torch.int32, B + 1, "cu_seqlens: int32 [B + 1]")
     _table(has_state, q.get_device(), torch.int32, B, "has_state: int32 [B]")
-    ws = workspace if workspace is not None else Workspace(q.device)
-    buf, nbytes = ws.get(nvfp4_gdn_prefill_workspace_bytes(T, B, *dims))
+    buf, nbytes = _scratch(workspace, q, nvfp4_gdn_prefill_workspace_bytes(T, B, *dims))
     nvfp4_gdn_prefill(*first, T, B, cu_seqlens, *dims, state, state.shape[0], state_index, has_state, scale, out, ldo,
                       buf, nbytes, stream)
     return out

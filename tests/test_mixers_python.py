@@ -39,6 +39,23 @@ def test_a_captured_calls_scratch_outlives_growth(monkeypatch):
     assert kept and first() is None
 
 
+def test_a_workspace_of_another_device_is_refused(monkeypatch):
+    """Its address would be another device's, or the host's, to the kernel."""
+    class OnGpu:
+        device = "cuda:0"
+
+        def get_device(self):
+            return 0
+
+    monkeypatch.setattr(torch.cuda, "is_current_stream_capturing", lambda: False)
+    ws = nv.Workspace("cpu")
+    with pytest.raises(AssertionError, match="workspace"):
+        nv._scratch(ws, OnGpu(), 64)
+    assert nv._scratch(ws, OnGpu(), 0) == (None, 0)        # nothing is needed
+    buf, n = nv._scratch(None, torch.zeros(1), 64)
+    assert buf.numel() == n == 64
+
+
 def test_growth_on_another_stream_waits_for_it(monkeypatch):
     """A buffer allocated on one stream and last used on another goes back to the allocator
     together with the stream of the call that grows the Workspace."""
