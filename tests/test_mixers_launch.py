@@ -14,8 +14,8 @@ HOST = os.path.join(ROOT, "tests", "abi_host")
 ROCM_INCLUDE = os.path.join(os.environ.get("ROCM_PATH", "/opt/rocm"), "include")
 
 
-def recorded(tmp_path, checker, *sources):
-    """Builds and runs a checker with the host code of .hip sources; its output."""
+def recorded(tmp_path, program, *sources):
+    """Builds and runs a program of tests/abi_host with the host code of .hip sources; its output."""
     gxx = shutil.which("g++")
     try:
         hipcc = build._hipcc()
@@ -30,7 +30,7 @@ def recorded(tmp_path, checker, *sources):
                         os.path.join(build.CSRC, src), "-o", objects[-1]], check=True, capture_output=True, timeout=300)
     exe = str(tmp_path / "check")
     b = subprocess.run([gxx, "-std=c++17", "-O1", "-Wall", "-D__HIP_PLATFORM_AMD__", "-I", ROCM_INCLUDE,
-                        os.path.join(HOST, checker), *objects, "-no-pie", "-Wl,--unresolved-symbols=ignore-in-object-files",
+                        os.path.join(HOST, program), *objects, "-no-pie", "-Wl,--unresolved-symbols=ignore-in-object-files",
                         "-o", exe], capture_output=True, text=True, timeout=300)   # (unresolved: the device code)
     assert b.returncode == 0, b.stderr[-4000:]
     r = subprocess.run([exe], capture_output=True, text=True, timeout=120)
