@@ -394,6 +394,18 @@ nvfp4_status nvfp4_kv_append(const void* q, const void* k, const void* v, int32_
                              const int64_t* slots, const nvfp4_kv_cache* cache, void* q_out, int64_t ldqo,
                              void* stream);
 
+/* nvfp4_kv_append with a norm of each head of q and k before the rotation:
+ *   y = x * (1 / sqrt(mean(x^2) + eps)) * w   over the head's head_dim elements, in
+ * binary32, rounded once, after the rotation.  q_norm, k_norm: fp32 [head_dim], the
+ * weights w for the heads of q and of k; NULL: no norm of these (q_norm needs q).  eps is
+ * finite, >= 0 (a head of zeros stays zero where it is 0).  |x| below 2^60, so that the
+ * squares' sum is finite; everything else as in nvfp4_kv_append. */
+nvfp4_status nvfp4_kv_append_norm(const void* q, const void* k, const void* v, int32_t src_dtype, int64_t T,
+                                  int32_t q_heads, int64_t ldq, int64_t ldk, int64_t ldv, const float* q_norm,
+                                  const float* k_norm, float eps, const float* rope, int32_t rot_dim, int64_t max_pos,
+                                  int32_t interleaved, const int64_t* positions, const int64_t* slots,
+                                  const nvfp4_kv_cache* cache, void* q_out, int64_t ldqo, void* stream);
+
 /* Attention of one new token for each of B sequences over the paged cache:
  *
  *   out[b][h] = sum_j p_j V[j],  p = softmax_j(scale * q[b][h] . K[j]),
@@ -472,6 +484,110 @@ nvfp4_status nvfp4_gdn_prefill(const void* q, int64_t ldq, const void* k, int64_
                                int32_t v_dim, float* state, int64_t num_states, const int32_t* state_index,
                                const int32_t* has_state, float scale, void* out, int64_t ldo, void* workspace,
                                size_t workspace_bytes, void* stream);
+
+/* ---------------------------------------------------------------------------
+ * Drafted tokens (speculative decoding): several new tokens of a sequence at once.
+ *
+ * A step takes, for each of B sequences, a tree of `nodes` tokens (1 to NVFP4_MAX_NODES):
+ * node 0 the last token known, the others drafted.  parents is int32 [B][nodes]: the node
+ * that a node continues, -1 where it continues the context itself; NULL: chains (node i
+ * continues node i - 1).  A node whose parent is neither -1 nor an earlier node, or
+ * whose way to the context meets such a node, is a padded node.  The nodes' keys and
+ * values are appended to the paged cache first, node i at row ctx_lens[b] + i of its
+ * sequence (nvfp4_kv_append, at the position of its depth); after the attention layers and
+ * the output projection nvfp4_verify_drafts says which nodes stay, and nvfp4_kv_compact
+ * moves their rows to where the sequence goes on.
+ *
+ * As for the token mixers, values that live on the device are checked by the kernels, which
+ * never read or write outside the buffers, and calls larger than a launch are refused
+ * (NVFP4_ESHAPE): more than 65535 sequences, (B + 7) times the heads times the nodes above
+ * 2^22 (attention), more than 2^22 chunks of 8192 logits (verification), 2^22 heads
+ * of k and v in all sequences and layers (compaction), or 2^22 pieces of 16 KB (pages).
+ * ------------------------------------------------------------------------- */
+#define NVFP4_MAX_NODES 64
+#define NVFP4_MAX_LAYERS 64
+
+/* Attention of the nodes of each sequence's tree over the paged cache:
+ *
+ *   out[b][i][h] = sum_j p_j V[j],  p = softmax_j(scale * q[b][i][h] . K[j]),
+ *   lse[b][i][h] = log sum_j exp(scale * q[b][i][h] . K[j])
+ * over the context [0, ctx) of the sequence, ctx = ctx_lens[b] (clamped to [0, max_len]),
+ * and the rows ctx + j of the node's ancestors j and of itself; of all these in order, the
+ * last `window` (0: all).  Pages, heads and padding as in nvfp4_attn_decode: tokens on a page number
+ * outside the pool are left out like masked ones, rows that a node does not see may hold
+ * anything (NaN included) without any effect on it, and a padded node gives out = 0, lse = -inf.
+ *
+ *   q          bf16 [B][nodes][q_heads][head_dim], a node's row stride ldq (multiple of 8).
+ *   block_table int32 [B][ldt], ldt >= ceil((max_len + nodes) / page_size).
+ *   max_len    upper bound of the context lengths, known on the host; at most 2^30.
+ *   out        bf16, a node's row stride ldo (multiple of 8); lse fp32 [B][nodes][q_heads] or NULL.
+ *   workspace  device scratch of nvfp4_attn_tree_workspace_bytes (contents need no setup;
+ *              NULL allowed when that is 0).
+ * Scores, the softmax and both sums are fp32; probabilities enter the product with V to 16
+ * significant bits.  The result does not depend on timing. */
+size_t nvfp4_attn_tree_workspace_bytes(int64_t B, int32_t nodes, int32_t q_heads, int32_t kv_heads, int32_t head_dim,
+                                       int64_t max_len, int64_t window);
+
+nvfp4_status nvfp4_attn_tree(const void* q_bf16, int64_t B, int32_t nodes, int32_t q_heads, int64_t ldq,
+                             const nvfp4_kv_cache* cache, const int32_t* block_table, int64_t ldt, const int32_t* ctx_lens,
+                             const int32_t* parents, int64_t max_len, float scale, int64_t window, void* out_bf16,
+                             int64_t ldo, float* lse, void* workspace, size_t workspace_bytes, void* stream);
+
+/* Which drafted tokens the target model accepts, and the token that follows them.
+ *
+ * logits fp32 [B][nodes][vocab], row stride ld, are the target's after each node;
+ * p_i = softmax(logits[b][i] / temperature[b]).  drafts int64 [B][nodes]: the nodes' tokens
+ * (of node 0 not read); a child whose token is outside [0, vocab) is never accepted.
+ * From node 0, which continues the context, the walk goes on at node i:
+ *   - draft_logits NULL (drafts picked without chance, e.g. a drafter's likeliest tokens):
+ *     the children of i in order, each token once: the first for which uniforms[b][i] is
+ *     below the sum of p_i over the children's tokens up to it is accepted;
+ *   - draft_logits fp32 [B][nodes][vocab], row stride ldd (drafts drawn by chance from
+ *     q_i = softmax(draft_logits[b][i] / temperature[b]), a chain): the first child, with
+ *     token x, if uniforms[b][i] * q_i(x) < p_i(x); further children are never accepted;
+ *   - temperature[b] not above 0, or temperature NULL: the first child whose token is the
+ *     largest logit's (the lowest index of equal ones).
+ * Where no child is accepted a last token is drawn: the first whose running sum of weights
+ * exceeds uniforms[b][nodes] times their total.  The weights are p_i without the children's
+ * tokens, or max(p_i - q_i, 0); p_i where i has no children; greedy: the largest logit.
+ * Accepted and last tokens together are distributed as the target model's own.
+ *
+ *   uniforms   fp32 [B][nodes + 1] in [0, 1) (others are clamped, NaN counts as 0); may be
+ *              NULL if temperature (fp32 [B]) is.
+ *   tokens     int64 [B][nodes]: the accepted tokens, then the last one; -1 behind it.
+ *   path       int32 [B][nodes]: node 0, the accepted nodes; -1 behind them.
+ *   counts     int32 [B]: the nodes on the path, which is also the number of tokens.
+ * A sequence whose node 0 is not a child of the context is padded: count 0, all -1.  A
+ * logit of -inf is a probability of 0; a last row of nothing else gives the token -1.  +inf
+ * and NaN never fault, what they give is unspecified.
+ * Probabilities and their sums are binary64, so results are those of the definition but
+ * where a uniform number lies within about 2^-40 of a border; they do not depend on timing.
+ * workspace: nvfp4_verify_drafts_workspace_bytes (contents need no setup). */
+size_t nvfp4_verify_drafts_workspace_bytes(int64_t B, int32_t nodes, int64_t vocab, int32_t with_draft_logits);
+
+nvfp4_status nvfp4_verify_drafts(const float* logits, int64_t B, int32_t nodes, int64_t vocab, int64_t ld,
+                                 const float* draft_logits, int64_t ldd, const int64_t* drafts, const int32_t* parents,
+                                 const float* temperature, const float* uniforms, int64_t* tokens, int32_t* path,
+                                 int32_t* counts, void* workspace, size_t workspace_bytes, void* stream);
+
+/* Moves the rows of the accepted nodes to where the sequence goes on: row ctx + path[b][i]
+ * to row ctx + i, ctx = ctx_lens[b], for i < counts[b] (clamped to [0, nodes]), in the caches
+ * of all layers: a HOST array of 1 to NVFP4_MAX_LAYERS caches of the same sizes, strides and
+ * type (NVFP4_ESHAPE), of which no rows overlap (NVFP4_EINVAL).  path int32 [B][nodes], as
+ * nvfp4_verify_drafts gives it; every row is read before one is written, so entries may be in
+ * any order.  A row is left out if its path entry is outside [0, nodes), or either row lies
+ * behind the ldt pages of the block table or on a page outside the pool.  Two sequences must
+ * not have a page in common that a row moves in: what it then holds is unspecified. */
+nvfp4_status nvfp4_kv_compact(const nvfp4_kv_cache* caches, int32_t layers, const int32_t* block_table, int64_t ldt,
+                              int64_t B, int32_t nodes, const int32_t* ctx_lens, const int32_t* path,
+                              const int32_t* counts, void* stream);
+
+/* Copies page src[i] to page dst[i], i < n (device int32), in the caches of all layers (as for
+ * nvfp4_kv_compact): the pages that a sequence forked from another needs for itself.  A pair
+ * with a page outside the pool is left out.  The pages of dst must differ from each other
+ * and from those of src: what they otherwise hold is unspecified. */
+nvfp4_status nvfp4_kv_copy_pages(const nvfp4_kv_cache* caches, int32_t layers, const int32_t* src, const int32_t* dst,
+                                 int64_t n, void* stream);
 
 /* ---------------------------------------------------------------------------
  * Diagnostic: the device conversion steps the encoders and GEMMs are built

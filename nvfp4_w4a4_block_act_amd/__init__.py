@@ -112,11 +112,28 @@ def _declare(lib):
     lib.nvfp4_kv_append.restype = ctypes.c_int
     lib.nvfp4_kv_append.argtypes = [_vp, _vp, _vp, _i32, _i64, _i32, _i64, _i64, _i64, _vp, _i32, _i64, _i32, _vp,
                                     _vp, cache_p, _vp, _i64, _vp]
+    lib.nvfp4_kv_append_norm.restype = ctypes.c_int
+    lib.nvfp4_kv_append_norm.argtypes = [_vp, _vp, _vp, _i32, _i64, _i32, _i64, _i64, _i64, _vp, _vp, _f32, _vp, _i32,
+                                         _i64, _i32, _vp, _vp, cache_p, _vp, _i64, _vp]
     lib.nvfp4_attn_decode_workspace_bytes.restype = _sz
     lib.nvfp4_attn_decode_workspace_bytes.argtypes = [_i64, _i32, _i32, _i32, _i64, _i64]
     lib.nvfp4_attn_decode.restype = ctypes.c_int
     lib.nvfp4_attn_decode.argtypes = [_vp, _i64, _i32, _i64, cache_p, _vp, _i64, _vp, _i64, _f32, _i64, _vp, _i64,
                                       _vp, _vp, _sz, _vp]
+    lib.nvfp4_attn_tree_workspace_bytes.restype = _sz
+    lib.nvfp4_attn_tree_workspace_bytes.argtypes = [_i64, _i32, _i32, _i32, _i32, _i64, _i64]
+    lib.nvfp4_attn_tree.restype = ctypes.c_int
+    lib.nvfp4_attn_tree.argtypes = [_vp, _i64, _i32, _i32, _i64, cache_p, _vp, _i64, _vp, _vp, _i64, _f32, _i64, _vp, _i64,
+                                    _vp, _vp, _sz, _vp]
+    lib.nvfp4_verify_drafts_workspace_bytes.restype = _sz
+    lib.nvfp4_verify_drafts_workspace_bytes.argtypes = [_i64, _i32, _i64, _i32]
+    lib.nvfp4_verify_drafts.restype = ctypes.c_int
+    lib.nvfp4_verify_drafts.argtypes = [_vp, _i64, _i32, _i64, _i64, _vp, _i64, _vp, _vp, _vp, _vp, _vp, _vp, _vp, _vp, _sz,
+                                        _vp]
+    lib.nvfp4_kv_compact.restype = ctypes.c_int
+    lib.nvfp4_kv_compact.argtypes = [cache_p, _i32, _vp, _i64, _i64, _i32, _vp, _vp, _vp, _vp]
+    lib.nvfp4_kv_copy_pages.restype = ctypes.c_int
+    lib.nvfp4_kv_copy_pages.argtypes = [cache_p, _i32, _vp, _vp, _i64, _vp]
     gdn = [_vp, _i64, _vp, _i64, _vp, _i64, _vp, _i64, _vp, _i64]
     lib.nvfp4_gdn_step.restype = ctypes.c_int
     lib.nvfp4_gdn_step.argtypes = gdn + [_i64, _i32, _i32, _i32, _i32, _vp, _i64, _vp, _f32, _vp, _i64, _vp]
@@ -300,6 +317,15 @@ def nvfp4_kv_append(q, k, v, src_dtype, T, q_heads, ldq, ldk, ldv, rope, rot_dim
                                   ldqo, _stream(stream)), "nvfp4_kv_append")
 
 
+def nvfp4_kv_append_norm(q, k, v, src_dtype, T, q_heads, ldq, ldk, ldv, q_norm, k_norm, eps, rope, rot_dim, max_pos, interleaved,
+                         positions, slots, cache, q_out, ldqo, stream=None):
+    """``cache`` is a KVCacheDesc."""
+    _check(_lib().nvfp4_kv_append_norm(_ptr(q), k.data_ptr(), v.data_ptr(), src_dtype, T, q_heads, ldq, ldk, ldv, _ptr(q_norm),
+                                       _ptr(k_norm), eps, _ptr(rope), rot_dim, max_pos, interleaved, _ptr(positions),
+                                       slots.data_ptr(), ctypes.byref(cache), _ptr(q_out), ldqo, _stream(stream)),
+           "nvfp4_kv_append_norm")
+
+
 def nvfp4_attn_decode_workspace_bytes(B, q_heads, kv_heads, head_dim, max_len, window):
     return _lib().nvfp4_attn_decode_workspace_bytes(B, q_heads, kv_heads, head_dim, max_len, window)
 
@@ -330,6 +356,42 @@ def nvfp4_gdn_prefill(q, ldq, k, ldk, v, ldv, g, ldg, beta, ldb, T, B, cu_seqlen
                                     cu_seqlens.data_ptr(), k_heads, v_heads, k_dim, v_dim, state.data_ptr(), num_states,
                                     _ptr(state_index), _ptr(has_state), scale, out.data_ptr(), ldo, _ptr(workspace),
                                     workspace_bytes, _stream(stream)), "nvfp4_gdn_prefill")
+
+
+def nvfp4_attn_tree_workspace_bytes(B, nodes, q_heads, kv_heads, head_dim, max_len, window):
+    return _lib().nvfp4_attn_tree_workspace_bytes(B, nodes, q_heads, kv_heads, head_dim, max_len, window)
+
+
+def nvfp4_attn_tree(q, B, nodes, q_heads, ldq, cache, block_table, ldt, ctx_lens, parents, max_len, scale, window, out, ldo, lse,
+                    workspace, workspace_bytes, stream=None):
+    """``cache`` is a KVCacheDesc."""
+    _check(_lib().nvfp4_attn_tree(q.data_ptr(), B, nodes, q_heads, ldq, ctypes.byref(cache), block_table.data_ptr(), ldt,
+                                  ctx_lens.data_ptr(), _ptr(parents), max_len, scale, window, out.data_ptr(), ldo, _ptr(lse),
+                                  _ptr(workspace), workspace_bytes, _stream(stream)), "nvfp4_attn_tree")
+
+
+def nvfp4_verify_drafts_workspace_bytes(B, nodes, vocab, with_draft_logits):
+    return _lib().nvfp4_verify_drafts_workspace_bytes(B, nodes, vocab, with_draft_logits)
+
+
+def nvfp4_verify_drafts(logits, B, nodes, vocab, ld, draft_logits, ldd, drafts, parents, temperature, uniforms, tokens, path,
+                        counts, workspace, workspace_bytes, stream=None):
+    _check(_lib().nvfp4_verify_drafts(logits.data_ptr(), B, nodes, vocab, ld, _ptr(draft_logits), ldd, drafts.data_ptr(),
+                                      _ptr(parents), _ptr(temperature), _ptr(uniforms), tokens.data_ptr(), path.data_ptr(),
+                                      counts.data_ptr(), _ptr(workspace), workspace_bytes, _stream(stream)),
+           "nvfp4_verify_drafts")
+
+
+def nvfp4_kv_compact(caches, layers, block_table, ldt, B, nodes, ctx_lens, path, counts, stream=None):
+    """``caches`` is a ctypes array of KVCacheDesc."""
+    _check(_lib().nvfp4_kv_compact(caches, layers, block_table.data_ptr(), ldt, B, nodes, ctx_lens.data_ptr(), path.data_ptr(),
+                                   counts.data_ptr(), _stream(stream)), "nvfp4_kv_compact")
+
+
+def nvfp4_kv_copy_pages(caches, layers, src, dst, n, stream=None):
+    """``caches`` is a ctypes array of KVCacheDesc."""
+    _check(_lib().nvfp4_kv_copy_pages(caches, layers, src.data_ptr(), dst.data_ptr(), n, _stream(stream)),
+           "nvfp4_kv_copy_pages")
 
 
 # ---- convenience layer: allocate with torch, call the C ABI --------------------------
@@ -671,13 +733,15 @@ class PagedKVCache:
 
 
 @_on_device
-def kv_append(k, v, cache, slots, q=None, positions=None, rope=None, interleaved=False, q_out=None, *, stream=None):
+def kv_append(k, v, cache, slots, q=None, positions=None, rope=None, interleaved=False, q_out=None, q_norm=None, k_norm=None,
+              eps=1e-6, *, stream=None):
     """Rotates k (and q) by position, and appends k and v to a PagedKVCache at rows ``slots``.
 
     k, v: fp32 or bf16 [T, kv_heads, head_dim]; q: the same type, [T, q_heads, head_dim].
     slots, positions: int64 [T] (slot < 0: a padded row); rope: fp32 [max_pos, rot_dim], the
-    cosines of a position's angles, then their sines; None: no rotation.  Returns q, rotated, as
-    bf16 (None without q)."""
+    cosines of a position's angles, then their sines; None: no rotation.  q_norm, k_norm: fp32
+    [head_dim], the weights of a norm of each head before the rotation, x / sqrt(mean(x^2) + eps) * w;
+    None: no norm.  Returns q, rotated, as bf16 (None without q)."""
     dev, D = cache.device_index, cache.head_dim
     T = k.shape[0]
     assert k.dtype in (torch.float32, torch.bfloat16), "k: fp32 or bf16"
@@ -700,6 +764,13 @@ def kv_append(k, v, cache, slots, q=None, positions=None, rope=None, interleaved
         ldqo = _rows3(q_out, dev, torch.bfloat16, T, heads, D, "q_out")
     else:
         assert q_out is None, "q_out needs q"
+    if q_norm is not None or k_norm is not None:
+        _table(q_norm, dev, torch.float32, D, "q_norm: fp32 [head_dim]")
+        _table(k_norm, dev, torch.float32, D, "k_norm: fp32 [head_dim]")
+        assert q is not None or q_norm is None, "q_norm needs q"
+        nvfp4_kv_append_norm(q, k, v, DTYPE[k.dtype], T, heads, ldq, ldk, ldv, q_norm, k_norm, eps, rope, rot, far,
+                             bool(interleaved), positions, slots, cache.desc, q_out, ldqo, stream)
+        return q_out
     nvfp4_kv_append(q, k, v, DTYPE[k.dtype], T, heads, ldq, ldk, ldv, rope, rot, far, bool(interleaved), positions, slots,
                     cache.desc, q_out, ldqo, stream)
     return q_out
@@ -783,3 +854,133 @@ def gdn_prefill(q, k, v, g, beta, state, cu_seqlens, has_state=None, state_index
     nvfp4_gdn_prefill(*first, T, B, cu_seqlens, *dims, state, state.shape[0], state_index, has_state, scale, out, ldo,
                       buf, nbytes, stream)
     return out
+
+
+# ---- drafted tokens: tree attention, verification, cache rows and pages that move -------
+def _block_table(x, dev, B):
+    """Checks a block table [B, pages]; its row stride."""
+    assert x.dtype is torch.int32 and x.dim() == 2 and x.shape[0] == B and x.get_device() == dev and \
+        (x.stride(1) == 1 or x.shape[1] <= 1), "block_table: int32 [B, pages]"
+    return x.stride(0) if B > 1 else x.shape[1]
+
+
+def _dense(x, dev, dtype, shape, what):
+    """Checks a contiguous tensor (None passes)."""
+    if x is not None:
+        assert x.dtype is dtype and x.shape == shape and x.get_device() == dev and x.is_contiguous(), what
+    return x
+
+
+@_on_device
+def attn_tree(q, cache, block_table, ctx_lens, parents=None, max_len=None, scale=None, window=0, workspace=None, out=None,
+              lse=None, *, stream=None):
+    """Attention of a tree of drafted tokens a sequence over a PagedKVCache -> (out bf16 [B, nodes, q_heads,
+    head_dim], lse fp32 [B, nodes, q_heads]).
+
+    q: bf16 [B, nodes, q_heads, head_dim], up to 64 nodes; block_table: int32 [B, pages]; ctx_lens: int32 [B],
+    the tokens before the tree, whose node i is in the cache at ctx_lens[b] + i.  parents: int32 [B, nodes], the
+    node that each continues (-1: the context; anything else than an earlier node: a padded node); None: chains.
+    A node attends to the context, its ancestors and itself, of these to the last ``window`` (0: all).  max_len:
+    a bound of ctx_lens (default: what the table holds beside the nodes); scale: default head_dim ** -0.5."""
+    dev, D = cache.device_index, cache.head_dim
+    assert q.dim() == 4, "q: bf16 [B, nodes, q_heads, head_dim]"
+    B, W, H = q.shape[0], q.shape[1], q.shape[2]
+    assert B <= 1 or W <= 1 or q.stride(0) == W * q.stride(1), "q: a sequence's nodes must follow the last one's"
+    ldq = _rows3(q.view(B * W, H, D) if q.is_contiguous() else q.flatten(0, 1), dev, torch.bfloat16, B * W, H, D, "q")
+    ldt = _block_table(block_table, dev, B)
+    room = block_table.shape[1] * cache.page_size - W
+    if max_len is None:
+        max_len = room
+    assert 0 <= max_len <= room, "max_len: more than the block table holds beside the nodes"
+    _table(ctx_lens, dev, torch.int32, B, "ctx_lens: int32 [B]")
+    _dense(parents, dev, torch.int32, (B, W), "parents: contiguous int32 [B, nodes]")
+    if out is None:
+        out = torch.empty((B, W, H, D), dtype=torch.bfloat16, device=q.device)
+    if lse is None:
+        lse = torch.empty((B, W, H), dtype=torch.float32, device=q.device)
+    _dense(out, dev, torch.bfloat16, (B, W, H, D), "out: contiguous bf16 [B, nodes, q_heads, head_dim]")
+    _dense(lse, dev, torch.float32, (B, W, H), "lse: contiguous fp32 [B, nodes, q_heads]")
+    buf, nbytes = _scratch(workspace, q, nvfp4_attn_tree_workspace_bytes(B, W, H, cache.kv_heads, D, max_len, window))
+    nvfp4_attn_tree(q, B, W, H, ldq, cache.desc, block_table, ldt, ctx_lens, parents, max_len,
+                    D ** -0.5 if scale is None else scale, window, out, H * D, lse, buf, nbytes, stream)
+    return out, lse
+
+
+@_on_device
+def verify_drafts(logits, drafts, parents=None, temperature=None, uniforms=None, draft_logits=None, workspace=None, out=None, *,
+                  stream=None):
+    """Which drafted tokens the target model accepts, and the token after them -> (tokens int64 [B, nodes],
+    path int32 [B, nodes], counts int32 [B]): the first counts[b] of tokens[b] are the accepted tokens and the
+    last one, of path[b] node 0 and the accepted nodes; -1 behind them.
+
+    logits: fp32 [B, nodes, vocab], the target's after each node; drafts: int64 [B, nodes], the nodes' tokens
+    (node 0: the last token known, not read); parents: as for attn_tree (None: chains); temperature: fp32 [B],
+    0 for the greedy rule (None: all of them); uniforms: fp32 [B, nodes + 1], random numbers of [0, 1): one for
+    each node's children, then one for the last token; draft_logits: fp32 [B, nodes, vocab] where a chain's tokens
+    were drawn from their softmax at the same temperature (None: the drafts were picked without chance)."""
+    dev = logits.get_device()
+    assert logits.dim() == 3, "logits: fp32 [B, nodes, vocab]"
+    B, W, V = logits.shape
+
+    def rows(x, what):
+        assert x.dtype is torch.float32 and x.shape == (B, W, V) and x.get_device() == dev, what
+        if x.is_contiguous():
+            return V
+        s0, s1, s2 = x.stride()
+        assert (s2 == 1 or V == 1) and (B <= 1 or W <= 1 or s0 == W * s1), f"{what}: rows must be contiguous and evenly spaced"
+        return s1 if W > 1 else (s0 if B > 1 else V)
+    ld = rows(logits, "logits: fp32 [B, nodes, vocab]")
+    ldd = rows(draft_logits, "draft_logits: fp32 [B, nodes, vocab]") if draft_logits is not None else 0
+    _dense(drafts, dev, torch.int64, (B, W), "drafts: contiguous int64 [B, nodes]")
+    _dense(parents, dev, torch.int32, (B, W), "parents: contiguous int32 [B, nodes]")
+    _dense(temperature, dev, torch.float32, (B,), "temperature: contiguous fp32 [B]")
+    _dense(uniforms, dev, torch.float32, (B, W + 1), "uniforms: contiguous fp32 [B, nodes + 1]")
+    assert temperature is None or uniforms is not None, "temperature needs uniforms"
+    if out is None:
+        out = (torch.empty((B, W), dtype=torch.int64, device=logits.device),
+               torch.empty((B, W), dtype=torch.int32, device=logits.device),
+               torch.empty(B, dtype=torch.int32, device=logits.device))
+    tokens, path, counts = out
+    _dense(tokens, dev, torch.int64, (B, W), "tokens: contiguous int64 [B, nodes]")
+    _dense(path, dev, torch.int32, (B, W), "path: contiguous int32 [B, nodes]")
+    _dense(counts, dev, torch.int32, (B,), "counts: contiguous int32 [B]")
+    sampled = draft_logits is not None and temperature is not None
+    buf, nbytes = _scratch(workspace, logits, nvfp4_verify_drafts_workspace_bytes(B, W, V, sampled))
+    nvfp4_verify_drafts(logits, B, W, V, ld, draft_logits, ldd, drafts, parents, temperature, uniforms, tokens, path, counts,
+                        buf, nbytes, stream)
+    return tokens, path, counts
+
+
+def _layers(caches, dev):
+    """The descriptors of one cache or of several layers' as an array."""
+    caches = [caches] if isinstance(caches, PagedKVCache) else caches
+    assert all(c.device_index == dev for c in caches), "caches: another device's"
+    return (KVCacheDesc * len(caches))(*[c.desc for c in caches]), len(caches)
+
+
+@_on_device
+def kv_compact(block_table, ctx_lens, path, counts, caches, *, stream=None):
+    """Moves the rows of accepted nodes to where their sequences go on, in one PagedKVCache or those of all layers
+    (a list of up to 64 of one shape): row ctx_lens[b] + path[b, i] to ctx_lens[b] + i for i < counts[b].
+
+    block_table: int32 [B, pages]; ctx_lens, counts: int32 [B]; path: int32 [B, nodes] (see verify_drafts)."""
+    dev = block_table.get_device()
+    B = block_table.shape[0]
+    ldt = _block_table(block_table, dev, B)
+    assert path.dim() == 2, "path: int32 [B, nodes]"
+    _dense(path, dev, torch.int32, (B, path.shape[1]), "path: contiguous int32 [B, nodes]")
+    _table(ctx_lens, dev, torch.int32, B, "ctx_lens: int32 [B]")
+    _table(counts, dev, torch.int32, B, "counts: int32 [B]")
+    descs, n = _layers(caches, dev)
+    nvfp4_kv_compact(descs, n, block_table, ldt, B, path.shape[1], ctx_lens, path, counts, stream)
+
+
+@_on_device
+def kv_copy_pages(src, dst, caches, *, stream=None):
+    """Copies page src[i] to page dst[i] (int32 [n]) in one PagedKVCache or those of all layers (a list of up to 64
+    of one shape)."""
+    dev, n = src.get_device(), src.shape[0]
+    _table(src, dev, torch.int32, n, "src: int32 [n]")
+    _table(dst, dev, torch.int32, n, "dst: int32 [n]")
+    descs, layers = _layers(caches, dev)
+    nvfp4_kv_copy_pages(descs, layers, src, dst, n, stream)

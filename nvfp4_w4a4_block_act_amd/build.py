@@ -17,8 +17,8 @@ LIB = os.path.join(PKG, "libnvfp4_w4a4.so")
 ARCH = "gfx950"
 
 HIP_SOURCES = ["quantize.hip", "gemm_skinny.hip", "gemm_mfma.hip", "kv_fp8.hip", "kv_append.hip", "attn_decode.hip",
-               "gdn_step.hip", "gdn_prefill.hip", "stream_probe.hip"]
-HOST_SOURCES = ["api.cpp", "api_mixers.cpp", "dispatch.cpp"]
+               "gdn_step.hip", "gdn_prefill.hip", "attn_tree.hip", "verify.hip", "kv_move.hip", "stream_probe.hip"]
+HOST_SOURCES = ["api.cpp", "api_mixers.cpp", "api_drafts.cpp", "dispatch.cpp"]
 
 COMMON = ["-O3", "-std=c++17", "-fPIC", "-Wall", "-Wno-unused-function"]
 DEVICE = [f"--offload-arch={ARCH}", "-ffp-contract=off",

@@ -5,99 +5,13 @@
 #include <math.h>
 #include <stdint.h>
 
-#include <utility>
-
-#include "api_checks.hpp"
+#include "cache_checks.hpp"
 #include "launch.hpp"
 #include "mixers.hpp"
 
 namespace {
 
 using namespace nvfp4::checks;
-
-constexpr int64_t kMaxStride = (int64_t)1 << 40;  // cache strides, in elements: extents stay inside int64
-constexpr int kMaxHeads = 1 << 16;
-constexpr int64_t kMaxLen = (int64_t)1 << 30;     // token index plus a split's tokens stay inside int32
-constexpr int64_t kMaxGroups = 1 << 22;  // workgroups of a launch: at most 2^32 threads
-
-size_t cache_elem(const nvfp4_kv_cache& c) { return c.dtype == NVFP4_E4M3 ? 1 : 2; }
-
-// Elements that the rows of one cache tensor span.
-int64_t cache_span(const nvfp4_kv_cache& c) {
-  return c.num_pages == 0 ? 0
-                          : (c.num_pages - 1) * c.page_stride + (int64_t)(c.page_size - 1) * c.token_stride +
-                                (int64_t)(c.kv_heads - 1) * c.head_stride + c.head_dim;
-}
-
-// The three axes that a row's place in a cache tensor has, by growing stride.
-struct Axes {
-  int64_t stride[3], count[3];
-};
-Axes axes_of(const nvfp4_kv_cache& c) {
-  Axes a = {{c.head_stride, c.token_stride, c.page_stride}, {c.kv_heads, c.page_size, c.num_pages}};
-  for (int i = 0; i < 3; ++i)
-    for (int j = i + 1; j < 3; ++j)
-      if (a.stride[j] < a.stride[i]) {
-        std::swap(a.stride[i], a.stride[j]);
-        std::swap(a.count[i], a.count[j]);
-      }
-  return a;
-}
-
-// Rows of one tensor do not overlap: each axis steps over what the smaller ones span (an
-// axis of one element has no stride).
-bool rows_disjoint(const Axes& a, int64_t dim) {
-  int64_t span = dim;
-  for (int i = 0; i < 3; ++i) {
-    if (a.count[i] <= 1) continue;
-    if (a.stride[i] < span) return false;
-    span += (a.count[i] - 1) * a.stride[i];
-  }
-  return true;
-}
-
-// Whether two rows of tensors `rest` elements apart, which differ by any steps along the
-// axes up to `axis`, have an element in common.  Since an axis steps over what the smaller
-// ones span, only the two steps on either side of `rest` come near enough.
-bool rows_meet(const Axes& a, int64_t dim, int64_t rest, int axis) {
-  if (axis < 0) return rest > -dim && rest < dim;
-  if (a.count[axis] <= 1) return rows_meet(a, dim, rest, axis - 1);
-  const int64_t most = a.count[axis] - 1, stride = a.stride[axis];
-  const int64_t below = rest / stride - (rest % stride < 0 ? 1 : 0);
-  for (const int64_t n : {below, below + 1})
-    if (n >= -most && n <= most && rows_meet(a, dim, rest - n * stride, axis - 1)) return true;
-  return false;
-}
-
-// No row of k overlaps one of v (rows_disjoint holds): they may lie interleaved.
-bool tensors_disjoint(const nvfp4_kv_cache& c, const Axes& a) {
-  if (c.num_pages == 0) return true;
-  const uintptr_t k = reinterpret_cast<uintptr_t>(c.k), v = reinterpret_cast<uintptr_t>(c.v);
-  const uintptr_t apart = (k < v ? v - k : k - v) / cache_elem(c);  // whole elements: both are aligned
-  return apart >= (uintptr_t)1 << 60 || !rows_meet(a, c.head_dim, (int64_t)apart, 2);  // spans are below 2^58
-}
-
-nvfp4_status check_cache(const nvfp4_kv_cache* c) {
-  if (!c) return NVFP4_EINVAL;
-  if (c->num_pages < 0 || c->page_size < 1 || c->kv_heads < 1) return NVFP4_EINVAL;
-  if (c->dtype != NVFP4_BF16 && c->dtype != NVFP4_E4M3) return NVFP4_EINVAL;
-  if (c->head_dim != 64 && c->head_dim != 128 && c->head_dim != 256) return NVFP4_ESHAPE;
-  if (c->page_size % 16 != 0 || c->page_size > (1 << 20) || c->kv_heads > kMaxHeads || c->num_pages >= kMaxDim)
-    return NVFP4_ESHAPE;
-  for (int64_t s : {c->page_stride, c->token_stride, c->head_stride})
-    if (s < 0 || s >= kMaxStride) return NVFP4_ESHAPE;
-  if (c->token_stride >= (1 << 26)) return NVFP4_ESHAPE;  // 16 rows within 32-bit byte offsets
-  // (num_pages - 1) * page_stride must stay far inside int64
-  if (c->num_pages > 1 && c->page_stride > ((int64_t)1 << 56) / c->num_pages) return NVFP4_ESHAPE;
-  const Axes axes = axes_of(*c);
-  if (!rows_disjoint(axes, c->head_dim)) return NVFP4_ESHAPE;
-  if (c->num_pages > 0 && (!c->k || !c->v || c->k == c->v)) return NVFP4_EINVAL;
-  if (c->dtype == NVFP4_E4M3 && (!c->k_amax || !c->v_amax)) return NVFP4_EINVAL;
-  if (!all_aligned({c->k, c->v, c->k_amax, c->v_amax})) return NVFP4_EALIGN;
-  const int64_t unit = 16 / (int64_t)cache_elem(*c);
-  if (c->page_stride % unit || c->token_stride % unit || c->head_stride % unit) return NVFP4_EALIGN;
-  return tensors_disjoint(*c, axes) ? NVFP4_OK : NVFP4_EINVAL;
-}
 
 nvfp4_status check_append(const nvfp4::AppendArgs& a, int32_t src_dtype, const nvfp4_kv_cache* cache) {
   const nvfp4_status s = check_cache(cache);
@@ -112,7 +26,7 @@ nvfp4_status check_append(const nvfp4::AppendArgs& a, int32_t src_dtype, const n
   if (a.T == 0) return NVFP4_OK;
   if (!a.k || !a.v || !a.slots || (a.rot > 0 && (!a.rope || !a.positions))) return NVFP4_EINVAL;
   const int elem = src_dtype == NVFP4_F32 ? 4 : 2, unit = 16 / elem;
-  if (!all_aligned({a.q, a.k, a.v, a.rope, a.positions, a.slots, a.q_out})) return NVFP4_EALIGN;
+  if (!all_aligned({a.q, a.k, a.v, a.rope, a.positions, a.slots, a.q_out, a.q_norm, a.k_norm})) return NVFP4_EALIGN;
   if (a.ldk % unit || a.ldv % unit || (a.q && (a.ldq % unit || a.ldqo % 8))) return NVFP4_EALIGN;
   const size_t span = (size_t)cache_span(*cache) * cache_elem(*cache);
   const Buf ins[] = {{a.q, extent(a.T, qw, a.ldq, elem)},
@@ -121,6 +35,8 @@ nvfp4_status check_append(const nvfp4::AppendArgs& a, int32_t src_dtype, const n
                      {a.rope, a.rot ? (size_t)(a.max_pos * a.rot) * 4 : 0},
                      {a.positions, a.rot ? (size_t)a.T * 8 : 0},
                      {a.slots, (size_t)a.T * 8},
+                     {a.q_norm, (size_t)dim * 4},
+                     {a.k_norm, (size_t)dim * 4},
                      {cache->k_amax, cache->dtype == NVFP4_E4M3 ? 4u : 0u},
                      {cache->v_amax, cache->dtype == NVFP4_E4M3 ? 4u : 0u}};
   // k and v of the cache may lie interleaved: check_cache holds their rows against each other
@@ -217,6 +133,21 @@ nvfp4_status nvfp4_kv_append(const void* q, const void* k, const void* v, int32_
                              void* stream) {
   nvfp4::AppendArgs a{q,     k,         v,     T, ldq, ldk, ldv, ldqo, max_pos, rope, positions, slots,
                       static_cast<uint16_t*>(q_out), {}, q_heads, rot_dim, interleaved != 0, src_dtype == NVFP4_F32};
+  const nvfp4_status s = check_append(a, src_dtype, cache);
+  if (s != NVFP4_OK || T == 0) return s;
+  a.cache = *cache;
+  return launched(nvfp4::launch_kv_append(a, static_cast<hipStream_t>(stream)));
+}
+
+nvfp4_status nvfp4_kv_append_norm(const void* q, const void* k, const void* v, int32_t src_dtype, int64_t T,
+                                  int32_t q_heads, int64_t ldq, int64_t ldk, int64_t ldv, const float* q_norm,
+                                  const float* k_norm, float eps, const float* rope, int32_t rot_dim, int64_t max_pos,
+                                  int32_t interleaved, const int64_t* positions, const int64_t* slots,
+                                  const nvfp4_kv_cache* cache, void* q_out, int64_t ldqo, void* stream) {
+  nvfp4::AppendArgs a{q,     k,         v,     T, ldq, ldk, ldv, ldqo, max_pos, rope, positions, slots,
+                      static_cast<uint16_t*>(q_out), {}, q_heads, rot_dim, interleaved != 0, src_dtype == NVFP4_F32,
+                      q_norm, k_norm, eps};
+  if (!isfinite(eps) || eps < 0.0f || (q_norm && !q && T > 0)) return NVFP4_EINVAL;
   const nvfp4_status s = check_append(a, src_dtype, cache);
   if (s != NVFP4_OK || T == 0) return s;
   a.cache = *cache;

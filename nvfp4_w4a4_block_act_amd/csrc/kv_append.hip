@@ -12,6 +12,11 @@
 // rows in, the rows out and one table row for each token; a token's heads find the table
 // row in the caches.  32768 tokens of 40 + 2 x 8 heads of 128, fp32 to FP8: 221 us,
 // 6.1 TB/s (245 us with 256 threads a token; hinted loads 254, stores too 242).
+//
+// With norms (nvfp4_kv_append_norm) a head of q or k is first y = x * (1 / sqrt(mean(x^2) +
+// eps)) * w: its head_dim / 16 items sit in as many lanes side by side of one wave (their
+// number is a power of two, and heads start at its multiples), which add their squares by
+// exchanges, in binary32; the values stay in registers between norm, rotation and rounding.
 #include <algorithm>
 
 #include "common.hpp"
@@ -48,7 +53,22 @@ __device__ __forceinline__ uint2 coded_run(uint4 w, float g) {
                     kv_encode_pair(w.z, g) | (kv_encode_pair(w.w, g) << 16));
 }
 
-template <bool F32, bool FP8>
+// Norm of one head, the 16 elements of this thread: per lanes side by side hold the head.
+__device__ __forceinline__ void norm_head(float (&x)[8], float (&y)[8], const float* w, int o1, int o2, int per, float eps) {
+  float sum = 0;
+#pragma unroll
+  for (int j = 0; j < 8; ++j) sum += x[j] * x[j] + y[j] * y[j];
+  for (int m = 1; m < per; m *= 2) sum += __shfl_xor(sum, m);
+  const float mean = sum / (float)(per * 16) + eps;
+  const float by = mean > 0.0f ? 1.0f / sqrtf(mean) : 0.0f;
+  float w1[8], w2[8];
+  load8<true>(w, o1, w1);
+  load8<true>(w, o2, w2);
+#pragma unroll
+  for (int j = 0; j < 8; ++j) x[j] = x[j] * by * w1[j], y[j] = y[j] * by * w2[j];
+}
+
+template <bool F32, bool FP8, bool NORM>
 __global__ __launch_bounds__(512) void kv_append_kernel(AppendArgs a) {
   const int64_t t = blockIdx.x;
   const nvfp4_kv_cache& c = a.cache;
@@ -75,6 +95,10 @@ __global__ __launch_bounds__(512) void kv_append_kernel(AppendArgs a) {
     float x[8], y[8];
     load8<F32>(src, from + o1, x);
     load8<F32>(src, from + o2, y);
+    if constexpr (NORM) {
+      const float* w = is_q ? a.q_norm : (is_v ? nullptr : a.k_norm);
+      if (w) norm_head(x, y, w, o1, o2, per, a.eps);
+    }
     if (turned) {
       float cs[8], sn[8];
       load8<true>(row, r * 8, cs);
@@ -118,19 +142,24 @@ __global__ __launch_bounds__(512) void kv_append_kernel(AppendArgs a) {
   }
 }
 
-hipError_t launch_kv_append(const AppendArgs& a, hipStream_t stream) {
+template <bool NORM>
+static hipError_t launch_norm(const AppendArgs& a, hipStream_t stream) {
   const int64_t items = (int64_t)((a.q ? a.q_heads : 0) + 2 * a.cache.kv_heads) * (a.cache.head_dim / 16);
   const dim3 grid((unsigned)a.T), block((unsigned)std::min<int64_t>(512, (items + 63) / 64 * 64));
   const bool fp8 = a.cache.dtype == NVFP4_E4M3;
   if (a.src_f32 && fp8)
-    kv_append_kernel<true, true><<<grid, block, 0, stream>>>(a);
+    kv_append_kernel<true, true, NORM><<<grid, block, 0, stream>>>(a);
   else if (a.src_f32)
-    kv_append_kernel<true, false><<<grid, block, 0, stream>>>(a);
+    kv_append_kernel<true, false, NORM><<<grid, block, 0, stream>>>(a);
   else if (fp8)
-    kv_append_kernel<false, true><<<grid, block, 0, stream>>>(a);
+    kv_append_kernel<false, true, NORM><<<grid, block, 0, stream>>>(a);
   else
-    kv_append_kernel<false, false><<<grid, block, 0, stream>>>(a);
+    kv_append_kernel<false, false, NORM><<<grid, block, 0, stream>>>(a);
   return hipGetLastError();
+}
+
+hipError_t launch_kv_append(const AppendArgs& a, hipStream_t stream) {
+  return a.q_norm || a.k_norm ? launch_norm<true>(a, stream) : launch_norm<false>(a, stream);
 }
 
 }  // namespace nvfp4

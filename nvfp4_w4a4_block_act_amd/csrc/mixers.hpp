@@ -21,6 +21,9 @@ struct AppendArgs {
   uint16_t* q_out;
   nvfp4_kv_cache cache;
   int q_heads, rot, interleaved, src_f32;
+  const float* q_norm = nullptr;  // weights of the heads' norms; null: no norm
+  const float* k_norm = nullptr;
+  float eps = 0;
 };
 hipError_t launch_kv_append(const AppendArgs& a, hipStream_t stream);
 
