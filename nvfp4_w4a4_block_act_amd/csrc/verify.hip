@@ -15,8 +15,8 @@
 // lane of a wave a node), and draws the last token: a running sum over the last node's
 // chunks, then over the 8192 logits of one chunk, which is all that is read again.
 // With draft logits (chains) the weights after a rejection are max(p - q, 0), which no
-// chunk sum of p and q gives: verify_rest sums them chunk by chunk, after a walk of its own
-// in each workgroup, and verify_draw takes these sums.
+// chunk sum of p and q gives: several workgroups of a sequence walk for themselves and sum them, and
+// the one that finishes last (a count that verify_rows clears) draws from these sums.
 //
 // Every sum has a fixed order: results do not depend on timing.
 #include <algorithm>
@@ -37,36 +37,61 @@ struct Part {
   double sum;  // of 2^((l - m) heat)
 };
 
-// Numbers of a launch: parts of target rows, parts of draft rows, sums of the rest.
+// Numbers of a launch: parts of target rows, parts of draft rows, sums of the rest and how many
+// of a sequence's workgroups have theirs.
 struct Sizes {
-  int chunks;
+  int chunks, groups;
   Part* p;
   Part* q;
   double* rest;
+  uint32_t* done;
 };
 static int64_t chunks_of(int64_t vocab) { return (vocab + kChunk - 1) / kChunk; }
 
-// 2^t, t <= 0 (NaN counts as 2^-1080: 0)
-__device__ __forceinline__ double exp2_below(double t) {
-  t = fmax(t, -1080.0);
-  const double n = rint(t), x = (t - n) * 0.69314718055994530942;
-  double p = 1.0 / 39916800.0;
-  p = fma(p, x, 1.0 / 3628800.0);
-  p = fma(p, x, 1.0 / 362880.0);
-  p = fma(p, x, 1.0 / 40320.0);
-  p = fma(p, x, 1.0 / 5040.0);
-  p = fma(p, x, 1.0 / 720.0);
-  p = fma(p, x, 1.0 / 120.0);
-  p = fma(p, x, 1.0 / 24.0);
-  p = fma(p, x, 1.0 / 6.0);
-  p = fma(p, x, 0.5);
-  p = fma(p, x, 1.0);
-  p = fma(p, x, 1.0);
-  return ldexp(p, (int)n);
+// 2^(i / kSteps), from the series of the exponential at compile time.
+constexpr int kSteps = 256;
+struct Powers {
+  double at[kSteps];
+};
+constexpr Powers powers() {
+  Powers t{};
+  for (int i = 0; i < kSteps; ++i) {
+    const double x = i * (0.69314718055994530942 / kSteps);
+    double p = 1.0;
+    for (int k = 20; k > 0; --k) p = p * x / k + 1.0;
+    t.at[i] = p;
+  }
+  return t;
+}
+__device__ const Powers kPowers = powers();
+
+// Into LDS, by the whole workgroup; a barrier has to follow.
+__device__ __forceinline__ void copy_powers(double* table) {
+  for (int i = threadIdx.x; i < kSteps; i += blockDim.x) table[i] = kPowers.at[i];
 }
 
-__device__ __forceinline__ double weight(float l, float m, double heat) {
-  return exp2_below(((double)l - (double)m) * heat);
+// 2^t for t <= 0, as 2^-1000 below that (and for NaN): t = n + i / kSteps + f, its whole steps from
+// the low bits of a sum that leaves no bits behind them.
+__device__ __forceinline__ double exp2_below(double t, const double* table) {
+  constexpr double kShift = 0x1.8p52 / kSteps, kLn2 = 0.69314718055994530942;
+  t = fmax(t, -1000.0);
+  const double up = t + kShift;
+  const int whole = __double2loint(up);
+  const double f = t - (up - kShift);
+  const double p = fma(fma(kLn2 * kLn2 * kLn2 / 6, f, kLn2 * kLn2 / 2), f, kLn2);
+  const double base = table[whole & (kSteps - 1)];
+  const double r = fma(p * f, base, base);
+  return __hiloint2double(__double2hiint(r) + (whole & ~(kSteps - 1)) * ((1 << 20) / kSteps), __double2loint(r));
+}
+
+// The weight of logit l where the largest is m: 2^(l heat - m heat).
+struct Scale {
+  double heat, shift;
+  const double* table;
+  __device__ __forceinline__ double of(float l) const { return exp2_below(fma((double)l, heat, shift), table); }
+};
+__device__ __forceinline__ Scale scale_of(double heat, float m, const double* table) {
+  return {heat, -(double)m * heat, table};
 }
 
 // log2(e) / temperature; 0: greedy
@@ -91,6 +116,15 @@ __device__ __forceinline__ int64_t lane_token(const VerifyArgs& a, int b, int la
   return t >= 0 && t < a.vocab ? t : -1;
 }
 
+// Four logits of a row of `count` from `at` on, -inf behind its end.
+__device__ __forceinline__ row4_t load4(const float* from, int at, int count) {
+  if (at + 4 <= count) return *reinterpret_cast<const row4_t*>(from + at);
+  row4_t w;
+#pragma unroll
+  for (int j = 0; j < 4; ++j) w[j] = at + j < count ? from[at + j] : -INFINITY;
+  return w;
+}
+
 // Sum over the workgroup's threads, in all of them.
 __device__ __forceinline__ double block_sum(double x, double* lds) {
 #pragma unroll
@@ -109,47 +143,52 @@ __global__ __launch_bounds__(kThreads) void verify_rows_kernel(VerifyArgs a, Siz
   row -= is_draft ? rows : 0;
   const int b = row / a.nodes, node = row % a.nodes;
   const int lane = threadIdx.x % 64;
-  const int parent = lane_parent(a, b, lane);
-  const int64_t token = lane_token(a, b, lane, parent);
-  uint64_t kids = __ballot(parent == node && token >= 0);
-  const bool is_greedy = greedy(a, b);
-  if (__shfl(parent, node) == -2) return;
-  if (is_draft && (is_greedy || kids == 0)) return;
-
   const int64_t first = (int64_t)chunk * kChunk;
   const float* from = (is_draft ? a.draft + row * a.ldd : a.logits + row * a.ld) + first;
   const int count = (int)min((int64_t)kChunk, a.vocab - first);
   float x[kEach];
+  auto load = [&] {
 #pragma unroll
-  for (int k = 0; k < kEach / 4; ++k) {
-    const int at = (k * kThreads + threadIdx.x) * 4;
-    if (at + 4 <= count) {
-      const row4_t w = *reinterpret_cast<const row4_t*>(from + at);
+    for (int k = 0; k < kEach / 4; ++k) {
+      const row4_t w = load4(from, (k * kThreads + threadIdx.x) * 4, count);
 #pragma unroll
       for (int j = 0; j < 4; ++j) x[4 * k + j] = w[j];
-    } else {
-#pragma unroll
-      for (int j = 0; j < 4; ++j) x[4 * k + j] = at + j < count ? from[at + j] : -INFINITY;
     }
+  };
+  // Where the launch does not fill the GPU the logits are on their way before it is known
+  // whether anybody asks for them.
+  const bool early = gridDim.x <= kCUs;
+  if (early) load();
+  if (a.draft && chunk == 0 && node == 0 && !is_draft && threadIdx.x == 0) z.done[b] = 0;
+  const int parent = lane_parent(a, b, lane);
+  const int64_t token = lane_token(a, b, lane, parent);
+  uint64_t kids = __ballot(parent == node && token >= 0);
+  const bool is_greedy = greedy(a, b);
+  if (!early) {
+    if (__shfl(parent, node) == -2 || (is_draft && (is_greedy || kids == 0))) return;
+    load();
   }
   float m = -INFINITY;
-  int at = -1;
 #pragma unroll
-  for (int e = 0; e < kEach; ++e)
-    if (x[e] > m) m = x[e], at = (e / 4 * kThreads + threadIdx.x) * 4 + e % 4;
+  for (int e = 0; e < kEach; ++e) m = fmaxf(m, x[e]);
+  const float mine = m;
   __shared__ float ms[kThreads / 64];
-  __shared__ int ats[kThreads / 64];
+  __shared__ int found;  // where the largest is
+  __shared__ double table[kSteps];
+  copy_powers(table);
 #pragma unroll
-  for (int s = 1; s < 64; s *= 2) {
-    const float om = __shfl_xor(m, s);
-    const int oat = __shfl_xor(at, s);
-    if (om > m || (om == m && (uint32_t)oat < (uint32_t)at)) m = om, at = oat;
-  }
-  if (lane == 0) ms[threadIdx.x / 64] = m, ats[threadIdx.x / 64] = at;
+  for (int s = 1; s < 64; s *= 2) m = fmaxf(m, __shfl_xor(m, s));
+  if (lane == 0) ms[threadIdx.x / 64] = m;
+  if (threadIdx.x == 0) found = 0x7FFFFFFF;
   __syncthreads();
+  m = fmaxf(fmaxf(ms[0], ms[1]), fmaxf(ms[2], ms[3]));
+  if (mine == m && m > -INFINITY) {
+    int at = 0x7FFFFFFF;
 #pragma unroll
-  for (int w = 0; w < kThreads / 64; ++w)
-    if (ms[w] > m || (ms[w] == m && (uint32_t)ats[w] < (uint32_t)at)) m = ms[w], at = ats[w];
+    for (int e = kEach - 1; e >= 0; --e)
+      if (x[e] == m) at = (e / 4 * kThreads + threadIdx.x) * 4 + e % 4;
+    atomicMin(&found, at);
+  }
 
   double sum = 0;
   if (!is_greedy) {
@@ -163,85 +202,120 @@ __global__ __launch_bounds__(kThreads) void verify_rows_kernel(VerifyArgs a, Siz
           if (e == mine) x[e] = -INFINITY;
       }
     }
-    const double heat = heat_of(a, b);
+    const Scale scale = scale_of(heat_of(a, b), m > -INFINITY ? m : 0.0f, table);
 #pragma unroll
-    for (int e = 0; e < kEach; ++e) sum += weight(x[e], m, heat);
+    for (int e = 0; e < kEach; ++e) sum += scale.of(x[e]);
     __shared__ double sums[kThreads / 64];
     sum = block_sum(sum, sums);
+  } else {
+    __syncthreads();
   }
   if (threadIdx.x == 0) {
-    const Part part = {m, at < 0 ? -1 : (int32_t)(at + first), sum};
+    const Part part = {m, m > -INFINITY ? (int32_t)(found + first) : -1, sum};
     (is_draft ? z.q : z.p)[(int64_t)row * z.chunks + chunk] = part;
   }
 }
 
+// The draw's kernel takes one chunk with many threads, so that each has only a few of its logits: its code
+// is run through once, by few workgroups, and fetching it sets their time (39 KB of code, with 256 threads,
+// took 13 and 21 us for one and 64 sequences, 10 KB 9 and 14).
+template <bool DRAWN>
+struct Draw {
+  static constexpr int kThreads = 1024, kEach = kChunk / kThreads, kWaves = kThreads / 64, kRuns = kEach / 4;
+  static constexpr int kSub = kThreads / NVFP4_MAX_NODES;  // threads that join a node's chunks
+};
+
 // What a walk ends with, in LDS.
 struct Walk {
+  double table[kSteps];
   float m[2][NVFP4_MAX_NODES];     // largest logit of each node's row; [1]: of its draft row
   double sum[2][NVFP4_MAX_NODES];  // of the row's weights, as verify_rows left them
   int at[NVFP4_MAX_NODES];         // where the largest logit is
-  int64_t tried[NVFP4_MAX_NODES];  // tokens of the last node's children
+  int tried[NVFP4_MAX_NODES];      // tokens of the last node's children
   int tries, node, count;          // count 0: a padded sequence
 };
 
-// The walk of sequence b by a workgroup; `store`: writes the outputs it decides.
+// The walk of sequence b by a workgroup; `store`: writes the outputs it decides.  Every number
+// a step may need is on its way before the first: each lane has its own node's, as a child.
+template <bool DRAWN>
 __device__ __forceinline__ void walk_tree(const VerifyArgs& a, const Sizes& z, int b, bool store, Walk& w) {
-  // four threads a node: its row's chunks
-  const int row = threadIdx.x / 4, sub = threadIdx.x % 4;
+  constexpr int kSub = Draw<DRAWN>::kSub;
+  const int lane = threadIdx.x % 64, row = threadIdx.x / kSub, sub = threadIdx.x % kSub;
+  const Part none = {-INFINITY, -1, 0.0};
+  const int64_t at_parts = ((int64_t)b * a.nodes + row) * z.chunks;
+  // the first chunk of each thread (a row that nobody asked for holds anything)
+  const bool one = row < a.nodes && sub < z.chunks;
+  Part ahead[2] = {one ? z.p[at_parts + sub] : none, none};
+  if (DRAWN && one) ahead[1] = z.q[at_parts + sub];
+  const float number = a.temperature && lane < a.nodes ? a.uniforms[(int64_t)b * (a.nodes + 1) + lane] : 0.0f;
+  const int parent = lane_parent(a, b, lane);
+  const int token = (int)lane_token(a, b, lane, parent);
   const bool is_greedy = greedy(a, b);
   const double heat = heat_of(a, b);
-  const int lane = threadIdx.x % 64;
-  const int parent = lane_parent(a, b, lane);
-  const int64_t token = lane_token(a, b, lane, parent);
-  uint64_t inner = 0;  // nodes that have children
-  for (int i = 0; i < a.nodes; ++i) inner |= __ballot(parent == i && token >= 0) ? 1ull << i : 0;
-  const uint64_t nodes = __ballot(parent != -2);
-#pragma unroll
-  for (int d = 0; d < 2; ++d) {
-    if (d == 1 && (!a.draft || is_greedy)) break;
-    const Part* parts = (d ? z.q : z.p) + ((int64_t)b * a.nodes + row) * z.chunks;
-    const bool here = row < a.nodes && ((d ? inner & nodes : nodes) >> row & 1);
-    float m = -INFINITY;
-    int at = -1;
-    if (here) {
-      for (int c = sub; c < z.chunks; c += 4)
+  float l[2] = {-INFINITY, -INFINITY};
+  if (!is_greedy && token >= 0) {
+    const int64_t up = (int64_t)b * a.nodes + parent;
+    l[0] = a.logits[up * a.ld + token];
+    if (DRAWN) l[1] = a.draft[up * a.ldd + token];
+  }
+  copy_powers(w.table);
+  uint64_t asked = __ballot(parent != -2);
+  if (threadIdx.x < NVFP4_MAX_NODES) w.m[0][lane] = w.m[1][lane] = -INFINITY, w.sum[0][lane] = w.sum[1][lane] = 0.0;
+  __syncthreads();
+#pragma unroll 1
+  for (int d = 0; d < (DRAWN ? 2 : 1); ++d) {
+    if (d == 1) {
+      uint64_t inner = 0;  // of draft rows only those of nodes that have children
+#pragma unroll 1
+      for (int i = 0; i < a.nodes; ++i) inner |= __ballot(parent == i && token >= 0) ? 1ull << i : 0;
+      asked &= inner;
+    }
+    if (row < a.nodes && (asked >> row & 1)) {
+      const Part* parts = (d ? z.q : z.p) + at_parts;
+      const Part first = d ? ahead[1] : ahead[0];
+      float m = first.m;
+      int at = first.at;
+#pragma unroll 1
+      for (int c = sub + kSub; c < z.chunks; c += kSub)
         if (parts[c].m > m) m = parts[c].m, at = parts[c].at;
-    }
 #pragma unroll
-    for (int s = 1; s < 4; s *= 2) {
-      const float om = __shfl_xor(m, s);
-      const int oat = __shfl_xor(at, s);
-      if (om > m || (om == m && (uint32_t)oat < (uint32_t)at)) m = om, at = oat;
-    }
-    double sum = 0;
-    if (here && !is_greedy)
-      for (int c = sub; c < z.chunks; c += 4)
-        if (parts[c].m > -INFINITY) sum += parts[c].sum * weight(parts[c].m, m, heat);
-    sum += __shfl_xor(sum, 1);
-    sum += __shfl_xor(sum, 2);
-    if (sub == 0) {
-      w.m[d][row] = m, w.sum[d][row] = sum;
-      if (d == 0) w.at[row] = at;
+      for (int s = 1; s < kSub; s *= 2) {
+        const float om = __shfl_xor(m, s);
+        const int oat = __shfl_xor(at, s);
+        if (om > m || (om == m && (uint32_t)oat < (uint32_t)at)) m = om, at = oat;
+      }
+      double sum = 0;
+      if (m > -INFINITY && !is_greedy) {
+        const Scale under = scale_of(heat, m, w.table);
+        Part p = first;
+#pragma unroll 1
+        for (int c = sub;;) {
+          if (p.m > -INFINITY) sum += p.sum * under.of(p.m);
+          c += kSub;
+          if (c >= z.chunks) break;
+          p = parts[c];
+        }
+      }
+#pragma unroll
+      for (int s = 1; s < kSub; s *= 2) sum += __shfl_xor(sum, s);
+      if (sub == 0) {
+        w.m[d][row] = m, w.sum[d][row] = sum;
+        if (d == 0) w.at[row] = at;
+      }
     }
   }
   __syncthreads();
   if (threadIdx.x < 64) {
     // the lane's node, as a child: its weights under its parent
-    double p = 0, q = 0;
-    if (token >= 0 && !is_greedy) {
-      const int64_t up = (int64_t)b * a.nodes + parent;
-      const float l = a.logits[up * a.ld + token];
-      p = l > -INFINITY ? weight(l, w.m[0][parent], heat) : 0.0;
-      if (a.draft) {
-        const float l2 = a.draft[up * a.ldd + token];
-        q = l2 > -INFINITY ? weight(l2, w.m[1][parent], heat) : 0.0;
-      }
-    }
+    double mine[2] = {0, 0};
+#pragma unroll
+    for (int d = 0; d < (DRAWN ? 2 : 1); ++d)
+      if (l[d] > -INFINITY) mine[d] = scale_of(heat, w.m[d][parent], w.table).of(l[d]);
     bool again = false;  // an earlier child of the same parent has the same token
-    if (!a.draft)
+    if (!DRAWN)
+#pragma unroll 4
       for (int i = 1; i < a.nodes; ++i) {
-        const int64_t t = __shfl(token, i);
-        const int up = __shfl(parent, i);
+        const int t = __builtin_amdgcn_readlane(token, i), up = __builtin_amdgcn_readlane(parent, i);
         again |= i < lane && t >= 0 && up == parent && t == token;
       }
     int node = 0, count = __shfl(parent, 0) == -1 ? 1 : 0;
@@ -253,25 +327,25 @@ __device__ __forceinline__ void walk_tree(const VerifyArgs& a, const Sizes& z, i
         const uint64_t best = __ballot(parent == node && token >= 0 && token == w.at[node]);
         if (best) taken = __builtin_ctzll(best);
       } else if (kids) {
-        const double u = fmin(fmax((double)a.uniforms[(int64_t)b * (a.nodes + 1) + node], 0.0), 1.0 - 0x1p-24);
-        if (a.draft) {
+        const double u = fmin(fmax((double)__shfl(number, node), 0.0), 1.0 - 0x1p-24);
+        if (DRAWN) {
           const int kid = __builtin_ctzll(kids);
-          const double pk = __shfl(p, kid) * w.sum[1][node], qk = __shfl(q, kid) * w.sum[0][node];
+          const double pk = __shfl(mine[0], kid) * w.sum[1][node], qk = __shfl(mine[1], kid) * w.sum[0][node];
           if (u * qk < pk) taken = kid;
           kids = 1ull << kid;
         } else {
           double total = w.sum[0][node], mass = 0;
-          for (uint64_t k = kids; k; k &= k - 1) total += __shfl(p, __builtin_ctzll(k));
+          for (uint64_t k = kids; k; k &= k - 1) total += __shfl(mine[0], __builtin_ctzll(k));
           for (uint64_t k = kids; k && taken < 0; k &= k - 1) {
             const int kid = __builtin_ctzll(k);
-            mass += __shfl(p, kid);
+            mass += __shfl(mine[0], kid);
             if (u * total < mass) taken = kid;
           }
         }
       }
       if (taken < 0) break;
       node = taken;
-      const int64_t t = __shfl(token, taken);
+      const int t = __shfl(token, taken);
       if (store && lane == 0) {
         a.tokens[(int64_t)b * a.nodes + count - 1] = t;
         a.path[(int64_t)b * a.nodes + count] = taken;
@@ -290,153 +364,205 @@ __device__ __forceinline__ void walk_tree(const VerifyArgs& a, const Sizes& z, i
   __syncthreads();
 }
 
-// The weight of token t (a column of the vocabulary) after the last node.
+// The weights after the last node: of p, or max(p - q, 0).
 struct Last {
   const float* l;
   const float* l2;  // null: no residual
-  float m, m2;
-  double heat, sum, sum2;
-  __device__ __forceinline__ double of(int64_t t) const {
-    const float x = l[t];
-    const double p = x > -INFINITY ? weight(x, m, heat) : 0.0;
-    if (!l2) return p;
-    const float y = l2[t];
-    return fmax(p / sum - (y > -INFINITY ? weight(y, m2, heat) / sum2 : 0.0), 0.0);
-  }
+  Scale p, q;
+  double per, per2;  // 1 / sums
 };
+template <bool DRAWN>
 __device__ __forceinline__ Last last_of(const VerifyArgs& a, const Walk& w, int b) {
   const int64_t row = (int64_t)b * a.nodes + w.node;
-  const bool rest = a.draft && w.tries > 0;
-  return {a.logits + row * a.ld, rest ? a.draft + row * a.ldd : nullptr, w.m[0][w.node], rest ? w.m[1][w.node] : 0.0f,
-          heat_of(a, b), w.sum[0][w.node], rest ? w.sum[1][w.node] : 0.0};
+  const bool rest = DRAWN && w.tries > 0;
+  const double heat = heat_of(a, b);
+  return {a.logits + row * a.ld,
+          rest ? a.draft + row * a.ldd : nullptr,
+          scale_of(heat, w.m[0][w.node], w.table),
+          scale_of(heat, rest ? w.m[1][w.node] : 0.0f, w.table),
+          rest ? 1.0 / w.sum[0][w.node] : 1.0,
+          rest && w.sum[1][w.node] > 0.0 ? 1.0 / w.sum[1][w.node] : 0.0};
 }
 
-// Sums of max(p - q, 0) by chunk.
-__global__ __launch_bounds__(kThreads) void verify_rest_kernel(VerifyArgs a, Sizes z) {
-  const int b = blockIdx.x / z.chunks, chunk = blockIdx.x % z.chunks;
-  __shared__ Walk w;
-  __shared__ double sums[kThreads / 64];
-  if (greedy(a, b)) return;
-  walk_tree(a, z, b, false, w);
-  if (w.count == 0 || w.tries == 0) return;
-  const Last last = last_of(a, w, b);
-  const int64_t first = (int64_t)chunk * kChunk;
-  const int count = (int)min((int64_t)kChunk, a.vocab - first);
-  double sum = 0;
-#pragma unroll 4
-  for (int k = 0; k < kEach; ++k) {
-    const int at = k * kThreads + threadIdx.x;
-    if (at < count) sum += last.of(first + at);
-  }
-  sum = block_sum(sum, sums);
-  if (threadIdx.x == 0) z.rest[(int64_t)b * z.chunks + chunk] = sum;
-}
-
-// First place whose running sum of the threads' values is above u times their total (or `target`
-// if that is not negative): the thread, and what is left of the target at its start.
-struct Found {
-  int thread;  // -1: all are 0
-  double left;
+// Weights of the chunk that begins at column `first`, this thread's runs of four.
+template <bool DRAWN>
+struct Weights {
+  double w[Draw<DRAWN>::kEach];
 };
-__device__ __forceinline__ Found find_thread(double x, double u, double target, double (&scan)[kThreads]) {
-  __syncthreads();
-  scan[threadIdx.x] = x;
-  __syncthreads();
-  for (int s = 1; s < kThreads; s *= 2) {
-    const double y = threadIdx.x >= s ? scan[threadIdx.x - s] : 0.0;
-    __syncthreads();
-    scan[threadIdx.x] += y;
-    __syncthreads();
+template <bool DRAWN>
+__device__ __forceinline__ void weights_of(const VerifyArgs& a, const Last& last, int64_t first, Weights<DRAWN>& r) {
+  const int count = (int)min((int64_t)kChunk, a.vocab - first);
+  row4_t x[Draw<DRAWN>::kRuns], y[Draw<DRAWN>::kRuns];
+#pragma unroll
+  for (int k = 0; k < Draw<DRAWN>::kRuns; ++k) {
+    x[k] = load4(last.l + first, (k * Draw<DRAWN>::kThreads + threadIdx.x) * 4, count);
+    y[k] = DRAWN && last.l2 ? load4(last.l2 + first, (k * Draw<DRAWN>::kThreads + threadIdx.x) * 4, count) : x[k];
   }
-  if (target < 0) target = u * scan[kThreads - 1];
-  __shared__ Found found;
-  __shared__ int last;
-  if (threadIdx.x == 0) found = {-1, 0.0}, last = -1;
-  __syncthreads();
-  const double before = threadIdx.x ? scan[threadIdx.x - 1] : 0.0;
-  if (x > 0.0) atomicMax(&last, (int)threadIdx.x);
-  if (before <= target && scan[threadIdx.x] > target) found = {(int)threadIdx.x, target - before};
-  __syncthreads();
-  Found f = found;
-  if (f.thread < 0 && last >= 0) f = {last, __builtin_inf()};  // rounding: the last one with a weight
-  return f;
+#pragma unroll
+  for (int e = 0; e < Draw<DRAWN>::kEach; ++e) {
+    const float l = x[e / 4][e % 4];
+    r.w[e] = l > -INFINITY ? last.p.of(l) : 0.0;
+  }
+  if (DRAWN && last.l2) {
+#pragma unroll
+    for (int e = 0; e < Draw<DRAWN>::kEach; ++e) {
+      const float l = y[e / 4][e % 4];
+      r.w[e] = fmax(r.w[e] * last.per - (l > -INFINITY ? last.q.of(l) * last.per2 : 0.0), 0.0);
+    }
+  }
 }
 
-__global__ __launch_bounds__(kThreads) void verify_draw_kernel(VerifyArgs a, Sizes z) {
-  const int b = blockIdx.x;
+// The sum over the lanes before this one.
+__device__ __forceinline__ double sum_before(double x, int lane) {
+  double run = x;
+#pragma unroll
+  for (int s = 1; s < 64; s *= 2) {
+    const double y = __shfl_up(run, s);
+    if (lane >= s) run += y;
+  }
+  return run - x;
+}
+
+// One workgroup a sequence, or with draft logits several, which share its chunks.
+template <bool DRAWN>
+__global__ __launch_bounds__(Draw<DRAWN>::kThreads) void verify_draw_kernel(VerifyArgs a, Sizes z) {
+  const int b = DRAWN ? blockIdx.x / z.groups : blockIdx.x, own = DRAWN ? blockIdx.x % z.groups : 0;
+  const int lane = threadIdx.x % 64, wave = threadIdx.x / 64;
   __shared__ Walk w;
-  __shared__ double scan[kThreads];
-  __shared__ int chosen;
-  __shared__ double rest;
-  walk_tree(a, z, b, true, w);
-  if (w.count == 0) return;
+  __shared__ double sums[Draw<DRAWN>::kRuns][Draw<DRAWN>::kWaves];
+  __shared__ bool is_last;
+  if (DRAWN && own > 0 && greedy(a, b)) return;
+  walk_tree<DRAWN>(a, z, b, own == 0, w);
+  if (w.count == 0 || (DRAWN && own > 0 && w.tries == 0)) return;
   int64_t* out = a.tokens + (int64_t)b * a.nodes + w.count - 1;
   if (greedy(a, b)) {
     if (threadIdx.x == 0) *out = w.at[w.node];
     return;
   }
-  const Last last = last_of(a, w, b);
+  const Last last = last_of<DRAWN>(a, w, b);
   const Part* parts = z.p + ((int64_t)b * a.nodes + w.node) * z.chunks;
   const double* rests = z.rest + (int64_t)b * z.chunks;
   const double u = fmin(fmax((double)a.uniforms[(int64_t)b * (a.nodes + 1) + a.nodes], 0.0), 1.0 - 0x1p-24);
-  auto chunk_sum = [&](int c) {
-    return last.l2 ? rests[c] : (parts[c].m > -INFINITY ? parts[c].sum * weight(parts[c].m, last.m, last.heat) : 0.0);
+  Weights<DRAWN> r;
+  double four[Draw<DRAWN>::kRuns];
+  auto add_up = [&] {  // the sums of the runs, of each wave
+#pragma unroll
+    for (int k = 0; k < Draw<DRAWN>::kRuns; ++k) {
+      double s = four[k] = (r.w[4 * k] + r.w[4 * k + 1]) + (r.w[4 * k + 2] + r.w[4 * k + 3]);
+#pragma unroll
+      for (int m = 1; m < 64; m *= 2) s += __shfl_xor(s, m);
+      if (lane == 0) sums[k][wave] = s;
+    }
+    __syncthreads();
   };
-  // the chunk: a run of chunks to each thread
-  const int each = (z.chunks + kThreads - 1) / kThreads, c0 = threadIdx.x * each, c1 = min(c0 + each, z.chunks);
-  double sum = 0;
-  for (int c = c0; c < c1; ++c) sum += chunk_sum(c);
-  Found f = find_thread(sum, u, -1.0, scan);
-  if (f.thread < 0) {  // no weight anywhere: the largest logit
+  int chunk = own;
+  double left = 0;
+  // With draft logits and a rejection the workgroup's turns sum its own chunks, and the workgroup that finishes
+  // last takes one more, in which it draws; otherwise there is only that one.
+  bool draw = !(DRAWN && last.l2);
+#pragma unroll 1
+  for (;;) {
+    if (draw) {
+      // The chunk, found by every wave alike: a run of chunks to each lane.
+      const int each = (z.chunks + 63) / 64, c0 = lane * each, c1 = min(c0 + each, z.chunks);
+      auto chunk_sum = [&](int c) {
+        return DRAWN && last.l2 ? __hip_atomic_load(&rests[c], __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT) : (parts[c].m > -INFINITY ? parts[c].sum * last.p.of(parts[c].m) : 0.0);
+      };
+      double sum = 0;
+#pragma unroll 1
+      for (int c = c0; c < c1; ++c) sum += chunk_sum(c);
+      const double before = sum_before(sum, lane), target = u * __shfl(before + sum, 63);
+      const uint64_t some = __ballot(sum > 0.0), above = __ballot(sum > 0.0 && before + sum > target);
+      if (some == 0) {  // no weight anywhere: the largest logit
+        if (threadIdx.x == 0) *out = w.at[w.node];
+        return;
+      }
+      // (none above only by rounding: then the last one with a weight)
+      const int owner = above ? __builtin_ctzll(above) : 63 - __builtin_clzll(some);
+      chunk = c0, left = target - before;
+#pragma unroll 1
+      for (int c = c0; c < c1 && each > 1; ++c) {
+        const double s = chunk_sum(c);
+        if (s <= 0.0) continue;
+        chunk = c;
+        if (s > left) break;
+        if (c + 1 < c1) left -= s;
+      }
+      chunk = __shfl(chunk, owner);
+      left = __shfl(left, owner);
+    }
+    const int64_t first = (int64_t)chunk * kChunk;
+    weights_of<DRAWN>(a, last, first, r);
+    if (!DRAWN) {
+#pragma unroll 1
+      for (int i = 0; i < w.tries; ++i) {
+        const int64_t t = w.tried[i] - first;
+        if (t < 0 || t >= kChunk || (t / 4) % Draw<DRAWN>::kThreads != threadIdx.x) continue;
+        const int mine = (int)(t / 4 / Draw<DRAWN>::kThreads * 4 + t % 4);
+#pragma unroll
+        for (int e = 0; e < Draw<DRAWN>::kEach; ++e)
+          if (e == mine) r.w[e] = 0.0;
+      }
+    }
+    add_up();
+    if (draw) break;
+    chunk += z.groups;
+    const bool more = chunk < z.chunks;
+    if (threadIdx.x == 0) {
+      double sum = 0;
+      for (int i = 0; i < Draw<DRAWN>::kRuns * Draw<DRAWN>::kWaves; ++i) sum += sums[i / Draw<DRAWN>::kWaves][i % Draw<DRAWN>::kWaves];
+      // The sums pass between workgroups as atomic values, which the cache of an XCD does not hold back, and the
+      // wait puts each before its count.  (Fences, which write back and drop whole caches, took 11 us of 39.)
+      __hip_atomic_store(&z.rest[(int64_t)b * z.chunks + chunk - z.groups], sum, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+      asm volatile("s_waitcnt vmcnt(0)" ::: "memory");
+      if (!more)
+        is_last = __hip_atomic_fetch_add(&z.done[b], 1u, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT) + 1 == (uint32_t)z.groups;
+      asm volatile("s_waitcnt vmcnt(0)" ::: "memory");
+    }
+    __syncthreads();
+    if (more) continue;
+    if (!is_last) return;
+    draw = true;
+  }
+
+  // The token in the chunk: runs of 4096 logits, a wave's part of a run, lanes, fours.  Every wave finds the
+  // part alike, a lane to each.
+  static_assert(Draw<DRAWN>::kRuns * Draw<DRAWN>::kWaves <= 64, "a lane to each part");
+  const double part_sum = lane < Draw<DRAWN>::kRuns * Draw<DRAWN>::kWaves ? sums[lane / Draw<DRAWN>::kWaves][lane % Draw<DRAWN>::kWaves] : 0.0;
+  const double part_before = sum_before(part_sum, lane);
+  const uint64_t filled = __ballot(part_sum > 0.0), past = __ballot(part_sum > 0.0 && part_before + part_sum > left);
+  if (filled == 0) {
     if (threadIdx.x == 0) *out = w.at[w.node];
     return;
   }
-  if ((int)threadIdx.x == f.thread) {
-    int best = c0;
-    double left = f.left;
-    for (int c = c0; c < c1; ++c) {
-      const double s = chunk_sum(c);
-      if (s <= 0.0) continue;
-      best = c;
-      if (s > left) break;
-      left -= s;
+  const int part = past ? __builtin_ctzll(past) : 63 - __builtin_clzll(filled);
+  const double in = left - __shfl(part_before, part);
+  if (wave != part % Draw<DRAWN>::kWaves) return;
+  double mine[4] = {0, 0, 0, 0}, total = 0;
+#pragma unroll
+  for (int k = 0; k < Draw<DRAWN>::kRuns; ++k)
+    if (k == part / Draw<DRAWN>::kWaves) {
+      total = four[k];
+#pragma unroll
+      for (int j = 0; j < 4; ++j) mine[j] = r.w[4 * k + j];
     }
-    chosen = best, rest = left;
+  const double before = sum_before(total, lane);
+  const uint64_t any = __ballot(total > 0.0), over = __ballot(total > 0.0 && before + total > in);
+  if (lane != (over ? __builtin_ctzll(over) : 63 - __builtin_clzll(any))) return;
+  int best = 0;
+  double rest = in - before;
+  bool found = false;
+#pragma unroll
+  for (int j = 0; j < 4; ++j) {
+    if (!found && mine[j] > 0.0) best = j, found = mine[j] > rest;
+    rest -= mine[j];
   }
-  __syncthreads();
-  // the token in it: a run of 32 to each thread
-  const int64_t first = (int64_t)chosen * kChunk + threadIdx.x * kEach;
-  const int count = (int)max((int64_t)0, min((int64_t)kEach, a.vocab - first));
-  const int tries = last.l2 ? 0 : w.tries;
-  auto of = [&](int64_t t) {
-    for (int i = 0; i < tries; ++i)
-      if (w.tried[i] == t) return 0.0;
-    return last.of(t);
-  };
-  sum = 0;
-  for (int e = 0; e < count; ++e) sum += of(first + e);
-  f = find_thread(sum, 0.0, rest, scan);
-  if (f.thread < 0) {
-    if (threadIdx.x == 0) *out = w.at[w.node];
-    return;
-  }
-  if ((int)threadIdx.x == f.thread) {
-    int64_t best = first;
-    double left = f.left;
-    for (int e = 0; e < count; ++e) {
-      const double s = of(first + e);
-      if (s <= 0.0) continue;
-      best = first + e;
-      if (s > left) break;
-      left -= s;
-    }
-    *out = best;
-  }
+  *out = (int64_t)chunk * kChunk + ((part / Draw<DRAWN>::kWaves) * Draw<DRAWN>::kThreads + wave * 64 + lane) * 4 + best;
 }
 
 size_t verify_workspace(int64_t B, int nodes, int64_t vocab, bool sampled) {
-  const size_t chunks = (size_t)chunks_of(vocab), rows = (size_t)B * nodes;
-  return rows * chunks * sizeof(Part) * (sampled ? 2 : 1) + (sampled ? ((size_t)B * chunks * sizeof(double) + 15) / 16 * 16 : 0);
+  const size_t chunks = (size_t)chunks_of(vocab), rows = (size_t)B * nodes, parts = rows * chunks * sizeof(Part);
+  return sampled ? 2 * parts + ((size_t)B * (chunks * sizeof(double) + sizeof(uint32_t)) + 15) / 16 * 16 : parts;
 }
 
 int64_t verify_groups(int64_t B, int nodes, int64_t vocab, bool sampled) {
@@ -447,15 +573,17 @@ hipError_t launch_verify(const VerifyArgs& a, hipStream_t stream) {
   const int rows = a.B * a.nodes, chunks = (int)chunks_of(a.vocab);
   Part* p = static_cast<Part*>(a.workspace);
   Part* q = a.draft ? p + (int64_t)rows * chunks : nullptr;
-  const Sizes z = {chunks, p, q, a.draft ? reinterpret_cast<double*>(q + (int64_t)rows * chunks) : nullptr};
+  double* rest = a.draft ? reinterpret_cast<double*>(q + (int64_t)rows * chunks) : nullptr;
+  // as many workgroups for a sequence as the GPU runs at once, one on a CU
+  const int groups = std::min(chunks, std::max(1, kCUs / a.B));
+  const Sizes z = {chunks, groups, p, q, rest, a.draft ? reinterpret_cast<uint32_t*>(rest + (int64_t)a.B * chunks) : nullptr};
   verify_rows_kernel<<<dim3((unsigned)((int64_t)rows * (a.draft ? 2 : 1) * chunks)), kThreads, 0, stream>>>(a, z);
-  hipError_t e = hipGetLastError();
-  if (e == hipSuccess && a.draft) {
-    verify_rest_kernel<<<dim3((unsigned)((int64_t)a.B * chunks)), kThreads, 0, stream>>>(a, z);
-    e = hipGetLastError();
-  }
+  const hipError_t e = hipGetLastError();
   if (e != hipSuccess) return e;
-  verify_draw_kernel<<<dim3((unsigned)a.B), kThreads, 0, stream>>>(a, z);
+  if (a.draft)
+    verify_draw_kernel<true><<<dim3((unsigned)((int64_t)a.B * groups)), Draw<true>::kThreads, 0, stream>>>(a, z);
+  else
+    verify_draw_kernel<false><<<dim3((unsigned)a.B), Draw<false>::kThreads, 0, stream>>>(a, z);
   return hipGetLastError();
 }
 

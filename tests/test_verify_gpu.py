@@ -81,7 +81,7 @@ def test_picked_drafts(B, W, V, kind):
 
 
 @pytest.mark.parametrize("kind", ["tree", "chain"])
-@pytest.mark.parametrize("B,W,V", [(1, 1, 5), (6, 4, 8191), (3, 8, 24577), (9, 6, 999), (2, 5, 100003)])
+@pytest.mark.parametrize("B,W,V", [(1, 1, 5), (6, 4, 8191), (3, 8, 24577), (9, 6, 999), (2, 5, 100003), (150, 2, 24577)])
 def test_drawn_drafts(B, W, V, kind):
     say(f"[verify] drawn B={B} W={W} V={V} {kind}")
     c = _case(B, W, V, seed=B * W + V, kind=kind, sampled=True, greedy=B // 3)
