@@ -59,8 +59,11 @@ __device__ __forceinline__ void norm_head(float (&x)[8], float (&y)[8], const fl
 #pragma unroll
   for (int j = 0; j < 8; ++j) sum += x[j] * x[j] + y[j] * y[j];
   for (int m = 1; m < per; m *= 2) sum += __shfl_xor(sum, m);
-  const float mean = sum / (float)(per * 16) + eps;
-  const float by = mean > 0.0f ? 1.0f / sqrtf(mean) : 0.0f;
+  // (a power of two; the root's instruction is off by one unit in the last place, and takes no subnormals)
+  const float mean = sum * (1.0f / (float)(per * 16)) + eps;
+  const bool tiny = mean < 0x1p-100f;
+  const float root = __builtin_amdgcn_rsqf(tiny ? mean * 0x1p100f : mean) * (tiny ? 0x1p50f : 1.0f);
+  const float by = mean > 0.0f ? root : 0.0f;
   float w1[8], w2[8];
   load8<true>(w, o1, w1);
   load8<true>(w, o2, w2);
