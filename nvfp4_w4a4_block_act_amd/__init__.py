@@ -717,6 +717,7 @@ class PagedKVCache:
         s = k.stride()
         self.desc = KVCacheDesc(k.data_ptr(), v.data_ptr(), _ptr(k_amax), _ptr(v_amax), self.num_pages, s[0], s[1],
                                 s[2], self.page_size, self.kv_heads, self.head_dim, DTYPE[k.dtype])
+        self._desc_bytes = bytes(self.desc)
 
     # read-only: another tensor in their place would leave desc with the address of freed memory
     k = property(lambda self: self._tensors[0])
@@ -954,8 +955,9 @@ def verify_drafts(logits, drafts, parents=None, temperature=None, uniforms=None,
 def _layers(caches, dev):
     """The descriptors of one cache or of several layers' as an array."""
     caches = [caches] if isinstance(caches, PagedKVCache) else caches
-    assert all(c.device_index == dev for c in caches), "caches: another device's"
-    return (KVCacheDesc * len(caches))(*[c.desc for c in caches]), len(caches)
+    here = [c._desc_bytes for c in caches if c.device_index == dev]     # (arrays of structs are slow to fill one by one)
+    assert len(here) == len(caches), "caches: another device's"
+    return (KVCacheDesc * len(here)).from_buffer_copy(b"".join(here)), len(here)
 
 
 @_on_device
