@@ -7,7 +7,14 @@
 // whole tree of 64 nodes of the widest row (512 bytes), or several heads of smaller ones.
 // A workgroup whose sequence keeps every row where it is reads its path and ends.
 //
-// kv_copy_pages: pieces of 16 bytes, four in flight for each thread, 16 KB a workgroup.
+// Bound by its launch and two chains of loads: 3.7 us alone for a chain of 8 in 16 layers,
+// 5.3 us for 64 trees of 24 (4.3 MB).
+//
+// kv_copy_pages: a thread moves one piece of 16 bytes, 4 KB a workgroup, with loads past the
+// caches (the source is not read again soon; the copy will be).  Bound by HBM: 96 pages of
+// 16 layers (403 MB read and written) take 62 us, 6.4 TB/s, where a library's copy of 1 GiB
+// reaches 5.2.  With ordinary loads 74 us, with stores past the caches as well 68; four
+// pieces a thread take 78 and eight 110, workgroups of 1024 threads 72.
 #include <algorithm>
 
 #include "common.hpp"
@@ -84,7 +91,7 @@ hipError_t launch_kv_compact(const CompactArgs& a, const LayerCaches& caches, hi
   return hipGetLastError();
 }
 
-constexpr int kCopyThreads = 256, kCopyPieces = 4;
+constexpr int kCopyThreads = 256;
 
 // Runs of a page: rows that follow each other without a gap count as one.
 PageShape page_shape(const nvfp4_kv_cache& c) {
@@ -102,41 +109,25 @@ PageShape page_shape(const nvfp4_kv_cache& c) {
 
 static int64_t page_pieces(const PageShape& p) { return p.run / 16 * p.mid * p.outer; }
 
-int64_t copy_groups(const PageShape& p) {
-  return (page_pieces(p) + kCopyThreads * kCopyPieces - 1) / (kCopyThreads * kCopyPieces);
-}
+int64_t copy_groups(const PageShape& p) { return (page_pieces(p) + kCopyThreads - 1) / kCopyThreads; }
 
 template <bool WHOLE>
 __global__ __launch_bounds__(kCopyThreads) void kv_copy_pages_kernel(const int32_t* src, const int32_t* dst,
                                                                     LayerCaches caches, PageShape shape, int pieces, int groups) {
   const nvfp4_kv_cache& c = caches.shape;
-  const int part = blockIdx.x % groups, rest = blockIdx.x / groups;
+  const int rest = blockIdx.x / groups, p = blockIdx.x % groups * kCopyThreads + threadIdx.x;
   const int tensor = rest % (2 * caches.layers), i = rest / (2 * caches.layers);
   const int from = src[i], to = dst[i];
-  if (from < 0 || from >= c.num_pages || to < 0 || to >= c.num_pages || from == to) return;
+  if (from < 0 || from >= c.num_pages || to < 0 || to >= c.num_pages || from == to || p >= pieces) return;
   uint8_t* base = tensor % 2 ? caches.v[tensor / 2] : caches.k[tensor / 2];
   const int64_t page = c.page_stride * elem_size(c);
-  const uint8_t* f = base + from * page;
-  uint8_t* t = base + to * page;
-  u32x4_t held[kCopyPieces];
-  int64_t at[kCopyPieces];
-#pragma unroll
-  for (int s = 0; s < kCopyPieces; ++s) {
-    const int p = (part * kCopyPieces + s) * kCopyThreads + threadIdx.x;
-    at[s] = -1;
-    if (p < pieces) {
-      if (WHOLE) {
-        at[s] = (int64_t)p * 16;
-      } else {
-        const int run = (int)(shape.run / 16), row = p / run, mid = (int)shape.mid;
-        at[s] = row / mid * shape.outer_stride + row % mid * shape.mid_stride + p % run * 16;
-      }
-      held[s] = *reinterpret_cast<const u32x4_t*>(f + at[s]);
-    }
+  int64_t at = (int64_t)p * 16;
+  if (!WHOLE) {
+    const int run = (int)(shape.run / 16), row = p / run, mid = (int)shape.mid;
+    at = row / mid * shape.outer_stride + row % mid * shape.mid_stride + p % run * 16;
   }
-#pragma unroll
-  for (int s = 0; s < kCopyPieces; ++s)
-    if (at[s] >= 0) *reinterpret_cast<u32x4_t*>(t + at[s]) = held[s];
+  const u32x4_t held = __builtin_nontemporal_load(reinterpret_cast<const u32x4_t*>(base + from * page + at));
+  *reinterpret_cast<u32x4_t*>(base + to * page + at) = held;
 }
 
 hipError_t launch_kv_copy_pages(const int32_t* src, const int32_t* dst, int64_t n, const LayerCaches& caches,
