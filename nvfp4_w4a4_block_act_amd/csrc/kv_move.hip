@@ -10,11 +10,12 @@
 // Bound by its launch and two chains of loads: 3.7 us alone for a chain of 8 in 16 layers,
 // 5.3 us for 64 trees of 24 (4.3 MB).
 //
-// kv_copy_pages: a thread moves one piece of 16 bytes, 4 KB a workgroup, with loads past the
-// caches (the source is not read again soon; the copy will be).  Bound by HBM: 96 pages of
-// 16 layers (403 MB read and written) take 62 us, 6.4 TB/s, where a library's copy of 1 GiB
-// reaches 5.2.  With ordinary loads 74 us, with stores past the caches as well 68; four
-// pieces a thread take 78 and eight 110, workgroups of 1024 threads 72.
+// kv_copy_pages: a thread moves one piece of 16 bytes, 4 KB a workgroup, past the caches (the
+// pages are more than they hold, or are not read again soon).  Bound by HBM: 96 pages of 16
+// layers (403 MB read and written) take 69 us after other work and 68 back to back, 5.9 TB/s,
+// where a library's copy of 1 GiB reaches 5.2.  With ordinary loads and stores 75 and 74,
+// loads alone past the caches 76 and 62 (and more for 3 to 12 pages); four pieces a thread
+// 80 and 78, eight 106, workgroups of 1024 threads 74.
 #include <algorithm>
 
 #include "common.hpp"
@@ -127,7 +128,7 @@ __global__ __launch_bounds__(kCopyThreads) void kv_copy_pages_kernel(const int32
     at = row / mid * shape.outer_stride + row % mid * shape.mid_stride + p % run * 16;
   }
   const u32x4_t held = __builtin_nontemporal_load(reinterpret_cast<const u32x4_t*>(base + from * page + at));
-  *reinterpret_cast<u32x4_t*>(base + to * page + at) = held;
+  __builtin_nontemporal_store(held, reinterpret_cast<u32x4_t*>(base + to * page + at));
 }
 
 hipError_t launch_kv_copy_pages(const int32_t* src, const int32_t* dst, int64_t n, const LayerCaches& caches,
