@@ -28,10 +28,10 @@
  *    HIP runtime rejected a launch (hipGetLastError); a call that enqueues
  *    several kernels (the two-pass quantizer, nvfp4_linear outside its
  *    one-launch range, some GEMMs with a ragged last tile column, nvfp4_attn_decode
- *    over split sequences, nvfp4_gdn_prefill) may already have enqueued the kernels
- *    before the rejected one, and all of its outputs are then unspecified -- of
- *    nvfp4_gdn_prefill the states too, which it updates in place: restore them before
- *    calling again.  The library never prints and never aborts.
+ *    and nvfp4_attn_tree over split sequences, nvfp4_gdn_prefill, nvfp4_verify_drafts)
+ *    may already have enqueued the kernels before the rejected one, and all of its
+ *    outputs are then unspecified -- of nvfp4_gdn_prefill the states too, which it
+ *    updates in place: restore them before calling again.  The library never prints and never aborts.
  *  - Element codes are packed two per byte, the even k in the low nibble:
  *    byte j of a row = code[2j] | code[2j+1] << 4; code = sign << 3 | mag,
  *    mag 0..7 = 0, 0.5, 1, 1.5, 2, 3, 4, 6.  Scales are E4M3FN bytes
@@ -52,7 +52,8 @@ extern "C" {
 #endif
 
 /* 2: nvfp4_gemm_form may return 2 (the MFMA GEMM with 256 x 128 tiles). */
-/* 3: nvfp4_read_probe; later also the token mixers (nvfp4_kv_append to nvfp4_gdn_prefill),
+/* 3: nvfp4_read_probe; later also the token mixers (nvfp4_kv_append to nvfp4_gdn_prefill)
+ *    and the drafted tokens (nvfp4_kv_append_norm, nvfp4_attn_tree to nvfp4_kv_copy_pages),
  *    which a library of version 3 may still lack: look the symbol up. */
 #define NVFP4_ABI_VERSION 3
 #define NVFP4_MAX_SEGMENTS 16
@@ -502,7 +503,7 @@ nvfp4_status nvfp4_gdn_prefill(const void* q, int64_t ldq, const void* k, int64_
  * never read or write outside the buffers, and calls larger than a launch are refused
  * (NVFP4_ESHAPE): more than 65535 sequences, (B + 7) times the heads times the nodes above
  * 2^22 (attention), more than 2^22 chunks of 8192 logits (verification), 2^22 heads
- * of k and v in all sequences and layers (compaction), or 2^22 pieces of 16 KB (pages).
+ * of k and v in all sequences and layers (compaction), or 2^24 - 1 pieces of 4 KB (pages).
  * ------------------------------------------------------------------------- */
 #define NVFP4_MAX_NODES 64
 #define NVFP4_MAX_LAYERS 64

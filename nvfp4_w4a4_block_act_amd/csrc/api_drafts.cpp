@@ -14,6 +14,7 @@ namespace {
 using namespace nvfp4::checks;
 
 constexpr int kMaxNodes = NVFP4_MAX_NODES;
+constexpr int64_t kMaxCopies = (1 << 24) - 1;  // workgroups of 256 threads: below 2^32 threads
 
 nvfp4_status check_tree(const nvfp4::TreeArgs& a, int64_t B, const nvfp4_kv_cache* cache, int64_t max_len, int64_t window,
                         size_t workspace_bytes) {
@@ -185,7 +186,7 @@ nvfp4_status nvfp4_kv_copy_pages(const nvfp4_kv_cache* caches, int32_t layers, c
   if (s != NVFP4_OK) return s;
   if (n < 0) return NVFP4_EINVAL;
   const int64_t groups = nvfp4::copy_groups(nvfp4::page_shape(c.shape));
-  if (n >= kMaxDim || groups > kMaxGroups || n > kMaxGroups / (2 * layers * groups)) return NVFP4_ESHAPE;
+  if (n >= kMaxDim || n > kMaxCopies / (2 * layers * groups)) return NVFP4_ESHAPE;
   if (n == 0) return NVFP4_OK;
   if (!src || !dst) return NVFP4_EINVAL;
   if (!all_aligned({src, dst})) return NVFP4_EALIGN;
