@@ -27,13 +27,13 @@
 // the pool, look at it.  In these tiles values that are no finite number are taken as 0, so
 // that a node's row that holds one does not reach the rows that do not see it.
 //
-// Bound by memory for few rows, by the issue of instructions for many: 48 sequences of up to 4099
+// Bound by memory for few rows, by each wave's chain of steps in a tile for many: 48 sequences of up to 4099
 // (E4M3, 5 heads on each of 8, 250 MB) take 54 us with 3 nodes (4.4 TB/s), 64 with 6, 96 with 12 and 125 with
-// 16 (80 rows in 128: two waves on a SIMD, each some 340 instructions a tile, which is 1.2 us;
-// 14 us of it the join).  6 of up to 32768 (bf16, 64 nodes, 6 heads of 256 on each of 4) take 455 us: 456 TFLOP/s
-// of the products, 684 of the matrix instructions, 55 % of a large matrix product's rate, with LDS
-// busy 60 % of the time: a wave has room for 16 rows' sums, and every 16 rows read the whole tile.
-// Four waves of 32 rows, one on a SIMD, take 637 us, without the overlap 488.
+// 16 (80 rows in 128: a turn takes 1.2 us; the fourth wave, which has no rows, may as well idle: no change; 14 us of
+// it the join).  6 of up to 32768 (bf16, 64 nodes, 6 heads of 256 on each of 4) take 436 us: 476 TFLOP/s
+// of the products, 714 of the matrix instructions, 58 % of a large matrix product's rate, with LDS
+// busy half of the time: a wave has room for 16 rows' sums, and every 16 rows read the whole tile.
+// Four waves of 32 rows, one on a SIMD, took 637 us, without the overlap 488, where this took 455.
 #include <algorithm>
 #include <type_traits>
 
@@ -77,7 +77,8 @@ struct Shape {
   // Where 16-byte piece `piece` of a row lies in LDS.  An access of 16 bytes a lane is served 16 lanes at a
   // time, of which 8 come from one run of 16 lanes and 8 from the next: here the 16 rows (keys) or pieces
   // (values) of such a set, from two neighbouring g, always fall on different banks, and so do the two rows
-  // that E4M3 lanes write side by side.  (Rows padded by 16 bytes instead spent 17 to 19 % of the time on conflicts.)
+  // that E4M3 lanes write side by side.  (Counted: conflicts take none of the time over bf16, 8 % over E4M3; with rows
+  // padded by 16 bytes instead 17 to 19 %.)
   static __device__ __forceinline__ int key_spot(int row, int piece) {
     return row * kLdsRow + (piece ^ (DIM == 64 ? row / 2 % 8 : row % 16)) * 16;
   }
@@ -749,8 +750,7 @@ int wg_rows(int64_t rows) { return rows <= 16 ? 16 : (rows <= 32 ? 32 : (rows <=
 Plan tree_plan(int64_t B, int nodes, int q_heads, int kv_heads, int head_dim, int64_t max_len, int64_t window) {
   const int64_t rows = (int64_t)nodes * (q_heads / kv_heads), per = wg_rows(rows);
   const int64_t blocks = (rows + per - 1) / per, each = B * kv_heads * blocks;
-  // workgroups that a CU runs at once: two, or one of eight waves
-  const Splits s = tree_splits(each, head_dim == 256 && per == 128 ? 1 : 2, max_len, nodes, window);
+  const Splits s = tree_splits(each, max_len, nodes, window);
   return {(int)each, (int)blocks, s.count, s.tokens, (int)tree_span(max_len, nodes, window)};
 }
 

@@ -17,6 +17,9 @@
 // eps)) * w: its head_dim / 16 items sit in as many lanes side by side of one wave (their
 // number is a power of two, and heads start at its multiples), which add their squares by
 // exchanges, in binary32; the values stay in registers between norm, rotation and rounding.
+// The rows above with both norms take 253 us, 5.4 TB/s, against 222 to 229 without: a wave waits for the
+// exchanges with its loads done.  Weights through LDS took 254, four tokens a workgroup 291, 72
+// registers instead of 78 (spills) 276, a root and a division instead of the root's instruction 251.
 #include <algorithm>
 
 #include "common.hpp"

@@ -18,12 +18,12 @@ __host__ __device__ inline int64_t tree_span(int64_t ctx, int64_t nodes, int64_t
   return (window > 0 && window < ctx ? window + kTreeTile - 1 : ctx) + nodes;
 }
 
-// rows: workgroups of one split; per_cu: of them that a CU runs at once.  About three rounds of workgroups: 48
-// sequences of up to 4099, 16 nodes, 5 query heads on each of 8, take 5 % more time with half as many splits and 2 %
-// with twice, 6 of up to 32768, 64 nodes, 6 heads of 256 on each of 4, 28 % and none.
-inline Splits tree_splits(int64_t rows, int per_cu, int64_t max_len, int64_t nodes, int64_t window) {
+// rows: workgroups of one split.  About six workgroups for each CU, of which one or two run at once: 6 sequences of
+// up to 32768, 64 nodes, 6 heads of 256 on each of 4 (one at once), take 436 us, 459 with three, 475 with eight and 493
+// with nine; 48 of up to 4099, 16 nodes, 5 heads on each of 8 (two), 125, 129 with three, 128 with eight and 135 with twelve.
+inline Splits tree_splits(int64_t rows, int64_t max_len, int64_t nodes, int64_t window) {
   const int64_t span = tree_span(max_len, nodes, window);
-  const int64_t want = std::max<int64_t>(1, (int64_t)kCUs * 3 * per_cu / rows);
+  const int64_t want = std::max<int64_t>(1, (int64_t)kCUs * 6 / rows);
   int64_t n = std::min(want, std::max<int64_t>(1, span / 512));
   if (n > 1 && rows * n < 2 * kCUs) n = std::min((2 * kCUs + rows - 1) / rows, span / 256);
   const int64_t tokens = (std::max<int64_t>(1, (span + n - 1) / n) + kTreeTile - 1) / kTreeTile * kTreeTile;

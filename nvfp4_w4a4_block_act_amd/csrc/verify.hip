@@ -3,8 +3,9 @@
 // Everything that decides is binary64: a token is the first whose running sum of weights
 // passes u times their total, and over a vocabulary of 10^5 the borders lie so close that
 // binary32 sums, or exponentials of binary32, would draw another token once in some
-// thousand draws.  e^((l - m) / T) is 2^(n + f), 2^f the first twelve terms of its power
-// series (|f| <= 1/2: the rest is below 2^-47 of it).
+// thousand draws.  e^((l - m) / T) is 2^(n + i / 256 + f): the power of i / 256 from a table in
+// LDS, 2^f the first four terms of its series (|f| <= 1/512: the rest is below 2^-42 of it).
+// (Without a table twelve terms are needed: 186 us against 136 for the sizes below.)
 //
 // verify_rows: one pass over the logits, and the only one.  A workgroup takes one chunk of
 // 8192 logits of one node, 32 to a thread, all loads in flight at once: their maximum, where
@@ -19,6 +20,11 @@
 // the one that finishes last (a count that verify_rows clears) draws from these sums.
 //
 // Every sum has a fixed order: results do not depend on timing.
+//
+// verify_rows is bound by the vector units, and by memory little behind them: 64 x 24 rows of 131072 logits
+// (805 MB) take 136 us, 5.9 TB/s, with 83 % of the vector units' time in use; 2 x 174 rows of 100003 take 30.
+// verify_draw is bound by its chain of loads, sums and exchanges: 8.4 us for one sequence, 13.6 for 64,
+// and 22.6 for 29 of which each sums the residuals of 100003 logits.
 #include <algorithm>
 
 #include "common.hpp"

@@ -55,26 +55,25 @@ int main() {
               ++n;
             }
   // A sequence of any length under the bound has no more splits than the launch, all of whole tiles.
-  for (int64_t rows : {1, 7, 100, 384, 2000, 100000})
-    for (int per_cu : {1, 2})
-      for (int64_t max_len : {0, 1, 31, 500, 1024, 4099, 33333, 1 << 20, 1 << 30})
-        for (int64_t window : {0, 1, 100, 5000})
-          for (int nodes : {1, 17, 64}) {
-            const nvfp4::Splits s = nvfp4::tree_splits(rows, per_cu, max_len, nodes, window);
-            const int64_t span_bound = nvfp4::tree_span(max_len, nodes, window);
-            if (s.count < 1 || s.tokens % nvfp4::kTreeTile || (int64_t)s.count * s.tokens < span_bound)
-              printf("splits %d of %d for %lld\n", s.count, s.tokens, (long long)span_bound), ++bad;
-            for (int64_t len = 0; len <= max_len; len = len * 3 / 2 + 1) {
-              const int64_t begin = window > 0 && window < len ? (len - window) / nvfp4::kTreeTile * nvfp4::kTreeTile : 0;
-              const int64_t span = len + nodes - begin;
-              if (span > span_bound) printf("span %lld above %lld\n", (long long)span, (long long)span_bound), ++bad;
-              const int t = s.count == 1 ? s.tokens : nvfp4::tree_split_tokens((int)rows, s.tokens, (int)span_bound, (int)span);
-              if (t < nvfp4::kTreeTile || t % nvfp4::kTreeTile || (span + t - 1) / t > s.count)
-                printf("rows %lld, %lld of %lld: %d splits of %d, sequence's %d\n", (long long)rows, (long long)span, (long long)span_bound,
-                       s.count, s.tokens, t), ++bad;
-              ++n;
-            }
+  for (int64_t rows : {1, 7, 72, 100, 384, 2000, 100000})
+    for (int64_t max_len : {0, 1, 31, 500, 1024, 4099, 33333, 1 << 20, 1 << 30})
+      for (int64_t window : {0, 1, 100, 5000})
+        for (int nodes : {1, 17, 64}) {
+          const nvfp4::Splits s = nvfp4::tree_splits(rows, max_len, nodes, window);
+          const int64_t span_bound = nvfp4::tree_span(max_len, nodes, window);
+          if (s.count < 1 || s.tokens % nvfp4::kTreeTile || (int64_t)s.count * s.tokens < span_bound)
+            printf("splits %d of %d for %lld\n", s.count, s.tokens, (long long)span_bound), ++bad;
+          for (int64_t len = 0; len <= max_len; len = len * 3 / 2 + 1) {
+            const int64_t begin = window > 0 && window < len ? (len - window) / nvfp4::kTreeTile * nvfp4::kTreeTile : 0;
+            const int64_t span = len + nodes - begin;
+            if (span > span_bound) printf("span %lld above %lld\n", (long long)span, (long long)span_bound), ++bad;
+            const int t = s.count == 1 ? s.tokens : nvfp4::tree_split_tokens((int)rows, s.tokens, (int)span_bound, (int)span);
+            if (t < nvfp4::kTreeTile || t % nvfp4::kTreeTile || (span + t - 1) / t > s.count)
+              printf("rows %lld, %lld of %lld: %d splits of %d, sequence's %d\n", (long long)rows, (long long)span, (long long)span_bound,
+                     s.count, s.tokens, t), ++bad;
+            ++n;
           }
+        }
   if (bad) return 1;
   printf("ok %d\n", n);
   return 0;

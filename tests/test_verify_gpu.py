@@ -1,6 +1,6 @@
 """The verification of drafted tokens against oracle/drafts.py in 64 bits: tokens, paths and counts
 are equal.  Probabilities and sums of both sides are binary64 (errors below 2^-40 of the total:
-131072 terms of 2^-47 relative each, summed in 53 bits), so cases whose closest decision is farther
+131072 terms of 2^-42 relative each, summed in 53 bits), so cases whose closest decision is farther
 from its border than 2^-36 have one answer; the seeds are such cases, and the tests say so."""
 import numpy as np
 import pytest
