@@ -965,10 +965,12 @@ def kv_compact(block_table, ctx_lens, path, counts, caches, *, stream=None):
     """Moves the rows of accepted nodes to where their sequences go on, in one PagedKVCache or those of all layers
     (a list of up to 64 of one shape): row ctx_lens[b] + path[b, i] to ctx_lens[b] + i for i < counts[b].
 
-    block_table: int32 [B, pages]; ctx_lens, counts: int32 [B]; path: int32 [B, nodes] (see verify_drafts)."""
+    block_table: contiguous int32 [B, pages]; ctx_lens, counts: int32 [B]; path: int32 [B, nodes] (see verify_drafts)."""
     dev = block_table.get_device()
     B = block_table.shape[0]
     ldt = _block_table(block_table, dev, B)
+    # (lengths on the device may reach any of a row's ldt entries)
+    assert ldt == block_table.shape[1], "block_table: contiguous int32 [B, pages]"
     assert path.dim() == 2, "path: int32 [B, nodes]"
     _dense(path, dev, torch.int32, (B, path.shape[1]), "path: contiguous int32 [B, nodes]")
     _table(ctx_lens, dev, torch.int32, B, "ctx_lens: int32 [B]")

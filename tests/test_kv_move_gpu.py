@@ -133,3 +133,17 @@ def test_past_two_to_the_31st_element():
     torch.cuda.synchronize()
     assert torch.equal(c.k[-2, 127], last[1]) and torch.equal(c.k[-2, :127], low[:127]) and torch.equal(c.k[-1], last)
     assert not c.k[: 100].any() and not c.k[-100:-3].any()
+
+
+def test_compact_takes_whole_block_tables():
+    """A table of which one sequence's row is every sequence's, or whose rows have entries that are not its own
+    behind them, is refused: lengths on the device could reach those."""
+    host, dev = caches(1, 6, 16, 2, 64, True, "plain", 2)
+    wide = torch.arange(12, dtype=torch.int32, device=DEV).reshape(2, 6)
+    lens, path, counts = torch.zeros(2, dtype=torch.int32, device=DEV), torch.zeros((2, 4), dtype=torch.int32, device=DEV), \
+        torch.ones(2, dtype=torch.int32, device=DEV)
+    for table in (wide[:1].expand(2, 6), wide[:, 2:], wide.t()[:2]):
+        with pytest.raises(AssertionError):
+            nv.kv_compact(table, lens, path, counts, dev)
+    torch.cuda.synchronize()
+    same(host, dev, True)
