@@ -183,3 +183,34 @@ def test_empty_batch():
     e = lambda *s, dtype=torch.float32: torch.empty(*s, dtype=dtype, device=DEV)  # noqa: E731
     tokens, path, counts = nv.verify_drafts(e(0, 3, 50), e(0, 3, dtype=torch.int64))
     assert tokens.shape == path.shape == (0, 3) and counts.shape == (0,)
+
+
+def test_two_graphs_of_drawn_drafts_with_one_workspace():
+    """The form whose workgroups count each other, captured twice over one workspace and replayed in turn with
+    other numbers, eager calls and synchronizations between the replays: each equals an eager call."""
+    ws = nv.Workspace(DEV)
+    sides = []
+    for seed, (B, W, V) in ((21, (3, 5, 20001)), (22, (40, 3, 9000))):
+        c = {k: _dev(x) for k, x in _case(B, W, V, seed=seed, sampled=True, kind="chain", greedy=1).items()}
+        c["parents"] = None
+        ws.get(nv.nvfp4_verify_drafts_workspace_bytes(B, W, V, True))
+        sides.append(c)
+    graphs = []
+    for c in sides:
+        out = nv.verify_drafts(**c, workspace=ws)
+        torch.cuda.synchronize()
+        g = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(g):
+            nv.verify_drafts(**c, workspace=ws, out=out)
+        graphs.append((g, out))
+    for turn in range(4):
+        for c, (g, out) in zip(sides, graphs):
+            c["uniforms"].copy_(_dev(np.random.default_rng(turn).random(tuple(c["uniforms"].shape)).astype(np.float32)))
+            c["temperature"][-1] = 0.0 if turn % 2 else 0.9
+            for o in out:
+                o.fill_(7)
+            g.replay()
+            want = nv.verify_drafts(**c)
+            torch.cuda.synchronize()
+            for a, b in zip(out, want):
+                assert torch.equal(a, b), f"turn {turn}"
