@@ -178,7 +178,7 @@ __global__ __launch_bounds__(kThreads) void verify_rows_kernel(VerifyArgs a, Siz
   float m = -INFINITY;
 #pragma unroll
   for (int e = 0; e < kEach; ++e) m = fmaxf(m, x[e]);
-  const float mine = m;
+  float mine = m;
   __shared__ float ms[kThreads / 64];
   __shared__ int found;  // where the largest is
   __shared__ double table[kSteps];
@@ -203,15 +203,21 @@ __global__ __launch_bounds__(kThreads) void verify_rows_kernel(VerifyArgs a, Siz
       for (; kids; kids &= kids - 1) {
         const int64_t t = __shfl(token, __builtin_ctzll(kids)) - first;
         if (t < 0 || t >= count || (t / 4) % kThreads != threadIdx.x) continue;
-        const int mine = (int)(t / 4 / kThreads * 4 + t % 4);
+        const int at = (int)(t / 4 / kThreads * 4 + t % 4);
+        mine = -INFINITY;
 #pragma unroll
-        for (int e = 0; e < kEach; ++e)
-          if (e == mine) x[e] = -INFINITY;
+        for (int e = 0; e < kEach; ++e) {
+          if (e == at) x[e] = -INFINITY;
+          mine = fmaxf(mine, x[e]);
+        }
       }
     }
     const Scale scale = scale_of(heat_of(a, b), m > -INFINITY ? m : 0.0f, table);
 #pragma unroll
     for (int e = 0; e < kEach; ++e) sum += scale.of(x[e]);
+    // A weight of -inf is 2^-1000 here: nothing beside another weight, but a chunk that has only such ones has
+    // none (the draw looks for a token in every chunk whose sum is above 0).
+    if (!(mine > -INFINITY)) sum = 0;
     __shared__ double sums[kThreads / 64];
     sum = block_sum(sum, sums);
   } else {
