@@ -517,6 +517,8 @@ nvfp4_status nvfp4_gdn_prefill(const void* q, int64_t ldq, const void* k, int64_
  * last `window` (0: all).  Pages, heads and padding as in nvfp4_attn_decode: tokens on a page number
  * outside the pool are left out like masked ones, rows that a node does not see may hold
  * anything (NaN included) without any effect on it, and a padded node gives out = 0, lse = -inf.
+ * An element of a value row that is no finite number makes that element of out inf or NaN
+ * for the nodes that do see the row.
  *
  *   q          bf16 [B][nodes][q_heads][head_dim], a node's row stride ldq (multiple of 8).
  *   block_table int32 [B][ldt], ldt >= ceil((max_len + nodes) / page_size).

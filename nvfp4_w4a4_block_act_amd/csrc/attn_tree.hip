@@ -25,7 +25,8 @@
 // Masks: the ancestors of a node are a word of 64 bits that the wave forms from the parents by
 // doubling; only tiles that hold drafted tokens, or the edge of a window, or a page outside
 // the pool, look at it.  In these tiles values that are no finite number are taken as 0, so
-// that a node's row that holds one does not reach the rows that do not see it.
+// that a node's row that holds one does not reach the rows that do not see it; where any
+// was, the rows that do see it get it at the end (the check for that takes 0.3 us of 14, 1 of 126).
 //
 // Bound by memory for few rows, by each wave's chain of steps in a tile for many: 48 sequences of up to 4099
 // (E4M3, 5 heads on each of 8, 250 MB) take 54 us with 3 nodes (4.4 TB/s), 64 with 6, 96 with 12 and 125 with
@@ -303,7 +304,8 @@ __global__ __launch_bounds__(RW* KW * 64, MIN) void attn_tree_kernel(TreeArgs a,
       }
     }
   };
-  auto put_values = [&](const Held& h, bool masked, uint8_t* lds) {
+  uint32_t dropped = 0;  // bits of values of this lane that `put_values` took for 0 in rows of the sequence
+  auto put_values = [&](const Held& h, int turn, bool masked, uint8_t* lds) {
 #pragma unroll
     for (int i = 0; i < kLoads; ++i) {
       uint32_t w[FP8 ? 8 : 4];
@@ -315,8 +317,15 @@ __global__ __launch_bounds__(RW* KW * 64, MIN) void attn_tree_kernel(TreeArgs a,
           w[x] = h.x[i][x];
       }
       if (masked) {
+        const int token = (tile0 + turn * KW) * kTreeTile + min(i * kMembers + member, kPieces - 1) / Sh::kLanes;
+        uint32_t gone = 0;
 #pragma unroll
-        for (int x = 0; x < (FP8 ? 8 : 4); ++x) w[x] = finite_pair(w[x], FP8 ? 0x7C00u : 0x7F80u);
+        for (int x = 0; x < (FP8 ? 8 : 4); ++x) {
+          const uint32_t kept = finite_pair(w[x], FP8 ? 0x7C00u : 0x7F80u);
+          gone |= w[x] ^ kept;
+          w[x] = kept;
+        }
+        dropped |= token < end ? gone : 0;
       }
       *reinterpret_cast<uint4*>(lds + value_spot[i]) = make_uint4(w[0], w[1], w[2], w[3]);
       if constexpr (FP8) *reinterpret_cast<uint4*>(lds + (value_spot[i] ^ 16)) = make_uint4(w[4], w[5], w[6], w[7]);
@@ -488,7 +497,7 @@ __global__ __launch_bounds__(RW* KW * 64, MIN) void attn_tree_kernel(TreeArgs a,
       const uint32_t gone_now = gone;
       const bool masked = is_masked(t, gone_now);
       put_keys(k, corner);
-      put_values(v, masked, values);
+      put_values(v, t, masked, values);
       wave_lds_fence();
       start_turn(min(t + 1, last));
       Scores s = scores_of(read_keys(corner));
@@ -518,7 +527,7 @@ __global__ __launch_bounds__(RW* KW * 64, MIN) void attn_tree_kernel(TreeArgs a,
     fetch_keys(0);
     fetch(vc, ahead, v);
     put_keys(k, keys[0]);
-    put_values(v, is_masked(0, gone & 3u), values[0]);
+    put_values(v, 0, is_masked(0, gone & 3u), values[0]);
     fetch_keys(1);
     fetch(vc, ahead, v);
     lds_barrier();
@@ -531,7 +540,7 @@ __global__ __launch_bounds__(RW* KW * 64, MIN) void attn_tree_kernel(TreeArgs a,
       const uint32_t gone_now = gone >> 4 & 3u, gone_next = gone >> 2 & 3u;
       const Keys read = read_keys(keys[odd ^ 1]);
       put_keys(k, keys[odd]);
-      put_values(v, is_masked(min(t + 1, last), gone_next), values[odd ^ 1]);
+      put_values(v, min(t + 1, last), is_masked(min(t + 1, last), gone_next), values[odd ^ 1]);
       fetch(vc, ahead, v);  // of turn t + 2
       fetch_keys(t + 3);
       if (is_masked(t, gone_now)) mask(s, t, gone_now);
@@ -551,6 +560,45 @@ __global__ __launch_bounds__(RW* KW * 64, MIN) void attn_tree_kernel(TreeArgs a,
     }
   }
 
+  // element of the row that output tile i holds in row 4 g + j: value rows are read in runs of 16 bytes at most
+  constexpr int kEach = DIM == 256 ? 8 : DIM / 16;
+
+  // Dropped values reach the rows that see them: their tiles are looked through again, a token at a time.
+  if (RW > 1 ? __syncthreads_or(dropped != 0) : __any(dropped != 0)) {
+#pragma unroll 1
+    for (int t = 0; t < turns; ++t) {
+      const Place p = look_up(t);
+      if (!is_masked(t, p.gone) || tile0 + t * KW >= tile_end) continue;
+      const int start = (tile0 + t * KW) * kTreeTile;
+#pragma unroll 1
+      for (int x = 0; x < min(kTreeTile, end - start); ++x) {
+        if (p.gone >> (x / 16) & 1u) continue;
+        const int drafted = start + x - range.ctx;
+        bool sees[NR], one = false;
+#pragma unroll
+        for (int n = 0; n < NR; ++n) {
+          sees[n] = anc[n] != 0 && (drafted < 0 ? start + x >= low[n] : (anc[n] >> drafted & 1) != 0);
+          one |= sees[n];
+        }
+        if (!__any(one)) continue;
+        const uint8_t* row = vc + p.first + (x < 16 ? 0 : p.step) + (int64_t)(x % 16) * c.token_stride * ES;
+#pragma unroll
+        for (int j = 0; j < 4; ++j)
+#pragma unroll
+          for (int i = 0; i < DIM / 16; ++i) {
+            const int at = i / kEach * 128 + (g * 4 + j) * kEach + i % kEach;
+            const uint32_t code = FP8 ? row[at] : reinterpret_cast<const uint16_t*>(row)[at];
+            const float value = FP8 ? __builtin_nanf("") : __uint_as_float(code << 16);
+            const uint32_t exponent = FP8 ? 0x7Fu : 0x7F80u;
+            if ((code & exponent) == exponent) {
+#pragma unroll
+              for (int n = 0; n < NR; ++n) o[n][i][j] += sees[n] ? value : 0.0f;
+            }
+          }
+      }
+    }
+  }
+
   float l[NR];
 #pragma unroll
   for (int n = 0; n < NR; ++n) {
@@ -564,8 +612,6 @@ __global__ __launch_bounds__(RW* KW * 64, MIN) void attn_tree_kernel(TreeArgs a,
   float* parts = static_cast<float*>(a.workspace);
   const Sink sink = {a, parts, reinterpret_cast<float2*>(parts + (int64_t)a.B * a.nodes * a.q_heads * splits * DIM),
                      FP8 ? *c.v_amax / 448.0f : 1.0f, b, kvh, group, splits, split, only};
-  // element of the row that output tile i holds in row 4 g + j: value rows are read in runs of 16 bytes at most
-  constexpr int kEach = DIM == 256 ? 8 : DIM / 16;
   if constexpr (KW == 1) {
 #pragma unroll
     for (int n = 0; n < NR; ++n) {
