@@ -527,8 +527,7 @@ nvfp4_status nvfp4_gdn_prefill(const void* q, int64_t ldq, const void* k, int64_
  *   workspace  device scratch of nvfp4_attn_tree_workspace_bytes (contents need no setup;
  *              NULL allowed when that is 0).
  * Scores, the softmax and both sums are fp32; probabilities enter the product with V and
- * their sum to 16 significant bits over a bf16 cache, to 11 (fp16: those below 2^-14 of a
- * row's largest to 2^-25 of it) over E4M3.  The result does not depend on timing. */
+ * their sum to 16 significant bits.  The result does not depend on timing. */
 size_t nvfp4_attn_tree_workspace_bytes(int64_t B, int32_t nodes, int32_t q_heads, int32_t kv_heads, int32_t head_dim,
                                        int64_t max_len, int64_t window);
 

@@ -16,10 +16,10 @@
 //  * V^T: lane (c, g) takes its head_dim / 16 elements of the value rows of those eight tokens,
 //    and the transposition is byte permutes within the lane, once for the NR blocks;
 //  * the sum of the weights is one more row of that product, of ones.
-// Over a bf16 cache a weight enters as the sum of two bf16 values (16 significant bits, two
-// matrix instructions).  E4M3 codes widen exactly, keys to bf16 like the queries, values to fp16,
-// so that a weight there is one fp16 value: 11 bits, and 2^-25 of the reference's weight
-// where it is smaller than 2^-14, both far below the output's own rounding.
+// A weight enters as the sum of two bf16 values (16 significant bits, of small ones too; two
+// matrix instructions); E4M3 codes widen to bf16 exactly.  (One fp16 value over E4M3, 126 us instead of 142 for
+// 48 x 16, has 11 bits, which the logarithm of their sum shows, and loses weights below 2^-25 of the largest,
+// which are a part of the result in long contexts.)
 // Where waves share a tile, the scores of the next one are formed while this one's weights are.
 //
 // Masks: the ancestors of a node are a word of 64 bits that the wave forms from the parents by
@@ -29,14 +29,13 @@
 // was, the rows that do see it get it at the end (the check for that takes 0.3 us of 14, 1 of 126).
 //
 // Bound by memory for few rows, by each wave's chain of steps in a tile for many: 48 sequences of up to 4099
-// (E4M3, 5 heads on each of 8, 250 MB) take 54 us with 3 nodes (4.4 TB/s), 64 with 6, 96 with 12 and 125 with
-// 16 (80 rows in 128: a turn takes 1.2 us; the fourth wave, which has no rows, may as well idle: no change; 14 us of
-// it the join).  6 of up to 32768 (bf16, 64 nodes, 6 heads of 256 on each of 4) take 436 us: 476 TFLOP/s
-// of the products, 714 of the matrix instructions, 58 % of a large matrix product's rate, with LDS
+// (E4M3, 5 heads on each of 8, 250 MB) take 55 us with 3 nodes (4.3 TB/s), 70 with 6, 107 with 12 and 142 with
+// 16 (80 rows in 128; the fourth wave, which has no rows, may as well idle: no change; 14 us of
+// it the join).  6 of up to 32768 (bf16, 64 nodes, 6 heads of 256 on each of 4) take 438 us: 474 TFLOP/s
+// of the products, 711 of the matrix instructions, 57 % of a large matrix product's rate, with LDS
 // busy half of the time: a wave has room for 16 rows' sums, and every 16 rows read the whole tile.
 // Four waves of 32 rows, one on a SIMD, took 637 us, without the overlap 488, where this took 455.
 #include <algorithm>
-#include <type_traits>
 
 #include "common.hpp"
 #include "drafts.hpp"
@@ -93,20 +92,15 @@ __device__ __forceinline__ uint32_t fp8_bf16(uint32_t w, bool high) {
   return __builtin_bit_cast(uint32_t, high ? __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(w, 1.0f, true)
                                            : __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(w, 1.0f, false));
 }
-__device__ __forceinline__ uint32_t fp8_half(uint32_t w, bool high) {
-  return __builtin_bit_cast(uint32_t, high ? __builtin_amdgcn_cvt_scalef32_pk_f16_fp8(w, 1.0f, true)
-                                           : __builtin_amdgcn_cvt_scalef32_pk_f16_fp8(w, 1.0f, false));
-}
-
 template <class T>
 __device__ __forceinline__ T octet(uint32_t a, uint32_t b, uint32_t c, uint32_t d) {
   return __builtin_bit_cast(T, make_uint4(a, b, c, d));
 }
 
-// Two values of 16 bits, 0 for one that is no finite number: all bits of `exponent` set.
-__device__ __forceinline__ uint32_t finite_pair(uint32_t w, uint32_t exponent) {
-  if ((w & exponent) == exponent) w &= 0xFFFF0000u;
-  if ((w & exponent << 16) == exponent << 16) w &= 0xFFFFu;
+// Two bf16 values, 0 for one that is no finite number.
+__device__ __forceinline__ uint32_t finite_pair(uint32_t w) {
+  if ((w & 0x7F80u) == 0x7F80u) w &= 0xFFFF0000u;
+  if ((w & 0x7F800000u) == 0x7F800000u) w &= 0xFFFFu;
   return w;
 }
 
@@ -152,7 +146,6 @@ struct Sink {
 template <int DIM, bool FP8, int NR, int RW, int KW, int MIN>
 __global__ __launch_bounds__(RW* KW * 64, MIN) void attn_tree_kernel(TreeArgs a, Plan plan) {
   using Sh = Shape<DIM, FP8>;
-  using Op = typename std::conditional<FP8, half8_t, bf16x8_t>::type;  // of weights and values
   constexpr int ES = FP8 ? 1 : 2, PAD = DIM + 4, kRows = NR * RW * 16, kWaves = RW * KW;
   constexpr int kPieces = kTreeTile * Sh::kLanes, kMembers = RW * 64;  // of a tile's keys; lanes that load a tile
   constexpr int kLoads = (kPieces + kMembers - 1) / kMembers;          // of a lane, for keys and for values
@@ -312,7 +305,7 @@ __global__ __launch_bounds__(RW* KW * 64, MIN) void attn_tree_kernel(TreeArgs a,
 #pragma unroll
       for (int x = 0; x < (FP8 ? 8 : 4); ++x) {
         if constexpr (FP8)
-          w[x] = fp8_half(h.x[i][x / 2], x % 2);
+          w[x] = fp8_bf16(h.x[i][x / 2], x % 2);
         else
           w[x] = h.x[i][x];
       }
@@ -321,7 +314,7 @@ __global__ __launch_bounds__(RW* KW * 64, MIN) void attn_tree_kernel(TreeArgs a,
         uint32_t gone = 0;
 #pragma unroll
         for (int x = 0; x < (FP8 ? 8 : 4); ++x) {
-          const uint32_t kept = finite_pair(w[x], FP8 ? 0x7C00u : 0x7F80u);
+          const uint32_t kept = finite_pair(w[x]);
           gone |= w[x] ^ kept;
           w[x] = kept;
         }
@@ -336,7 +329,7 @@ __global__ __launch_bounds__(RW* KW * 64, MIN) void attn_tree_kernel(TreeArgs a,
     float4_t x[NR][2];
   };
   struct Weights {
-    Op hi[NR], lo[NR];
+    bf16x8_t hi[NR], lo[NR];
   };
   struct Keys {
     uint4 x[DIM / 32][2];
@@ -418,15 +411,11 @@ __global__ __launch_bounds__(RW* KW * 64, MIN) void attn_tree_kernel(TreeArgs a,
 #pragma unroll
       for (int e = 0; e < 4; ++e) {
         const float x = p[n][2 * e], y = p[n][2 * e + 1];
-        if constexpr (FP8) {
-          hw[e] = half_pair(x, y);
-        } else {
-          hw[e] = bf16_pair(x, y);
-          lw[e] = bf16_pair(x - __uint_as_float(hw[e] << 16), y - __uint_as_float(hw[e] & 0xFFFF0000u));
-        }
+        hw[e] = bf16_pair(x, y);
+        lw[e] = bf16_pair(x - __uint_as_float(hw[e] << 16), y - __uint_as_float(hw[e] & 0xFFFF0000u));
       }
-      w.hi[n] = octet<Op>(hw[0], hw[1], hw[2], hw[3]);
-      if constexpr (!FP8) w.lo[n] = octet<Op>(lw[0], lw[1], lw[2], lw[3]);
+      w.hi[n] = octet<bf16x8_t>(hw[0], hw[1], hw[2], hw[3]);
+      w.lo[n] = octet<bf16x8_t>(lw[0], lw[1], lw[2], lw[3]);
     }
     return w;
   };
@@ -452,26 +441,22 @@ __global__ __launch_bounds__(RW* KW * 64, MIN) void attn_tree_kernel(TreeArgs a,
   };
   // The values, whose first run has been read.
   auto add_values = [&](const Weights& w, const Run& first, const uint8_t* lds) {
-    auto add = [&](Op v, int n, float4_t& to) {
-      if constexpr (FP8) {
-        to = __builtin_amdgcn_mfma_f32_16x16x32_f16(v, w.hi[n], to, 0, 0, 0);
-      } else {
-        to = __builtin_amdgcn_mfma_f32_16x16x32_bf16(v, w.lo[n], to, 0, 0, 0);
-        to = __builtin_amdgcn_mfma_f32_16x16x32_bf16(v, w.hi[n], to, 0, 0, 0);
-      }
+    auto add = [&](bf16x8_t v, int n, float4_t& to) {
+      to = __builtin_amdgcn_mfma_f32_16x16x32_bf16(v, w.lo[n], to, 0, 0, 0);
+      to = __builtin_amdgcn_mfma_f32_16x16x32_bf16(v, w.hi[n], to, 0, 0, 0);
     };
-    constexpr uint32_t kOnes = FP8 ? 0x3C003C00u : 0x3F803F80u;
+    constexpr uint32_t kOnes = 0x3F803F80u;
 #pragma unroll
-    for (int n = 0; n < NR; ++n) add(octet<Op>(kOnes, kOnes, kOnes, kOnes), n, sum[n]);
+    for (int n = 0; n < NR; ++n) add(octet<bf16x8_t>(kOnes, kOnes, kOnes, kOnes), n, sum[n]);
 #pragma unroll
     for (int u = 0; u < kRuns; ++u) {
       const Run v = u == 0 ? first : read_run(lds, u);
 #pragma unroll
       for (int x = 0; x < kRun; ++x) {
-        const Op even = octet<Op>(low_halves(v.x[0][x], v.x[1][x]), low_halves(v.x[2][x], v.x[3][x]),
-                                  low_halves(v.x[4][x], v.x[5][x]), low_halves(v.x[6][x], v.x[7][x]));
-        const Op odd = octet<Op>(high_halves(v.x[0][x], v.x[1][x]), high_halves(v.x[2][x], v.x[3][x]),
-                                 high_halves(v.x[4][x], v.x[5][x]), high_halves(v.x[6][x], v.x[7][x]));
+        const bf16x8_t even = octet<bf16x8_t>(low_halves(v.x[0][x], v.x[1][x]), low_halves(v.x[2][x], v.x[3][x]),
+                                              low_halves(v.x[4][x], v.x[5][x]), low_halves(v.x[6][x], v.x[7][x]));
+        const bf16x8_t odd = octet<bf16x8_t>(high_halves(v.x[0][x], v.x[1][x]), high_halves(v.x[2][x], v.x[3][x]),
+                                             high_halves(v.x[4][x], v.x[5][x]), high_halves(v.x[6][x], v.x[7][x]));
         const int i = (u * kRun + x) * 2;
 #pragma unroll
         for (int n = 0; n < NR; ++n) add(even, n, o[n][i]), add(odd, n, o[n][i + 1]);
@@ -823,15 +808,17 @@ hipError_t launch_dim(const TreeArgs& a, hipStream_t stream) {
   // Few rows: groups of waves that take tiles in turn.  More: waves that share a tile, two blocks of 16 rows to
   // each where the accumulators leave room (heads of 256: one).  What spills is not taken: two blocks to each of
   // four such groups took 191 us for 48 sequences, 30 rows, in bf16, two waves with one block in two groups 120
-  // (E4M3: 64 and 69); heads of 256 have one wave on a SIMD there, 148 us against 228 for 6 x 32768.
+  // (E4M3, heads of 128: 70 and 74, heads of 64: 46 and 44); heads of 256 have one wave on a SIMD there, 148 us
+  // against 228 for 6 x 32768.
   if constexpr (DIM == 256) {
     e = rows == 16   ? launch_rows<DIM, FP8, 1, 1, 4, 1>(a, plan, stream)
         : rows == 32 ? launch_rows<DIM, FP8, 1, 2, 2, 1>(a, plan, stream)
         : rows == 64 ? launch_rows<DIM, FP8, 1, 4, 1, 2>(a, plan, stream)
                      : launch_rows<DIM, FP8, 1, 8, 1, 2>(a, plan, stream);
   } else {
+    constexpr bool kPairs = FP8 && DIM == 128;
     e = rows == 16   ? launch_rows<DIM, FP8, 1, 1, 4, 2>(a, plan, stream)
-        : rows == 32 ? launch_rows<DIM, FP8, FP8 ? 2 : 1, FP8 ? 1 : 2, FP8 ? 4 : 2, 2>(a, plan, stream)
+        : rows == 32 ? launch_rows<DIM, FP8, kPairs ? 2 : 1, kPairs ? 1 : 2, kPairs ? 4 : 2, 2>(a, plan, stream)
         : rows == 64 ? launch_rows<DIM, FP8, 1, 4, 1, 2>(a, plan, stream)
                      : launch_rows<DIM, FP8, 2, 4, 1, 2>(a, plan, stream);
   }
