@@ -17,9 +17,9 @@
 // eps)) * w: its head_dim / 16 items sit in as many lanes side by side of one wave (their
 // number is a power of two, and heads start at its multiples), which add their squares by
 // exchanges, in binary32; the values stay in registers between norm, rotation and rounding.
-// The rows above with both norms take 253 us, 5.4 TB/s, against 222 to 229 without: a wave waits for the
+// The rows above with both norms take 251 us, 5.4 TB/s, against 222 to 229 without: a wave waits for the
 // exchanges with its loads done.  Weights through LDS took 254, four tokens a workgroup 291, 72
-// registers instead of 78 (spills) 276, a root and a division instead of the root's instruction 251.
+// registers instead of 78 (spills) 276.
 #include <algorithm>
 
 #include "common.hpp"
@@ -62,11 +62,8 @@ __device__ __forceinline__ void norm_head(float (&x)[8], float (&y)[8], const fl
 #pragma unroll
   for (int j = 0; j < 8; ++j) sum += x[j] * x[j] + y[j] * y[j];
   for (int m = 1; m < per; m *= 2) sum += __shfl_xor(sum, m);
-  // (a power of two; the root's instruction is off by one unit in the last place, and takes no subnormals)
-  const float mean = sum * (1.0f / (float)(per * 16)) + eps;
-  const bool tiny = mean < 0x1p-100f;
-  const float root = __builtin_amdgcn_rsqf(tiny ? mean * 0x1p100f : mean) * (tiny ? 0x1p50f : 1.0f);
-  const float by = mean > 0.0f ? root : 0.0f;
+  const float mean = sum * (1.0f / (float)(per * 16)) + eps;  // (a power of two)
+  const float by = mean > 0.0f ? 1.0f / sqrtf(mean) : 0.0f;
   float w1[8], w2[8];
   load8<true>(w, o1, w1);
   load8<true>(w, o2, w2);
