@@ -400,7 +400,7 @@ nvfp4_status nvfp4_kv_append(const void* q, const void* k, const void* v, int32_
  * binary32, rounded once, after the rotation.  q_norm, k_norm: fp32 [head_dim], the
  * weights w for the heads of q and of k; NULL: no norm of these (q_norm needs q).  eps is
  * finite, >= 0 (a head of zeros stays zero where it is 0).  |x| below 2^60, so that the
- * squares' sum is finite; everything else as in nvfp4_kv_append. */
+ * squares' sum is finite, and as small as binary32 has it; everything else as in nvfp4_kv_append. */
 nvfp4_status nvfp4_kv_append_norm(const void* q, const void* k, const void* v, int32_t src_dtype, int64_t T,
                                   int32_t q_heads, int64_t ldq, int64_t ldk, int64_t ldv, const float* q_norm,
                                   const float* k_norm, float eps, const float* rope, int32_t rot_dim, int64_t max_pos,

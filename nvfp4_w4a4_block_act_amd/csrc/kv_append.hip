@@ -56,13 +56,24 @@ __device__ __forceinline__ uint2 coded_run(uint4 w, float g) {
                     kv_encode_pair(w.z, g) | (kv_encode_pair(w.w, g) << 16));
 }
 
-// Norm of one head, the 16 elements of this thread: per lanes side by side hold the head.
-__device__ __forceinline__ void norm_head(float (&x)[8], float (&y)[8], const float* w, int o1, int o2, int per, float eps) {
+// The squares' sum of one head, the 16 elements of this thread: per lanes side by side hold the head.
+__device__ __forceinline__ float squares(const float (&x)[8], const float (&y)[8], int per) {
   float sum = 0;
 #pragma unroll
   for (int j = 0; j < 8; ++j) sum += x[j] * x[j] + y[j] * y[j];
   for (int m = 1; m < per; m *= 2) sum += __shfl_xor(sum, m);
-  const float mean = sum * (1.0f / (float)(per * 16)) + eps;  // (a power of two)
+  return sum;
+}
+
+// Norm of the head.
+__device__ __forceinline__ void norm_head(float (&x)[8], float (&y)[8], const float* w, int o1, int o2, int per, float eps) {
+  const float part = 1.0f / (float)(per * 16);  // (a power of two)
+  float mean = squares(x, y, per) * part + eps;
+  if (mean < 0x1p-100f) {  // (in all lanes of the head) squares that lose bits, or vanish: the head times 2^100
+#pragma unroll
+    for (int j = 0; j < 8; ++j) x[j] *= 0x1p100f, y[j] *= 0x1p100f;
+    mean = squares(x, y, per) * part + eps * 0x1p100f * 0x1p100f;
+  }
   const float by = mean > 0.0f ? 1.0f / sqrtf(mean) : 0.0f;
   float w1[8], w2[8];
   load8<true>(w, o1, w1);
