@@ -74,7 +74,7 @@ __device__ __forceinline__ void norm_head(float (&x)[8], float (&y)[8], const fl
     for (int j = 0; j < 8; ++j) x[j] *= 0x1p100f, y[j] *= 0x1p100f;
     mean = squares(x, y, per) * part + eps * 0x1p100f * 0x1p100f;
   }
-  const float by = mean > 0.0f ? 1.0f / sqrtf(mean) : 0.0f;
+  const float by = mean == 0.0f ? 0.0f : 1.0f / sqrtf(mean);
   float w1[8], w2[8];
   load8<true>(w, o1, w1);
   load8<true>(w, o2, w2);

@@ -37,3 +37,29 @@ def test_small_heads(eps, src, dim):
     assert (off <= tol).all(), f"{(off > tol).sum()} of {y.size} off, worst {(off / tol).max():.1f} of the tolerance"
     keys = cache.k.view(T, dim).double().cpu().numpy()
     assert (np.abs(keys - y[:, 0]) <= tol[:, 0]).all()
+
+
+@pytest.mark.parametrize("bad", [float("nan"), float("inf")])
+def test_an_element_that_is_no_finite_number(bad):
+    """By the formula a head that holds NaN is NaN throughout; one that holds an infinity is NaN there and 0
+    elsewhere.  Other heads are what they were."""
+    g = torch.Generator(DEV).manual_seed(1)
+    x, w = torch.randn(32, 5, 128, device=DEV, generator=g), torch.rand(128, device=DEV, generator=g) + 0.5
+    spoilt = x.clone()
+    spoilt[3, 2, 40] = spoilt[17, 0, 127] = spoilt[31, 4, 0] = bad
+    got = []
+    for a in (x, spoilt):
+        cache = nv.PagedKVCache.empty(2, 16, 5, 128, DEV)
+        q = nv.kv_append(a, a, cache, torch.arange(32, device=DEV), q=a, q_norm=w, k_norm=w)
+        got.append((q.float().cpu(), cache.k.view(32, 5, 128).float().cpu()))
+    torch.cuda.synchronize()
+    heads, at = ([3, 17, 31], [2, 0, 4]), ([3, 17, 31], [2, 0, 4], [40, 127, 0])
+    for good, out in zip(*got):
+        kept = torch.ones(32, 5, dtype=torch.bool)
+        kept[heads] = False
+        assert torch.equal(out[kept], good[kept])
+        assert torch.isnan(out[at]).all()
+        rest = torch.ones(32, 5, 128, dtype=torch.bool)
+        rest[at] = False
+        inside = out[rest & ~kept[..., None]]
+        assert torch.isnan(inside).all() if bad != bad else (inside == 0).all()
