@@ -17,22 +17,22 @@
 //    and the transposition is byte permutes within the lane, once for the NR blocks;
 //  * the sum of the weights is one more row of that product, of ones.
 // A weight enters as the sum of two bf16 values (16 significant bits, of small ones too; two
-// matrix instructions); E4M3 codes widen to bf16 exactly.  (One fp16 value over E4M3, 126 us instead of 142 for
+// matrix instructions); E4M3 codes widen to bf16 exactly.  (One fp16 value over E4M3, 126 us instead of 141 for
 // 48 x 16, has 11 bits, which the logarithm of their sum shows, and loses weights below 2^-25 of the largest,
 // which are a part of the result in long contexts.)
 // Where waves share a tile, the scores of the next one are formed while this one's weights are.
 //
-// Masks: the ancestors of a node are a word of 64 bits that the wave forms from the parents by
+// Masks: the ancestors of a node are 64 bits that the wave forms from the parents by
 // doubling; only tiles that hold drafted tokens, or the edge of a window, or a page outside
 // the pool, look at it.  In these tiles values that are no finite number are taken as 0, so
 // that a node's row that holds one does not reach the rows that do not see it; where any
 // was, the rows that do see it get it at the end (the check for that takes 0.3 us of 14, 1 of 126).
 //
 // Bound by memory for few rows, by each wave's chain of steps in a tile for many: 48 sequences of up to 4099
-// (E4M3, 5 heads on each of 8, 250 MB) take 55 us with 3 nodes (4.3 TB/s), 70 with 6, 107 with 12 and 142 with
+// (E4M3, 5 heads on each of 8, 250 MB) take 55 us with 3 nodes (4.3 TB/s), 75 with 6, 107 with 12 and 141 with
 // 16 (80 rows in 128; the fourth wave, which has no rows, may as well idle: no change; 14 us of
-// it the join).  6 of up to 32768 (bf16, 64 nodes, 6 heads of 256 on each of 4) take 438 us: 474 TFLOP/s
-// of the products, 711 of the matrix instructions, 57 % of a large matrix product's rate, with LDS
+// it the join).  6 of up to 32768 (bf16, 64 nodes, 6 heads of 256 on each of 4) take 435 us: 478 TFLOP/s
+// of the products, 717 of the matrix instructions, 58 % of a large matrix product's rate, with LDS
 // busy half of the time: a wave has room for 16 rows' sums, and every 16 rows read the whole tile.
 // Four waves of 32 rows, one on a SIMD, took 637 us, without the overlap 488, where this took 455.
 #include <algorithm>
@@ -104,17 +104,36 @@ __device__ __forceinline__ uint32_t finite_pair(uint32_t w) {
   return w;
 }
 
-// Nodes on each lane's way to the context, itself included, from the lanes' parents; 0 for a padded node.
-__device__ __forceinline__ uint64_t ancestors(int nodes, int lane, int up) {
+// A set of nodes, as two words: a shift of 64 bits by an amount in the last vector register that a wave has reads
+// a wrong amount, which the compiler does not know of (with 256 registers to a wave nodes saw rows of others).
+struct Nodes {
+  uint32_t lo, hi;
+  __device__ __forceinline__ bool none() const { return (lo | hi) == 0; }
+  __device__ __forceinline__ int count() const { return __popc(lo) + __popc(hi); }
+  __device__ __forceinline__ uint32_t has(int node) const {  // (mod 64)
+    const uint32_t l = lo, h = hi;
+    return (node & 32 ? h : l) >> (node & 31) & 1u;
+  }
+  __device__ __forceinline__ Nodes without_first() const {
+    const uint32_t l = lo, h = hi;
+    return {l & (l - 1), l ? h : h & (h - 1)};
+  }
+  __device__ __forceinline__ Nodes of(int lane) const { return {__shfl(lo, lane), __shfl(hi, lane)}; }
+};
+
+// Nodes on each lane's way to the context, itself included, from the lanes' parents; none for a padded node.
+__device__ __forceinline__ Nodes ancestors(int nodes, int lane, int up) {
   if (lane >= nodes || up < -1 || up >= lane) up = -2;
-  uint64_t seen = 1ull << lane;
+  const uint32_t own = 1u << (lane & 31);
+  Nodes seen = {lane < 32 ? own : 0, lane < 32 ? 0 : own};
   for (int s = 1; s < nodes; s *= 2) {
     const int at = max(up, 0);
-    const uint32_t lo = __shfl((uint32_t)seen, at), hi = __shfl((uint32_t)(seen >> 32), at);
+    const Nodes more = seen.of(at);
     const int next = __shfl(up, at);
-    if (up >= 0) seen |= (uint64_t)hi << 32 | lo, up = next;
+    if (up >= 0) seen.lo |= more.lo, seen.hi |= more.hi, up = next;
   }
-  return up == -1 ? seen : 0;
+  if (up != -1) seen = {0, 0};
+  return seen;
 }
 
 __device__ __forceinline__ int64_t lane_value(int64_t x, int lane) {
@@ -183,25 +202,24 @@ __global__ __launch_bounds__(RW* KW * 64, MIN) void attn_tree_kernel(TreeArgs a,
   const bool only = split_tokens >= range.span;  // the sequence has one split: no join
   if (split > 0 && from >= end) return;
 
-  const uint64_t anc_lane = ancestors(a.nodes, lane, parent);
+  const Nodes anc_lane = ancestors(a.nodes, lane, parent);
   const float scale = a.scale * (FP8 ? *c.k_amax / 448.0f : 1.0f) * kLog2e;
   // scores of the sign that makes the factor positive, so that the largest is the largest score
   const uint32_t flip = scale < 0.0f ? 0x80008000u : 0u;
   const float factor = fmaxf(fabsf(scale), 1e-37f);
-  uint64_t anc[NR];
+  Nodes anc[NR];
   int low[NR];  // first token of the context that the row sees
   bf16x8_t q[NR][DIM / 32];
   bool any = false;
 #pragma unroll
   for (int n = 0; n < NR; ++n) {
     const int node = min(row0 + n * 16 + r, all_rows - 1) / group;
-    const uint32_t lo = __shfl((uint32_t)anc_lane, node), hi = __shfl((uint32_t)(anc_lane >> 32), node);
-    anc[n] = (uint64_t)hi << 32 | lo;
+    anc[n] = anc_lane.of(node);
     low[n] = 0;
-    any |= anc[n] != 0 && row0 + n * 16 + r < all_rows;
-    if (a.window > 0 && anc[n]) {
-      int own = __popcll(anc[n]);
-      for (; own > a.window; --own) anc[n] &= anc[n] - 1;  // the farthest ancestors
+    any |= !anc[n].none() && row0 + n * 16 + r < all_rows;
+    if (a.window > 0 && !anc[n].none()) {
+      int own = anc[n].count();
+      for (; own > a.window; --own) anc[n] = anc[n].without_first();  // the farthest ancestors
       low[n] = max(0, range.ctx - (a.window - own));
     }
 #pragma unroll
@@ -366,7 +384,7 @@ __global__ __launch_bounds__(RW* KW * 64, MIN) void attn_tree_kernel(TreeArgs a,
 #pragma unroll
       for (int e = 0; e < 8; ++e) {
         const int t = start + e / 4 * 16 + g * 4 + e % 4, drafted = t - range.ctx;
-        const uint32_t in_tree = (uint32_t)(anc[n] >> (drafted & 63)) & (drafted < 64 ? 1u : 0u);
+        const uint32_t in_tree = drafted < 64 ? anc[n].has(drafted) : 0u;
         const uint32_t in_context = t >= low[n] ? 1u : 0u;
         const uint32_t seen = (drafted < 0 ? in_context : in_tree) & ~(gone >> (e / 4));
         s.x[n][e / 4][e % 4] = seen & 1u ? s.x[n][e / 4][e % 4] : -INFINITY;
@@ -562,7 +580,7 @@ __global__ __launch_bounds__(RW* KW * 64, MIN) void attn_tree_kernel(TreeArgs a,
         bool sees[NR], one = false;
 #pragma unroll
         for (int n = 0; n < NR; ++n) {
-          sees[n] = anc[n] != 0 && (drafted < 0 ? start + x >= low[n] : (anc[n] >> drafted & 1) != 0);
+          sees[n] = !anc[n].none() && (drafted < 0 ? start + x >= low[n] : anc[n].has(drafted) != 0);
           one |= sees[n];
         }
         if (!__any(one)) continue;
@@ -588,7 +606,7 @@ __global__ __launch_bounds__(RW* KW * 64, MIN) void attn_tree_kernel(TreeArgs a,
 #pragma unroll
   for (int n = 0; n < NR; ++n) {
     l[n] = sum[n][0];
-    if (anc[n] == 0) {  // a padded node: the tiles of the context have no mask
+    if (anc[n].none()) {  // a padded node: the tiles of the context have no mask
       m[n] = kNone, l[n] = 0;
 #pragma unroll
       for (int i = 0; i < DIM / 16; ++i) o[n][i] = {0, 0, 0, 0};
@@ -808,7 +826,7 @@ hipError_t launch_dim(const TreeArgs& a, hipStream_t stream) {
   // Few rows: groups of waves that take tiles in turn.  More: waves that share a tile, two blocks of 16 rows to
   // each where the accumulators leave room (heads of 256: one).  What spills is not taken: two blocks to each of
   // four such groups took 191 us for 48 sequences, 30 rows, in bf16, two waves with one block in two groups 120
-  // (E4M3, heads of 128: 70 and 74, heads of 64: 46 and 44); heads of 256 have one wave on a SIMD there, 148 us
+  // (E4M3: 72 and 75, one sequence of 32768 29.7 and 27.1); heads of 256 have one wave on a SIMD there, 148 us
   // against 228 for 6 x 32768.
   if constexpr (DIM == 256) {
     e = rows == 16   ? launch_rows<DIM, FP8, 1, 1, 4, 1>(a, plan, stream)
@@ -816,9 +834,8 @@ hipError_t launch_dim(const TreeArgs& a, hipStream_t stream) {
         : rows == 64 ? launch_rows<DIM, FP8, 1, 4, 1, 2>(a, plan, stream)
                      : launch_rows<DIM, FP8, 1, 8, 1, 2>(a, plan, stream);
   } else {
-    constexpr bool kPairs = FP8 && DIM == 128;
     e = rows == 16   ? launch_rows<DIM, FP8, 1, 1, 4, 2>(a, plan, stream)
-        : rows == 32 ? launch_rows<DIM, FP8, kPairs ? 2 : 1, kPairs ? 1 : 2, kPairs ? 4 : 2, 2>(a, plan, stream)
+        : rows == 32 ? launch_rows<DIM, FP8, 1, 2, 2, 2>(a, plan, stream)
         : rows == 64 ? launch_rows<DIM, FP8, 1, 4, 1, 2>(a, plan, stream)
                      : launch_rows<DIM, FP8, 2, 4, 1, 2>(a, plan, stream);
   }
