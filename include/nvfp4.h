@@ -564,8 +564,9 @@ nvfp4_status nvfp4_attn_tree(const void* q_bf16, int64_t B, int32_t nodes, int32
  * logit of -inf is a probability of 0; a last row of nothing else gives the token -1.  +inf
  * and NaN never fault, what they give is unspecified.
  * Probabilities and their sums are binary64, so results are those of the definition but
- * where a uniform number lies within about 2^-40 of a border, at any temperature; they do
- * not depend on timing.
+ * where a uniform number lies within about 2^-40 of a border, at any temperature -- of the
+ * last token's after a drawn one was turned down, where the weights' total sum max(p_i - q_i, 0)
+ * is 1 no longer, within 2^-40 over that total.  They do not depend on timing.
  * workspace: nvfp4_verify_drafts_workspace_bytes (contents need no setup). */
 size_t nvfp4_verify_drafts_workspace_bytes(int64_t B, int32_t nodes, int64_t vocab, int32_t with_draft_logits);
 
