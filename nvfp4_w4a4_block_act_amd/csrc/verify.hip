@@ -524,13 +524,11 @@ __global__ __launch_bounds__(Draw<DRAWN>::kThreads) void verify_draw_kernel(Veri
     if (threadIdx.x == 0) {
       double sum = 0;
       for (int i = 0; i < Draw<DRAWN>::kRuns * Draw<DRAWN>::kWaves; ++i) sum += sums[i / Draw<DRAWN>::kWaves][i % Draw<DRAWN>::kWaves];
-      // The sums pass between workgroups as atomic values, which the cache of an XCD does not hold back, and the
-      // wait puts each before its count.  (Fences, which write back and drop whole caches, took 11 us of 39.)
+      // Each workgroup's sums come before its count, and all counts before the last one reads the sums.  (One thread's
+      // release and acquire: 54.4 us, as with the order left to the instructions' own waits.)
       __hip_atomic_store(&z.rest[(int64_t)b * z.chunks + chunk - z.groups], sum, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
-      asm volatile("s_waitcnt vmcnt(0)" ::: "memory");
       if (!more)
-        is_last = __hip_atomic_fetch_add(&z.done[b], 1u, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT) + 1 == (uint32_t)z.groups;
-      asm volatile("s_waitcnt vmcnt(0)" ::: "memory");
+        is_last = __hip_atomic_fetch_add(&z.done[b], 1u, __ATOMIC_ACQ_REL, __HIP_MEMORY_SCOPE_AGENT) + 1 == (uint32_t)z.groups;
     }
     __syncthreads();
     if (more) continue;
