@@ -697,11 +697,15 @@ __global__ __launch_bounds__(RW* KW * 64, MIN) void attn_tree_kernel(TreeArgs a,
 }
 
 // Joins the splits of the rows: each counts 2^(its m - the largest m), in a fixed order.  A row has DIM / 4 lanes
-// side by side, which take kJoin splits at a time, or, for few rows of many splits, kGroups such sets of lanes.
-// (With a workgroup of four sets for each row 48 sequences of 16 nodes and 40 heads in up to four splits took 24 us,
-// so 14.)
+// side by side, which take kJoin splits at a time, or, for fewer rows of more splits, 4 or 16 such sets of lanes.
+// Attention and join, us, with one set, four and sixteen (E4M3, heads of 128; *: bf16, 256):
+//   rows x splits   200 x 7   200 x 12   640 x 12   40 x 61   640 x 188   1000 x 61   768* x 61   1280 x 23   1920 x 47   2560 x 23
+//   one             14.8      15.8       21.2       28.8      150         55.1        89.8        43.0        74.0        51.6
+//   four            14.8      15.3       20.9       27.1      148         54.4        88.4        42.4        72.7        51.4
+//   sixteen         14.9      15.3       22.3       24.3      144         53.2        92.3        44.6        76.4        57.7
+// (and 48 sequences of 16 nodes and 40 heads in up to four splits, 30720 rows: 14 us of join with one, 24 with four).
 constexpr int kJoin = 8;
-constexpr int64_t kFewRows = 2048;
+constexpr int64_t kFewRows = 2048, kFewColumns = 1 << 17;
 
 template <int DIM, bool FP8>
 __device__ __forceinline__ void store_row(const TreeArgs& a, int64_t row, int d, float4_t x, float m, float sum) {
@@ -843,7 +847,7 @@ hipError_t launch_dim(const TreeArgs& a, hipStream_t stream) {
   const int64_t all = (int64_t)a.B * a.nodes * a.q_heads;
   if (plan.splits <= kJoin || all >= kFewRows)
     tree_join_kernel<DIM, FP8><<<dim3((unsigned)((all + 1024 / DIM - 1) / (1024 / DIM))), 256, 0, stream>>>(a, plan);
-  else if (plan.splits <= 16)
+  else if (plan.splits <= 16 || all * DIM > kFewColumns)
     tree_join_many_kernel<DIM, FP8, 4><<<dim3((unsigned)all), DIM, 0, stream>>>(a, plan);
   else
     tree_join_many_kernel<DIM, FP8, 16><<<dim3((unsigned)all), DIM * 4, 0, stream>>>(a, plan);

@@ -19,8 +19,8 @@ __host__ __device__ inline int64_t tree_span(int64_t ctx, int64_t nodes, int64_t
 }
 
 // rows: workgroups of one split.  About six workgroups for each CU, of which one or two run at once: 6 sequences of
-// up to 32768, 64 nodes, 6 heads of 256 on each of 4 (one at once), take 436 us, 459 with three, 475 with eight and 493
-// with nine; 48 of up to 4099, 16 nodes, 5 heads on each of 8 (two), 125, 129 with three, 128 with eight and 135 with twelve.
+// up to 32768, 64 nodes, 6 heads of 256 on each of 4 (one at once), take 444 us, 470 with three, 454 with four, 481
+// with eight and 530 with twelve; 48 of up to 4099, 16 nodes, 5 heads on each of 8 (two), 143, 153, 153, 145 and 150.
 inline Splits tree_splits(int64_t rows, int64_t max_len, int64_t nodes, int64_t window) {
   const int64_t span = tree_span(max_len, nodes, window);
   const int64_t want = std::max<int64_t>(1, (int64_t)kCUs * 6 / rows);

@@ -163,7 +163,8 @@ __global__ __launch_bounds__(kThreads) void verify_rows_kernel(VerifyArgs a, Siz
     }
   };
   // Where the launch does not fill the GPU the logits are on their way before it is known
-  // whether anybody asks for them.
+  // whether anybody asks for them: 14.2 us in all for 1 x 8 x 32000, otherwise 14.5, 14.8 and 15.0 for
+  // 2 x 8 x 100003; 18.9 and 18.7 for 8 x 8 x 100003, with 832 workgroups.
   const bool early = gridDim.x <= kCUs;
   if (early) load();
   if (a.draft && chunk == 0 && node == 0 && !is_draft && threadIdx.x == 0) z.done[b] = 0;

@@ -106,3 +106,12 @@ def test_joins_of_many_rows(dim, lens, kind, fp8):
     got = c.run()
     c.fp8 = False
     c.check(got)
+
+
+@pytest.mark.parametrize("W,heads,kv,dim,lens", [(64, 16, 2, 256, [9000]), (30, 32, 4, 128, [4300]), (12, 16, 2, 64, [20000]), (50, 8, 1, 256, [6000, 2500])])
+def test_joins_of_fewer_rows(W, heads, kv, dim, lens):
+    """Joins by four and by sixteen sets of lanes a row: up to 2047 rows of more than eight splits."""
+    c = Repeated(lens, W, heads, kv, dim, 64, False, seed=W, kind="tree")
+    say(f"[turns] joins {lens} {W * heads * len(lens)} rows of {dim} in {c.splits()} splits")
+    assert c.splits() > 8 and len(lens) * W * heads < 2048
+    c.check(c.run())
