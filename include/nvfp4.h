@@ -561,8 +561,9 @@ nvfp4_status nvfp4_attn_tree(const void* q_bf16, int64_t B, int32_t nodes, int32
  *   path       int32 [B][nodes]: node 0, the accepted nodes; -1 behind them.
  *   counts     int32 [B]: the nodes on the path, which is also the number of tokens.
  * A sequence whose node 0 is not a child of the context is padded: count 0, all -1.  A
- * logit of -inf is a probability of 0; a last row of nothing else gives the token -1.  +inf
- * and NaN never fault, what they give is unspecified.
+ * logit of -inf is a probability of 0, and so is one below about 2^-900 of its row's largest; a
+ * last row of nothing but -inf gives the token -1.  +inf and NaN never fault, what they
+ * give is unspecified.
  * Probabilities and their sums are binary64, so results are those of the definition but
  * where a uniform number lies within about 2^-40 of a border, at any temperature -- of the
  * last token's after a drawn one was turned down, where the weights' total sum max(p_i - q_i, 0)

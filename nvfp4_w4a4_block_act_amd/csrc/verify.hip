@@ -101,6 +101,12 @@ struct Scale {
 };
 __device__ __forceinline__ Scale scale_of(double heat, float m, const double* table) { return {heat, (double)m, table}; }
 
+// A weight below kLeast is none, and so is a chunk's sum below kLeastSum (one above it has a weight above kLeast): of
+// -inf exp2_below leaves 2^-1000, of a chunk in which only turned-down tokens have a logit 2^-987, and a number of 0
+// must find neither.
+constexpr double kLeastSum = 0x1p-900, kLeast = kLeastSum / (2 * kChunk);
+__device__ __forceinline__ double weight_or_none(double w) { return w > kLeast ? w : 0.0; }
+
 // log2(e) / temperature; 0: greedy
 __device__ __forceinline__ double heat_of(const VerifyArgs& a, int b) {
   const float t = a.temperature ? a.temperature[b] : 0.0f;
@@ -179,7 +185,7 @@ __global__ __launch_bounds__(kThreads) void verify_rows_kernel(VerifyArgs a, Siz
   float m = -INFINITY;
 #pragma unroll
   for (int e = 0; e < kEach; ++e) m = fmaxf(m, x[e]);
-  float mine = m;
+  const float mine = m;
   __shared__ float ms[kThreads / 64];
   __shared__ int found;  // where the largest is
   __shared__ double table[kSteps];
@@ -204,21 +210,15 @@ __global__ __launch_bounds__(kThreads) void verify_rows_kernel(VerifyArgs a, Siz
       for (; kids; kids &= kids - 1) {
         const int64_t t = __shfl(token, __builtin_ctzll(kids)) - first;
         if (t < 0 || t >= count || (t / 4) % kThreads != threadIdx.x) continue;
-        const int at = (int)(t / 4 / kThreads * 4 + t % 4);
-        mine = -INFINITY;
+        const int mine = (int)(t / 4 / kThreads * 4 + t % 4);
 #pragma unroll
-        for (int e = 0; e < kEach; ++e) {
-          if (e == at) x[e] = -INFINITY;
-          mine = fmaxf(mine, x[e]);
-        }
+        for (int e = 0; e < kEach; ++e)
+          if (e == mine) x[e] = -INFINITY;
       }
     }
     const Scale scale = scale_of(heat_of(a, b), m > -INFINITY ? m : 0.0f, table);
 #pragma unroll
     for (int e = 0; e < kEach; ++e) sum += scale.of(x[e]);
-    // A weight of -inf is 2^-1000 here: nothing beside another weight, but a chunk that has only such ones has
-    // none (the draw looks for a token in every chunk whose sum is above 0).
-    if (!(mine > -INFINITY)) sum = 0;
     __shared__ double sums[kThreads / 64];
     sum = block_sum(sum, sums);
   } else {
@@ -324,7 +324,7 @@ __device__ __forceinline__ void walk_tree(const VerifyArgs& a, const Sizes& z, i
     double mine[2] = {0, 0};
 #pragma unroll
     for (int d = 0; d < (DRAWN ? 2 : 1); ++d)
-      if (l[d] > -INFINITY) mine[d] = scale_of(heat, w.m[d][parent], w.table).of(l[d]);
+      if (l[d] > -INFINITY) mine[d] = weight_or_none(scale_of(heat, w.m[d][parent], w.table).of(l[d]));
     bool again = false;  // an earlier child of the same parent has the same token
     if (!DRAWN)
 #pragma unroll 4
@@ -413,15 +413,12 @@ __device__ __forceinline__ void weights_of(const VerifyArgs& a, const Last& last
     y[k] = DRAWN && last.l2 ? load4(last.l2 + first, (k * Draw<DRAWN>::kThreads + threadIdx.x) * 4, count) : x[k];
   }
 #pragma unroll
-  for (int e = 0; e < Draw<DRAWN>::kEach; ++e) {
-    const float l = x[e / 4][e % 4];
-    r.w[e] = l > -INFINITY ? last.p.of(l) : 0.0;
-  }
+  for (int e = 0; e < Draw<DRAWN>::kEach; ++e) r.w[e] = weight_or_none(last.p.of(x[e / 4][e % 4]));
   if (DRAWN && last.l2) {
 #pragma unroll
     for (int e = 0; e < Draw<DRAWN>::kEach; ++e) {
       const float l = y[e / 4][e % 4];
-      r.w[e] = fmax(r.w[e] * last.per - (l > -INFINITY ? last.q.of(l) * last.per2 : 0.0), 0.0);
+      r.w[e] = fmax(r.w[e] * last.per - weight_or_none(last.q.of(l)) * last.per2, 0.0);
     }
   }
 }
@@ -480,7 +477,9 @@ __global__ __launch_bounds__(Draw<DRAWN>::kThreads) void verify_draw_kernel(Veri
       // The chunk, found by every wave alike: a run of chunks to each lane.
       const int each = (z.chunks + 63) / 64, c0 = lane * each, c1 = min(c0 + each, z.chunks);
       auto chunk_sum = [&](int c) {
-        return DRAWN && last.l2 ? __hip_atomic_load(&rests[c], __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT) : (parts[c].m > -INFINITY ? parts[c].sum * last.p.of(parts[c].m) : 0.0);
+        if (DRAWN && last.l2) return __hip_atomic_load(&rests[c], __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+        const double s = parts[c].m > -INFINITY ? parts[c].sum * last.p.of(parts[c].m) : 0.0;
+        return s > kLeastSum ? s : 0.0;
       };
       double sum = 0;
 #pragma unroll 1

@@ -5,6 +5,7 @@ import numpy as np
 import pytest
 
 from gpu_util import say
+from oracle import drafts as O
 from test_verify_gpu import _case, _check, _run
 
 pytestmark = pytest.mark.gpu
@@ -57,3 +58,21 @@ def test_large_logits_at_ordinary_temperatures():
     c = _case(24, 4, 9001, seed=33, kind="chain")
     c["logits"] = (np.float32(2.0 ** 20) * np.repeat([1, -1, 3], 8)[:, None, None].astype(np.float32) + np.round(8 * c["logits"]) / 8).astype(np.float32)
     _check(c, _run(c))
+
+
+@pytest.mark.parametrize("sampled", [False, True])
+def test_numbers_of_0_near_temperature_0(sampled):
+    """0 takes the first token that has a weight: near temperature 0 the largest logits have all of it."""
+    say(f"[cold] zeros {sampled}")
+    c = _cold(_case(3 * len(COLD), 4, 20001, seed=34, kind="chain", sampled=sampled))
+    c["temperature"] = np.minimum(c["temperature"], np.float32(1e-10))
+    c["uniforms"][:, 3:] = 0
+    c["uniforms"][::2] = 0
+    if sampled:
+        for i in range(3):
+            c["drafts"][:, i + 1] = c["draft_logits"][:, i].argmax(-1)
+    tokens, path, counts = _run(c)
+    for b in range(len(counts)):                    # (a number of 0 and a weight of 0 lie on the border, and on its one side)
+        t, p, _ = O.verify(c["logits"][b], c["drafts"][b], None, c["temperature"][b], c["uniforms"][b],
+                           c["draft_logits"][b] if sampled else None)
+        assert counts[b] == len(p) and list(path[b, :len(p)]) == p and list(tokens[b, :len(t)]) == t, (b, tokens[b], t)
