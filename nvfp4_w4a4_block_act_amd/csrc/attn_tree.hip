@@ -26,7 +26,7 @@
 // doubling; only tiles that hold drafted tokens, or the edge of a window, or a page outside
 // the pool, look at it.  In these tiles values that are no finite number are taken as 0, so
 // that a node's row that holds one does not reach the rows that do not see it; where any
-// was, the rows that do see it get it at the end (the check for that takes 0.3 us of 14, 1 of 126).
+// was, the rows that do see it get it at the end (the check for that takes 0.3 us of 15, 1 of 141).
 //
 // Bound by memory for few rows, by each wave's chain of steps in a tile for many: 48 sequences of up to 4099
 // (E4M3, 5 heads on each of 8, 250 MB) take 55 us with 3 nodes (4.3 TB/s), 75 with 6, 107 with 12 and 141 with
@@ -77,7 +77,7 @@ struct Shape {
   // Where 16-byte piece `piece` of a row lies in LDS.  An access of 16 bytes a lane is served 16 lanes at a
   // time, of which 8 come from one run of 16 lanes and 8 from the next: here the 16 rows (keys) or pieces
   // (values) of such a set, from two neighbouring g, always fall on different banks, and so do the two rows
-  // that E4M3 lanes write side by side.  (Counted: conflicts take none of the time over bf16, 8 % over E4M3; with rows
+  // that E4M3 lanes write side by side.  (Counted: conflicts take none of the time over bf16, 6 % over E4M3; with rows
   // padded by 16 bytes instead 17 to 19 %.)
   static __device__ __forceinline__ int key_spot(int row, int piece) {
     return row * kLdsRow + (piece ^ (DIM == 64 ? row / 2 % 8 : row % 16)) * 16;

@@ -22,10 +22,10 @@
 // Every sum has a fixed order: results do not depend on timing.
 //
 // verify_rows is bound by the vector units, and by memory little behind them: 64 x 24 rows of 131072 logits
-// (740 MB without those of padded nodes) take 136 us, 5.4 TB/s, with 83 % of the vector units' time in use; 2 x 174
-// rows of 100003 (128 MB without draft rows that no child follows) 30.
-// verify_draw is bound by its chain of loads, sums and exchanges: 8.4 us for one sequence, 13.6 for 64,
-// and 22.6 for 29 of which each sums the residuals of 100003 logits.
+// (740 MB without those of padded nodes) take 140 us, 5.3 TB/s, with 84 % of the vector units' time in use; 2 x 174
+// rows of 100003 (128 MB without draft rows that no child follows) 31.
+// verify_draw is bound by its chain of loads, sums and exchanges: 8.3 us for one sequence, 13.3 for 64,
+// and 23.0 for 29 of which each sums the residuals of 100003 logits.
 #include <algorithm>
 
 #include "common.hpp"
