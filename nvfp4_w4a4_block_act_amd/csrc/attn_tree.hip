@@ -26,7 +26,8 @@
 // doubling; only tiles that hold drafted tokens, or the edge of a window, or a page outside
 // the pool, look at it.  In these tiles values that are no finite number are taken as 0, so
 // that a node's row that holds one does not reach the rows that do not see it; where any
-// was, the rows that do see it get it at the end (the check for that takes 0.3 us of 15, 1 of 141).
+// was, the rows that do see it get it at the end (the check for that takes 0.6 us of 15, 3 of 143; a call in which
+// each sequence has one up to 1.8 times as long -- of padded nodes' rows, which may hold anything, it asks nothing).
 //
 // Bound by memory for few rows, by each wave's chain of steps in a tile for many: 48 sequences of up to 4099
 // (E4M3, 5 heads on each of 8, 250 MB) take 55 us with 3 nodes (4.3 TB/s), 75 with 6, 107 with 12 and 141 with
@@ -203,6 +204,8 @@ __global__ __launch_bounds__(RW* KW * 64, MIN) void attn_tree_kernel(TreeArgs a,
   if (split > 0 && from >= end) return;
 
   const Nodes anc_lane = ancestors(a.nodes, lane, parent);
+  const uint64_t somebody = __ballot(!anc_lane.none());
+  const Nodes alive = {(uint32_t)somebody, (uint32_t)(somebody >> 32)};  // nodes that are not padded: their rows are in the cache
   const float scale = a.scale * (FP8 ? *c.k_amax / 448.0f : 1.0f) * kLog2e;
   // scores of the sign that makes the factor positive, so that the largest is the largest score
   const uint32_t flip = scale < 0.0f ? 0x80008000u : 0u;
@@ -315,7 +318,7 @@ __global__ __launch_bounds__(RW* KW * 64, MIN) void attn_tree_kernel(TreeArgs a,
       }
     }
   };
-  uint32_t dropped = 0;  // bits of values of this lane that `put_values` took for 0 in rows of the sequence
+  uint32_t dropped = 0;  // bits of values of this lane that `put_values` took for 0 in rows that somebody sees
   auto put_values = [&](const Held& h, int turn, bool masked, uint8_t* lds) {
 #pragma unroll
     for (int i = 0; i < kLoads; ++i) {
@@ -336,7 +339,7 @@ __global__ __launch_bounds__(RW* KW * 64, MIN) void attn_tree_kernel(TreeArgs a,
           gone |= w[x] ^ kept;
           w[x] = kept;
         }
-        dropped |= token < end ? gone : 0;
+        dropped |= token < range.ctx || (token < end && alive.has(token - range.ctx)) ? gone : 0;
       }
       *reinterpret_cast<uint4*>(lds + value_spot[i]) = make_uint4(w[0], w[1], w[2], w[3]);
       if constexpr (FP8) *reinterpret_cast<uint4*>(lds + (value_spot[i] ^ 16)) = make_uint4(w[4], w[5], w[6], w[7]);

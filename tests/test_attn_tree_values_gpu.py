@@ -103,3 +103,23 @@ def test_values_that_nobody_sees(fp8):
     got = c.run(window=20)
     torch.cuda.synchronize()
     c.check(got, window=20)
+
+
+@pytest.mark.parametrize("fp8", [False, True])
+@pytest.mark.parametrize("W,heads,dim", [(9, 4, 128), (20, 8, 128), (40, 8, 64), (30, 6, 256)])
+def test_values_among_those_of_padded_nodes(W, heads, dim, fp8):
+    """Padded nodes' rows that hold no numbers (as they all do here) beside nodes' rows of which one does."""
+    say(f"[values] padded W={W} {heads}x{dim} fp8={fp8}")
+    c = Case([100, 61, 333], W, heads, 2, dim, 16, fp8, seed=W, kind="chain")
+    c.parents = np.tile(np.arange(-1, W - 1, dtype=np.int32), (3, 1))
+    c.parents[:, W // 2 + 1:] = -2
+    c.dev_parents = torch.from_numpy(c.parents).to(DEV)
+    for b in range(3):
+        for row in range(int(c.lens[b]) + W // 2 + 1, int(c.lens[b]) + W):
+            at = int(c.table[b, row // 16]), row % 16
+            for t in (c.cache.k, c.cache.v):
+                t[at] = 0x7F if fp8 else float("nan")
+    got = c.run()
+    torch.cuda.synchronize()
+    c.check(got)
+    check(c, plant(c, [(0, 100 + W // 2), (2, 333)], W))
