@@ -32,9 +32,10 @@
 // Bound by memory for few rows, by each wave's chain of steps in a tile for many: 48 sequences of up to 4099
 // (E4M3, 5 heads on each of 8, 250 MB) take 55 us with 3 nodes (4.3 TB/s), 75 with 6, 107 with 12 and 141 with
 // 16 (80 rows in 128; the fourth wave, which has no rows, may as well idle: no change; 14 us of
-// it the join).  6 of up to 32768 (bf16, 64 nodes, 6 heads of 256 on each of 4) take 435 us: 478 TFLOP/s
-// of the products, 717 of the matrix instructions, 58 % of a large matrix product's rate, with LDS
-// busy half of the time: a wave has room for 16 rows' sums, and every 16 rows read the whole tile.
+// it the join), in bf16 107 with 3 (4.3 TB/s) and 121 with 6.  6 of up to 32768 (bf16, 64 nodes, 6 heads of
+// 256 on each of 4) take 435 us: 478 TFLOP/s of the products, 717 of the matrix instructions, 58 % of a large
+// matrix product's rate, with LDS busy half of the time: a wave has room for 16 rows' sums, and every 16 rows
+// read the whole tile.
 // Four waves of 32 rows, one on a SIMD, took 637 us, without the overlap 488, where this took 455.
 #include <algorithm>
 
